@@ -10,7 +10,11 @@ from .binding import (  # noqa: F401
     MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_OK, MOE_SCALE_E8M0,
     MOE_SCALE_FP32, MOE_SCALE_FP32_RECIPROCAL, MOE_SCALES_NONE, MOE_SCALES_PER_EXPERT,
     MOE_SCALES_SCALAR, MOE_SCALES_SHARED, MOE_TOKEN_BF16, MOE_TOKEN_F16, Launch, MoeDcConfig, MoeDcError,
-    alloc_dispatch_outputs, token_torch_dtype,
+    MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_MM_SCALE_MX, MOE_MM_SCALE_NONE, MOE_MM_SCALE_ROW,
+    MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W4_E2M1, MOE_W4_INT4, MoeGate, MoeMatmul,
+    alloc_dispatch_outputs, gate_topk, grouped_matmul, grouped_matmul_w4, make_gate, make_matmul,
+    moe_gate_topk, moe_grouped_matmul, moe_grouped_matmul_w4, prepare_gate_topk,
+    prepare_grouped_matmul, prepare_grouped_matmul_w4, token_torch_dtype,
     code_row_elems, code_type, combine, combine_block_count, combine_int8, combine_quantize,
     combine_scatter, dispatch, load_library, make_config, moe_combine, moe_combine_int8,
     moe_combine_quantize, moe_combine_scatter, moe_dc_combine_scatter_workspace_bytes,

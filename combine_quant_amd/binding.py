@@ -21,6 +21,10 @@ MOE_SCALES_NONE, MOE_SCALES_SCALAR, MOE_SCALES_SHARED, MOE_SCALES_PER_EXPERT = 0
 MOE_SCALE_FP32, MOE_SCALE_E8M0, MOE_SCALE_FP32_RECIPROCAL = 0, 1, 2
 MOE_DC_FLAG_SEPARATE_ROUTE, MOE_DC_FLAG_CHECK_IDS = 1, 2
 MOE_TOKEN_BF16, MOE_TOKEN_F16 = 0, 1
+MOE_MM_SCALE_NONE, MOE_MM_SCALE_ROW, MOE_MM_SCALE_MX = 0, 1, 2
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
+MOE_W4_INT4, MOE_W4_E2M1 = 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 _STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
            -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_DEVICE"}
 
@@ -28,6 +32,7 @@ EXPORTS = ("moe_dc_validate", "moe_dc_scales_per_row", "moe_dc_dispatch_workspac
            "moe_dc_combine_scatter_workspace_bytes", "moe_dispatch",
            "moe_dispatch_no_workspace", "moe_combine",
            "moe_combine_scatter", "moe_combine_quantize", "moe_combine_int8",
+           "moe_gate_topk", "moe_grouped_matmul", "moe_grouped_matmul_w4",
            "moe_dc_last_error", "moe_dc_version")
 
 
@@ -64,6 +69,32 @@ class MoeDcConfig(ctypes.Structure):
     @property
     def L(self):
         return self.moe_expert_num // self.ep_world_size
+
+
+class MoeMatmul(ctypes.Structure):
+    """Mirror of moe_matmul."""
+    _fields_ = [
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("group_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class MoeGate(ctypes.Structure):
+    """Mirror of moe_gate."""
+    _fields_ = [
+        ("score", ctypes.c_int32),
+        ("group_count", ctypes.c_int32),
+        ("group_keep", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("factor", ctypes.c_float),
+    ]
 
 
 class MoeDcError(RuntimeError):
@@ -104,6 +135,13 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     lib.moe_combine_quantize.argtypes = [cfgp] + [P] * 4 + [P]
     lib.moe_combine_int8.restype = ctypes.c_int
     lib.moe_combine_int8.argtypes = [cfgp] + [P] * 10 + [P]
+    mmp, gatep = ctypes.POINTER(MoeMatmul), ctypes.POINTER(MoeGate)
+    lib.moe_grouped_matmul.restype = ctypes.c_int
+    lib.moe_grouped_matmul.argtypes = [cfgp, mmp] + [P] * 7 + [P]
+    lib.moe_grouped_matmul_w4.restype = ctypes.c_int
+    lib.moe_grouped_matmul_w4.argtypes = [cfgp, mmp] + [P] * 6 + [P]
+    lib.moe_gate_topk.restype = ctypes.c_int
+    lib.moe_gate_topk.argtypes = [cfgp, gatep] + [P] * 4 + [P]
     lib.moe_dc_last_error.restype = ctypes.c_char_p
     lib.moe_dc_last_error.argtypes = []
     lib.moe_dc_version.restype = ctypes.c_char_p
@@ -120,6 +158,18 @@ def make_config(W, E, BS, H, K, quant_mode=0, zero_expert_num=0, copy_expert_num
     return MoeDcConfig(W, E, BS, H, K, quant_mode, zero_expert_num, copy_expert_num,
                        const_expert_num, expert_token_nums_type, mask_kind, out_dtype,
                        scales_kind, scale_format, flags, token_dtype, cap)
+
+
+def make_matmul(in_features, out_features, x_dtype=MOE_DTYPE_DEFAULT,
+                scaling=MOE_MM_SCALE_NONE, activation=MOE_ACT_NONE, weight_dtype=0,
+                group_size=0):
+    return MoeMatmul(in_features, out_features, x_dtype, scaling, activation, weight_dtype,
+                     group_size, 0)
+
+
+def make_gate(score=MOE_SCORE_SOFTMAX, group_count=1, group_keep=1, group_top=1,
+              renormalize=False, factor=1.0):
+    return MoeGate(score, group_count, group_keep, group_top, int(renormalize), factor)
 
 
 def token_torch_dtype(cfg):
@@ -410,6 +460,90 @@ def moe_combine_int8(cfg, codes, block_scales, expert_ids, expand_idx, expert_sc
                                 ep_recv_count, recv_offsets, x_active_mask, ori_x, y), stream)
 
 
+# -- the router and the experts' products -----------------------------------------------------
+
+_ROW_DTYPES = {MOE_DTYPE_INT8: torch.int8, MOE_DTYPE_E4M3: (torch.uint8, torch.float8_e4m3fn),
+               MOE_DTYPE_E5M2: (torch.uint8, torch.float8_e5m2)}
+
+
+def _out_columns(mm):
+    return mm.out_features // 2 if mm.activation == MOE_ACT_SWIGLU else mm.out_features
+
+
+def _routed_rows(cfg, ep_recv_count, recv_offsets, dev):
+    return [_ptr(ep_recv_count, torch.int32, (cfg.ep_world_size, cfg.L * cfg.ep_world_size),
+                 "ep_recv_count", dev),
+            _ptr(recv_offsets, torch.int64, (cfg.ep_world_size + 1,), "recv_offsets", dev)]
+
+
+def _grouped_matmul_call(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales,
+                         weight_scales, out):
+    E, cap, I, N = cfg.moe_expert_num, cfg.expand_rows_capacity, mm.in_features, mm.out_features
+    dev, token = out.device, token_torch_dtype(cfg)
+    tokens = mm.x_dtype == MOE_DTYPE_DEFAULT
+    wtype = token if tokens else _ROW_DTYPES.get(
+        MOE_DTYPE_E4M3 if mm.x_dtype == MOE_DTYPE_E5M2 else mm.x_dtype)
+    sdt, xshape, wshape = torch.float32, (cap,), (E, N)
+    if mm.scaling == MOE_MM_SCALE_MX:
+        sdt, xshape, wshape = torch.uint8, (cap, I // 32), (E, N, I // 32)
+    args = [
+        _ptr(x, token if tokens else _ROW_DTYPES.get(mm.x_dtype), (cap, I), "x", dev),
+        _ptr(x_scales, sdt, xshape, "x_scales", dev),
+        _ptr(weight, wtype, (E, N, I), "weight", dev),
+        _ptr(weight_scales, sdt, wshape, "weight_scales", dev),
+        *_routed_rows(cfg, ep_recv_count, recv_offsets, dev),
+        _ptr(out, token, (cap, _out_columns(mm)), "out", dev),
+    ]
+    return load_library().moe_grouped_matmul, (ctypes.byref(cfg), ctypes.byref(mm), *args), dev
+
+
+def moe_grouped_matmul(cfg, mm, x, x_scales, weight, weight_scales, ep_recv_count, recv_offsets,
+                       out, stream=None):
+    """Enqueue one product of the packed rows with their experts' weights on `stream`."""
+    _launch(*_grouped_matmul_call(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales,
+                                  weight_scales, out), stream)
+
+
+def _grouped_matmul_w4_call(cfg, mm, x, weight, weight_scales, ep_recv_count, recv_offsets, out):
+    E, cap, I, N = cfg.moe_expert_num, cfg.expand_rows_capacity, mm.in_features, mm.out_features
+    dev, token = out.device, token_torch_dtype(cfg)
+    sdt = torch.uint8 if mm.weight_dtype == MOE_W4_E2M1 else token
+    args = [
+        _ptr(x, token, (cap, I), "x", dev),
+        _ptr(weight, torch.uint8, (E, N, I // 2), "weight", dev),
+        _ptr(weight_scales, sdt, (E, N, I // max(1, mm.group_size)), "weight_scales", dev),
+        *_routed_rows(cfg, ep_recv_count, recv_offsets, dev),
+        _ptr(out, token, (cap, _out_columns(mm)), "out", dev),
+    ]
+    return (load_library().moe_grouped_matmul_w4, (ctypes.byref(cfg), ctypes.byref(mm), *args),
+            dev)
+
+
+def moe_grouped_matmul_w4(cfg, mm, x, weight, weight_scales, ep_recv_count, recv_offsets, out,
+                          stream=None):
+    """Enqueue one product of the packed token rows with 4-bit expert weights on `stream`."""
+    _launch(*_grouped_matmul_w4_call(cfg, mm, x, weight, weight_scales, ep_recv_count,
+                                     recv_offsets, out), stream)
+
+
+def _gate_topk_call(cfg, gate, logits, bias, expert_ids, expert_scales):
+    W, BS, K = cfg.ep_world_size, cfg.bs, cfg.topk
+    n = cfg.moe_expert_num + cfg.zero_expert_num + cfg.copy_expert_num
+    dev = logits.device
+    args = [
+        _ptr(logits, torch.float32, (W, BS, n), "logits", dev),
+        _ptr(bias, torch.float32, (n,), "bias", dev),
+        _ptr(expert_ids, torch.int32, (W, BS, K), "expert_ids", dev),
+        _ptr(expert_scales, torch.float32, (W, BS, K), "expert_scales", dev),
+    ]
+    return load_library().moe_gate_topk, (ctypes.byref(cfg), ctypes.byref(gate), *args), dev
+
+
+def moe_gate_topk(cfg, gate, logits, bias, expert_ids, expert_scales, stream=None):
+    """Enqueue the router on `stream`: the K best ids of every token and their weights."""
+    _launch(*_gate_topk_call(cfg, gate, logits, bias, expert_ids, expert_scales), stream)
+
+
 # -- allocation helpers (torch owns the memory; the library never allocates) ----------------
 
 def alloc_dispatch_outputs(cfg, device="cuda"):
@@ -557,3 +691,64 @@ def combine_int8(cfg, codes, block_scales, expert_ids, expand_idx, expert_scales
                                      x_active_mask, ori_x, y)
     launch(stream)
     return y
+
+
+def prepare_grouped_matmul(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales=None,
+                           weight_scales=None, out=None):
+    """Plan for moe_grouped_matmul: (launch, out)."""
+    if out is None:
+        out = torch.empty((cfg.expand_rows_capacity, _out_columns(mm)),
+                          dtype=token_torch_dtype(cfg), device=x.device)
+    fn, args, dev = _grouped_matmul_call(cfg, mm, x, weight, ep_recv_count, recv_offsets,
+                                         x_scales, weight_scales, out)
+    keep = (cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales, weight_scales, out)
+    return Launch(fn, args, dev, keep), out
+
+
+def grouped_matmul(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales=None,
+                   weight_scales=None, out=None, stream=None):
+    """Allocate (or reuse `out`) and enqueue moe_grouped_matmul; returns out ([cap][N], or
+    [cap][N/2] with SwiGLU; rows at or past recv_offsets[W] are not written)."""
+    launch, out = prepare_grouped_matmul(cfg, mm, x, weight, ep_recv_count, recv_offsets,
+                                         x_scales, weight_scales, out)
+    launch(stream)
+    return out
+
+
+def prepare_grouped_matmul_w4(cfg, mm, x, weight, weight_scales, ep_recv_count, recv_offsets,
+                              out=None):
+    """Plan for moe_grouped_matmul_w4: (launch, out)."""
+    if out is None:
+        out = torch.empty((cfg.expand_rows_capacity, _out_columns(mm)),
+                          dtype=token_torch_dtype(cfg), device=x.device)
+    fn, args, dev = _grouped_matmul_w4_call(cfg, mm, x, weight, weight_scales, ep_recv_count,
+                                            recv_offsets, out)
+    keep = (cfg, mm, x, weight, weight_scales, ep_recv_count, recv_offsets, out)
+    return Launch(fn, args, dev, keep), out
+
+
+def grouped_matmul_w4(cfg, mm, x, weight, weight_scales, ep_recv_count, recv_offsets, out=None,
+                      stream=None):
+    """Allocate (or reuse `out`) and enqueue moe_grouped_matmul_w4; returns out."""
+    launch, out = prepare_grouped_matmul_w4(cfg, mm, x, weight, weight_scales, ep_recv_count,
+                                            recv_offsets, out)
+    launch(stream)
+    return out
+
+
+def prepare_gate_topk(cfg, gate, logits, bias=None, out=None):
+    """Plan for moe_gate_topk: (launch, (expert_ids, expert_scales))."""
+    if out is None:
+        shape = (cfg.ep_world_size, cfg.bs, cfg.topk)
+        out = (torch.empty(shape, dtype=torch.int32, device=logits.device),
+               torch.empty(shape, dtype=torch.float32, device=logits.device))
+    fn, args, dev = _gate_topk_call(cfg, gate, logits, bias, out[0], out[1])
+    return Launch(fn, args, dev, (cfg, gate, logits, bias, out)), out
+
+
+def gate_topk(cfg, gate, logits, bias=None, out=None, stream=None):
+    """Allocate (or reuse `out`) and enqueue moe_gate_topk; returns (expert_ids, expert_scales)
+    as dispatch and combine take them."""
+    launch, out = prepare_gate_topk(cfg, gate, logits, bias, out)
+    launch(stream)
+    return out

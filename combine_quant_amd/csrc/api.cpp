@@ -157,6 +157,10 @@ moe_status moe_dc::set_error(moe_status st, const char* msg)
     return fail(st, "%s", msg);
 }
 
+moe_status moe_dc::set_ok() { return ok(); }
+
+moe_status moe_dc::check_config(const moe_dc_config* cfg, Shape* out) { return check(cfg, out); }
+
 moe_status moe_dc::check_dispatch_args(const moe_dc_config* cfg, const void* x,
                                        const int32_t* expert_ids, const float* scales,
                                        const uint8_t* x_active_mask, const float* expert_scales,

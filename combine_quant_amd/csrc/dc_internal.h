@@ -12,7 +12,13 @@ namespace moe_dc {
 // Records `msg` as the calling thread's moe_dc_last_error() text and returns `st`.
 moe_status set_error(moe_status st, const char* msg);
 
+// Clears that text and returns MOE_OK.
+moe_status set_ok();
+
 struct Shape;
+
+// The config's rules alone (moe_dc_validate); fills *out (if not null) on success.
+moe_status check_config(const moe_dc_config* cfg, Shape* out);
 
 // Every host-side rule of moe_dispatch except those on the workspace: the config, the
 // required pointers and the pairings of optional ones.  Fills *out (if not null) on success.

@@ -1,0 +1,263 @@
+// grouped_matmul_w4.hip -- products of the packed token rows with 4-bit expert weights.
+//
+// A workgroup takes NT * 16 weight rows of one expert; its four waves take chunks of 128
+// elements (64 bytes of codes) in turn, straight from global memory.  Lane l loads, of weight row
+// l % 16, the 16 bytes that hold elements (l / 16) * 32 + 0..31 of the chunk; a 4 x 4 exchange
+// of dwords between the four lane groups then leaves in dword j the lane's eight elements of
+// 32-element step j, the operand layout of the 16x16x32 instructions.
+//
+// Codes become 16-bit floats exactly.  int4 for bf16 rows: the four bits under an exponent of 2^7
+// are 136 + code, and the surplus 136 * sum(x) leaves through the accumulator's start value, a
+// product with constant -136 shared by all weight tiles; for fp16 rows 1032 + code, minus
+// 1032 by a packed subtraction.  E2M1 by the conversion instruction.  x is the A operand
+// (rows of the result), the weights B (columns), so that one lane holds one weight row's results
+// and one scale: each group's sum is formed by itself in fp32, scaled and added in fp32.
+#include "experts_device.h"
+
+namespace moe_dc {
+namespace {
+
+typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kW4Waves = 4;
+constexpr int kW4MaxZ = 8;
+
+// 4 x 4 transpose of dwords over the lane groups l / 16.
+__device__ __forceinline__ v4i_t exchange(v4i_t v)
+{
+    const u2_t p = __builtin_amdgcn_permlane32_swap((uint32_t)v.x, (uint32_t)v.z, false, false);
+    const u2_t q = __builtin_amdgcn_permlane32_swap((uint32_t)v.y, (uint32_t)v.w, false, false);
+    const u2_t r = __builtin_amdgcn_permlane16_swap(p.x, q.x, false, false);
+    const u2_t t = __builtin_amdgcn_permlane16_swap(p.y, q.y, false, false);
+    return v4i_t{(int)r.x, (int)r.y, (int)t.x, (int)t.y};
+}
+
+// Eight codes of a dword as 16-bit floats.  int4: in the order 0 4 1 5 2 6 3 7 (see pair_order);
+// for bf16 each is 136 + code.
+template <bool F16, bool E2M1>
+__device__ __forceinline__ v4i_t decode(uint32_t w)
+{
+    v4i_t r;
+    if constexpr (E2M1) {
+        if constexpr (F16) {
+            r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+            r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+            r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+            r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+        } else {
+            r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
+            r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
+            r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
+            r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
+        }
+    } else {
+        constexpr uint32_t magic = F16 ? 0x64086408u : 0x43084308u;   // the XOR makes code + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) ^ magic;
+            if constexpr (F16) {
+                const h2_t off = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+                u = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2_t, u) + off);
+            }
+            r[i] = (int)u;
+        }
+    }
+    return r;
+}
+
+// Eight 16-bit elements 0..7 in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ v4i_t pair_order(v4i_t x)
+{
+    v4i_t r;
+    r.x = (int)__builtin_amdgcn_perm((uint32_t)x.z, (uint32_t)x.x, 0x05040100u);
+    r.y = (int)__builtin_amdgcn_perm((uint32_t)x.z, (uint32_t)x.x, 0x07060302u);
+    r.z = (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.y, 0x05040100u);
+    r.w = (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.y, 0x07060302u);
+    return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ v4f_t mma16(v4i_t a, v4i_t b, v4f_t c)
+{
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h_t, a),
+                                                      __builtin_bit_cast(v8h_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_t, a),
+                                                       __builtin_bit_cast(v8bf_t, b), c, 0, 0, 0);
+}
+
+// STEPS: 32-element steps per scale (1, 2 or 4).
+template <bool F16, bool E2M1, int STEPS, int MT, int NT>
+__device__ __forceinline__ void w4_tile(const MatmulShape& s, const MatmulArgs& a, int e, int n0,
+                                        int row0, int rows, float* lds)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = threadIdx.x / kWave;
+    const int l16 = lane & 15, g = lane >> 4;
+    const uint32_t xrow = (uint32_t)s.in * 2, wrow = (uint32_t)s.in / 2;
+    const int chunks = (s.in + 127) / 128;
+    const int half = s.swiglu ? s.out / 2 : s.out;
+    const int per = s.swiglu ? NT / 2 * 16 : NT * 16;
+    const int left = half - n0 < per ? half - n0 : per;
+    const int mrows = rows < MT * 16 ? rows : MT * 16;
+    const char* wbase = static_cast<const char*>(a.w) + ((size_t)e * s.out + n0) * wrow;
+    const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(wbase, (uint32_t)left * wrow);
+    const __amdgpu_buffer_rsrc_t wr1 =
+        make_rsrc(wbase + (size_t)half * wrow, (uint32_t)left * wrow);
+    const __amdgpu_buffer_rsrc_t xr =
+        make_rsrc(static_cast<const char*>(a.x) + (size_t)row0 * xrow, (uint32_t)mrows * xrow);
+    const int ns = s.in / (STEPS * 32);                     // scales per weight row
+    const size_t srow = (size_t)e * s.out + n0;
+
+    v4f_t acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t] = v4f_t{0, 0, 0, 0};
+    const int neg136 = (int)0xC308C308u;                    // bf16 -136, twice
+    const v4i_t minus = {neg136, neg136, neg136, neg136};
+
+    v4i_t wv[NT], xv[MT][4];
+    float sc[NT][4 / STEPS];
+    const auto fetch = [&](int c) {
+        const uint32_t kw = (uint32_t)c * 64 + g * 16;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int part = s.swiglu ? t / (NT / 2) : 0;
+            const int rt = s.swiglu ? t % (NT / 2) : t;
+            wv[t] = load_chunk(part ? wr1 : wr0,
+                               kw < wrow ? (uint32_t)(rt * 16 + l16) * wrow + kw : kRsrcPastEnd);
+            const int n = rt * 16 + l16 < left ? rt * 16 + l16 : left - 1;
+            const size_t so = (srow + (size_t)part * half + n) * ns;
+#pragma unroll
+            for (int j = 0; j < 4 / STEPS; ++j) {
+                const int gi = c * (4 / STEPS) + j < ns ? c * (4 / STEPS) + j : ns - 1;
+                if constexpr (E2M1) {
+                    // 2^(byte - 127); byte 0 is the subnormal 2^-127, byte 255 NaN
+                    const uint32_t b = static_cast<const uint8_t*>(a.w_scales)[so + gi];
+                    sc[t][j] = __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+                } else {
+                    const uint32_t b = static_cast<const uint16_t*>(a.w_scales)[so + gi];
+                    sc[t][j] = F16 ? f16_lo(b) : bf16_lo(b);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t kx = (uint32_t)c * 256 + j * 64 + g * 16;
+                xv[m][j] = load_chunk(xr, kx < xrow ? (uint32_t)(m * 16 + l16) * xrow + kx : kRsrcPastEnd);
+            }
+    };
+    for (int c = wave; c < chunks; c += kW4Waves) {
+        fetch(c);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) wv[t] = exchange(wv[t]);
+#pragma unroll
+        for (int j = 0; j < 4 / STEPS; ++j) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                v4f_t start = {0, 0, 0, 0};
+                v4i_t xo[STEPS];
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    xo[i] = E2M1 ? xv[m][j * STEPS + i] : pair_order(xv[m][j * STEPS + i]);
+                    if (!E2M1 && !F16) start = mma16<F16>(xo[i], minus, start);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    v4f_t p = start;
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i)
+                        p = mma16<F16>(xo[i], decode<F16, E2M1>((uint32_t)wv[t][j * STEPS + i]), p);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[m][t][q] = __builtin_fmaf(p[q], sc[t][j], acc[m][t][q]);
+                }
+            }
+        }
+    }
+
+    v4f_t* part = reinterpret_cast<v4f_t*>(lds);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[((wave * MT + m) * NT + t) * kWave + lane] = acc[m][t];
+    __syncthreads();
+    const int nt = s.swiglu ? NT / 2 : NT;
+    for (int i = wave; i < MT * nt; i += kW4Waves) {
+        const int m = i / nt, t = i - m * nt;
+        v4f_t r = part[(m * NT + t) * kWave + lane], u = r;
+#pragma unroll
+        for (int w = 1; w < kW4Waves; ++w) r += part[((w * MT + m) * NT + t) * kWave + lane];
+        if (s.swiglu) {
+            u = part[(m * NT + t + nt) * kWave + lane];
+#pragma unroll
+            for (int w = 1; w < kW4Waves; ++w) u += part[((w * MT + m) * NT + t + nt) * kWave + lane];
+        }
+        const int n = t * 16 + l16;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int row = m * 16 + g * 4 + q;
+            const float y = s.swiglu ? silu(r[q]) * u[q] : r[q];
+            if (row < mrows && n < left)
+                static_cast<uint16_t*>(a.out)[(size_t)(row0 + row) * half + n0 + n] =
+                    (uint16_t)f32_to_tok_rt(y, F16);
+        }
+    }
+    __syncthreads();
+}
+
+template <bool F16, bool E2M1, int STEPS>
+__global__ __launch_bounds__(kW4Waves * kWave) void w4_kernel(MatmulShape s, MatmulArgs a)
+{
+    constexpr int NT = 2, MT = 4;
+    __shared__ float lds[kW4Waves * MT * NT * kWave * 4];
+    const int half = s.swiglu ? s.out / 2 : s.out;
+    const int per = s.swiglu ? NT / 2 * 16 : NT * 16;
+    const int e = blockIdx.y;
+    const int begin = expert_end(s, a.ep_recv_count, a.recv_offsets, e - 1);
+    const int end = expert_end(s, a.ep_recv_count, a.recv_offsets, e);
+    for (int n0 = blockIdx.x * per; n0 < half; n0 += gridDim.x * per) {
+        for (int row = begin + blockIdx.z * MT * 16; row < end; row += gridDim.z * MT * 16) {
+            const int rows = end - row;
+            if (rows <= 16)
+                w4_tile<F16, E2M1, STEPS, 1, NT>(s, a, e, n0, row, rows, lds);
+            else if (rows <= 32)
+                w4_tile<F16, E2M1, STEPS, 2, NT>(s, a, e, n0, row, rows, lds);
+            else
+                w4_tile<F16, E2M1, STEPS, MT, NT>(s, a, e, n0, row, rows, lds);
+        }
+    }
+}
+
+template <bool F16>
+hipError_t launch_token(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+{
+    const int half = s.swiglu ? s.out / 2 : s.out;
+    const int per = s.swiglu ? 16 : 32;
+    int64_t z = (s.rows / s.E + 63) / 64;
+    z = z < 1 ? 1 : z > kW4MaxZ ? kW4MaxZ : z;
+    const dim3 grid((unsigned)((half + per - 1) / per), (unsigned)s.E, (unsigned)z);
+    const dim3 block(kW4Waves * kWave);
+    if (s.w4 == MOE_W4_E2M1)
+        w4_kernel<F16, true, 1><<<grid, block, 0, stream>>>(s, a);
+    else if (s.group == 32)
+        w4_kernel<F16, false, 1><<<grid, block, 0, stream>>>(s, a);
+    else if (s.group == 64)
+        w4_kernel<F16, false, 2><<<grid, block, 0, stream>>>(s, a);
+    else
+        w4_kernel<F16, false, 4><<<grid, block, 0, stream>>>(s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped_matmul_w4(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+{
+    return s.tok_f16 ? launch_token<true>(s, a, stream) : launch_token<false>(s, a, stream);
+}
+
+}  // namespace moe_dc

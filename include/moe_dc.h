@@ -348,6 +348,136 @@ moe_status moe_combine_int8(const moe_dc_config* cfg, const int8_t* codes,
                             const uint8_t* x_active_mask, const void* ori_x, void* y,
                             void* stream);
 
+/* ---- the router and the experts' products -------------------------------------------------
+ *
+ * The calls on either side of the exchange: moe_gate_topk makes the expert_ids and
+ * expert_scales that moe_dispatch and moe_combine take, and the products turn the packed rows
+ * of expand_x into the rows of expert_out.  They follow the conventions at the top of this
+ * header, except that x and weight must be 16-byte aligned (there is no element-wise
+ * fallback).  They need no workspace; each is one kernel. */
+
+/* How the products' codes are scaled. */
+typedef enum {
+    MOE_MM_SCALE_NONE = 0,      /* token rows and weights                                  */
+    MOE_MM_SCALE_ROW = 1,       /* one fp32 per row of x and one per weight row            */
+    MOE_MM_SCALE_MX = 2         /* one E8M0 byte per 32 elements of x and of the weights   */
+} moe_mm_scaling;
+
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SWIGLU = 1          /* weight rows [0, N/2) are the gate, [N/2, N) the up rows  */
+} moe_activation;
+
+/* 4-bit weights: two codes per byte, the element of even index in the low nibble. */
+typedef enum {
+    MOE_W4_INT4 = 1,            /* two's complement, -8..7                                 */
+    MOE_W4_E2M1 = 2             /* OCP E2M1 with E8M0 scales (MX)                          */
+} moe_w4_dtype;
+
+/* One product of the packed rows with the experts' weights.  Eight int32, 32 bytes. */
+typedef struct {
+    int32_t in_features;        /* I, in [1, 65536]: elements of a row of x                 */
+    int32_t out_features;       /* N, in [1, 65536]: weight rows per expert                 */
+    int32_t x_dtype;            /* moe_dtype of the rows: DEFAULT = the token type, INT8,
+                                   E4M3 or E5M2 (moe_grouped_matmul only)                   */
+    int32_t scaling;            /* moe_mm_scaling: NONE for tokens, ROW for INT8, ROW or MX for
+                                   E4M3 and E5M2                                            */
+    int32_t activation;         /* moe_activation                                           */
+    int32_t weight_dtype;       /* moe_w4_dtype for moe_grouped_matmul_w4, else 0            */
+    int32_t group_size;         /* moe_grouped_matmul_w4: 32, 64 or 128 elements per scale
+                                   (E2M1: 32), else 0                                        */
+    int32_t reserved;           /* 0                                                        */
+} moe_matmul;
+
+/* moe_grouped_matmul -- every packed row times its expert's weights.
+ *
+ * For the rows p of expert e (receiver r = e / L, local expert j = e % L: rows from
+ * recv_offsets[r] + ep_recv_count[r][j*W - 1] (0 for j = 0) up to recv_offsets[r] +
+ * ep_recv_count[r][j*W + W - 1]), with X and V the values of x and weight:
+ *   S[p][n]   = sum over i of X[p][i] * V[e][n][i]
+ *   out[p][n] = S[p][n]                                        MOE_ACT_NONE,   n < N
+ *   out[p][n] = silu(S[p][n]) * S[p][N/2 + n], silu(t) = t / (1 + exp(-t))
+ *                                                              MOE_ACT_SWIGLU, n < N/2
+ * X and V are the tokens themselves, code * scale of the row (ROW), or code * 2^(byte - 127) of
+ * the block (MX).
+ *
+ * Inputs:
+ *   x              [cap][I] in x_dtype (mode-0 expand_x, or its codes)
+ *   x_scales       ROW: fp32 [cap] (mode 2's dynamic_scales), or NULL for all 1 (mode 1, whose
+ *                  static scale belongs into weight_scales); MX: bytes [cap][I/32] (the
+ *                  dynamic_scales of MOE_SCALE_E8M0); NULL for tokens
+ *   weight         [E][N][I]: tokens for token rows, int8 for INT8, E4M3 for E4M3 and E5M2
+ *   weight_scales  ROW: fp32 [E][N]; MX: bytes [E][N][I/32]; NULL for tokens
+ *   ep_recv_count, recv_offsets: as produced by moe_dispatch for this config
+ * Output:
+ *   out            token type [cap][N], or [cap][N/2] with SwiGLU.  Rows at or past
+ *                  recv_offsets[W] are not written
+ * I must be a multiple of 8 (tokens), 16 (ROW) or 128 (MX).
+ * Numerics: products are exact; int8 sums are exact in 32 bits; the other sums are fp32 in an
+ * order that depends on the sizes only (the same inputs give the same bytes); ROW scales
+ * multiply the sum (weight's, then row's); out is rounded once, to nearest even.  The fp8
+ * matrix instructions add eight consecutive products at a time and drop, of each product, what
+ * lies below 2^-13 of the largest one's power of two.  An infinity or NaN stays within its own
+ * row (or weight row).
+ * Errors: MOE_ERR_UNSUPPORTED for E2M1 rows; otherwise as for moe_dispatch. */
+moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, const void* x,
+                              const void* x_scales, const void* weight,
+                              const void* weight_scales, const int32_t* ep_recv_count,
+                              const int64_t* recv_offsets, void* out, void* stream);
+
+/* moe_grouped_matmul_w4 -- moe_grouped_matmul of token rows with 4-bit weights.
+ *
+ * V[e][n][i] = code * scale of the group of group_size elements that i belongs to.
+ *   x              token type [cap][I]
+ *   weight         bytes [E][N][I/2], two codes per byte
+ *   weight_scales  int4: token type [E][N][I/group_size]; E2M1: E8M0 bytes [E][N][I/32]
+ * I must be a multiple of group_size.  The codes enter the matrix instructions exactly; each
+ * group's sum is formed in fp32, multiplied by its scale and added in fp32.  x must be finite.
+ * Everything else as for moe_grouped_matmul. */
+moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm, const void* x,
+                                 const void* weight, const void* weight_scales,
+                                 const int32_t* ep_recv_count, const int64_t* recv_offsets,
+                                 void* out, void* stream);
+
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0,
+    MOE_SCORE_SIGMOID = 1
+} moe_score;
+
+/* Attributes of the router.  Five int32 and one float, 24 bytes. */
+typedef struct {
+    int32_t score;              /* moe_score                                                */
+    int32_t group_count;        /* G >= 1, at most 64, a divisor of n; 1 = no group limit    */
+    int32_t group_keep;         /* groups kept per token, in [1, G]                          */
+    int32_t group_top;          /* a group's value is the sum of its 1 or 2 best choices     */
+    int32_t renormalize;        /* 1: the K weights are divided by their sum + 1e-20          */
+    float factor;               /* multiplies the weights                                   */
+} moe_gate;
+
+/* moe_gate_topk -- the K best experts of every token, and their weights.
+ *
+ * Over the n = E + zero + copy ids of the config (n <= 2048, else MOE_ERR_UNSUPPORTED):
+ *   score  = softmax over the n logits, or sigmoid of each
+ *   choice = score + bias (score alone without a bias)
+ *   the ids fall into G groups of n / G in order; with G > 1 only the group_keep groups with
+ *   the largest value (sum of the group_top largest choices) stay
+ *   expert_ids = the K remaining ids with the largest choice, largest first
+ *   expert_scales = their scores (without the bias), divided by (their sum + 1e-20) with
+ *   renormalize, times factor
+ * Equal choices and equal groups go to the lower id.  Choices are compared in binary64, so
+ * that scores next to each other keep their order; without a bias the logits are compared
+ * (which is the same order), and only group values with group_top 2 are sums of scores.
+ *   logits         fp32 [W][BS][n]
+ *   bias           fp32 [n] or NULL
+ *   expert_ids     int32 [W][BS][K]
+ *   expert_scales  fp32 [W][BS][K]
+ * A NaN choice ranks below every number; a softmax row without a finite logit (or with a NaN
+ * or +infinity) has weights 0 or NaN, and its ids are distinct and in range all the same.
+ * K may not exceed the ids of the kept groups. */
+moe_status moe_gate_topk(const moe_dc_config* cfg, const moe_gate* gate, const float* logits,
+                         const float* bias, int32_t* expert_ids, float* expert_scales,
+                         void* stream);
+
 /* Text of the last non-OK status on this thread ("" if none). */
 const char* moe_dc_last_error(void);
 
