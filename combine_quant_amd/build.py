@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_dc.so")
 SOURCES = ["api.cpp", "route.hip", "dispatch.hip", "combine.hip", "noalloc.hip",
-           "experts_api.cpp", "gate.hip", "grouped_matmul.hip", "grouped_matmul_w4.hip"]
+           "experts_api.cpp", "gate.hip", "grouped_matmul_16.hip", "grouped_matmul_int8.hip",
+           "grouped_matmul_fp8.hip", "grouped_matmul_mx.hip", "grouped_matmul_w4.hip"]
 # measurement kernels of bench.py's ceiling mode (the access patterns without the arithmetic)
 CEILING_LIB = os.path.join(HERE, "libmoe_dc_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]

@@ -65,6 +65,19 @@ moe_status check_matmul(const moe_dc_config* cfg, const moe_matmul* mm, MatmulSh
     return MOE_OK;
 }
 
+hipError_t launch_grouped_matmul(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+{
+    switch (s.type) {
+    case moe_dc::kMmBf16: return moe_dc::launch_grouped_bf16(s, a, stream);
+    case moe_dc::kMmF16: return moe_dc::launch_grouped_f16(s, a, stream);
+    case moe_dc::kMmInt8: return moe_dc::launch_grouped_int8(s, a, stream);
+    case moe_dc::kMmE4m3: return moe_dc::launch_grouped_e4m3(s, a, stream);
+    case moe_dc::kMmE5m2: return moe_dc::launch_grouped_e5m2(s, a, stream);
+    case moe_dc::kMmMxE4m3: return moe_dc::launch_grouped_mxe4m3(s, a, stream);
+    default: return moe_dc::launch_grouped_mxe5m2(s, a, stream);
+    }
+}
+
 moe_status check_pointers(const MatmulArgs& a)
 {
     if (!a.x || !a.w || !a.ep_recv_count || !a.recv_offsets || !a.out)
@@ -132,7 +145,7 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
         return fail(MOE_ERR_INVALID_ARG, "weight_scales is required for scaling %d", mm->scaling);
     if (mm->scaling == MOE_MM_SCALE_MX && !x_scales)
         return fail(MOE_ERR_INVALID_ARG, "x_scales is required for MX rows");
-    return launched(moe_dc::launch_grouped_matmul(s, a, static_cast<hipStream_t>(stream)),
+    return launched(launch_grouped_matmul(s, a, static_cast<hipStream_t>(stream)),
                     "grouped matmul launch");
 }
 

@@ -76,6 +76,16 @@ struct Mm {
     }
 };
 
+// Two fp32 values as a pair of tokens, rounded to nearest even by the conversion instructions.
+__device__ __forceinline__ uint32_t pack_out2(float lo, float hi, bool f16)
+{
+    typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+    typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+    const b2_t b = {(__bf16)lo, (__bf16)hi};
+    const h2_t h = {(_Float16)lo, (_Float16)hi};
+    return f16 ? __builtin_bit_cast(uint32_t, h) : __builtin_bit_cast(uint32_t, b);
+}
+
 __device__ __forceinline__ float silu(float t) { return t / (1.0f + __expf(-t)); }
 
 }  // namespace moe_dc

@@ -39,7 +39,14 @@ struct MatmulArgs {
     void* out;
 };
 
-hipError_t launch_grouped_matmul(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+// One per MmType.
+hipError_t launch_grouped_bf16(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_f16(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_int8(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_e4m3(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_e5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_mxe4m3(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_mxe5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_matmul_w4(const MatmulShape& s, const MatmulArgs& a,
                                     hipStream_t stream);
 

@@ -1,8 +1,10 @@
-// grouped_matmul.hip -- products of the packed rows with their experts' weights.
+// grouped_matmul_stream.h -- the experts' products for few rows per expert.
 //
-// Streaming kernel: a workgroup takes NT * 16 weight rows of one expert and walks their inner
-// dimension once, its four waves taking 128-byte chunks in turn, straight from global memory
-// into matrix registers; the waves' sums meet in LDS at the end.
+// A workgroup takes NT * 16 weight rows of one expert and walks their inner dimension once, its
+// four waves taking 128-byte chunks in turn, straight from global memory into matrix registers;
+// the waves' sums meet in LDS at the end.
+#pragma once
+
 #include "experts_device.h"
 
 namespace moe_dc {
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void stream_kernel(MatmulShap
 }
 
 template <int TYPE>
-hipError_t launch_type(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+hipError_t launch_stream(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
     const int half = s.swiglu ? s.out / 2 : s.out;
     const int per = s.swiglu ? 16 : 32;
@@ -173,18 +175,4 @@ hipError_t launch_type(const MatmulShape& s, const MatmulArgs& a, hipStream_t st
 }
 
 }  // namespace
-
-hipError_t launch_grouped_matmul(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
-{
-    switch (s.type) {
-    case kMmBf16: return launch_type<kMmBf16>(s, a, stream);
-    case kMmF16: return launch_type<kMmF16>(s, a, stream);
-    case kMmInt8: return launch_type<kMmInt8>(s, a, stream);
-    case kMmE4m3: return launch_type<kMmE4m3>(s, a, stream);
-    case kMmE5m2: return launch_type<kMmE5m2>(s, a, stream);
-    case kMmMxE4m3: return launch_type<kMmMxE4m3>(s, a, stream);
-    default: return launch_type<kMmMxE5m2>(s, a, stream);
-    }
-}
-
 }  // namespace moe_dc
