@@ -46,11 +46,14 @@ struct Mm {
     static constexpr int kBytes = TYPE == kMmBf16 || TYPE == kMmF16 ? 2 : 1;
     typedef typename std::conditional<kInt, v4i_t, v4f_t>::type Acc;
 
-    // acc += A chunk (a0, a1) * B chunk (b0, b1); sa, sb: the chunk's E8M0 bytes of the lane's
-    // 32-element block l / 16 (MX only).
-    static __device__ __forceinline__ Acc mma(v4i_t a0, v4i_t a1, v4i_t b0, v4i_t b1, Acc acc,
-                                              int sa, int sb)
+    // acc += A chunk * B chunk; sa, sb: the chunk's E8M0 bytes of the lane's 32-element block
+    // l / 16 (MX only).
+    static __device__ __forceinline__ Acc mma(v8i_t a, v8i_t b, Acc acc, int sa, int sb)
     {
+        const v4i_t a0 = __builtin_shufflevector(a, a, 0, 1, 2, 3);
+        const v4i_t a1 = __builtin_shufflevector(a, a, 4, 5, 6, 7);
+        const v4i_t b0 = __builtin_shufflevector(b, b, 0, 1, 2, 3);
+        const v4i_t b1 = __builtin_shufflevector(b, b, 4, 5, 6, 7);
         if constexpr (TYPE == kMmBf16) {
             acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_t, a0),
                                                           __builtin_bit_cast(v8bf_t, b0), acc, 0, 0, 0);
@@ -65,8 +68,6 @@ struct Mm {
             acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, b0, acc, 0, 0, 0);
             return __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, b1, acc, 0, 0, 0);
         } else {
-            const v8i_t a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
-            const v8i_t b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
             // weights are E4M3 (format 0); x is E4M3 or E5M2 (format 1).  Row-scaled codes run
             // with block scales of 2^0.
             constexpr int fx = TYPE == kMmE5m2 || TYPE == kMmMxE5m2 ? 1 : 0;
@@ -75,6 +76,12 @@ struct Mm {
         }
     }
 };
+
+// The two halves of a lane's chunk as one operand.
+__device__ __forceinline__ v8i_t join(v4i_t lo, v4i_t hi)
+{
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
 // Two fp32 values as a pair of tokens, rounded to nearest even by the conversion instructions.
 __device__ __forceinline__ uint32_t pack_out2(float lo, float hi, bool f16)

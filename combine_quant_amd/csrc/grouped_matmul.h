@@ -14,7 +14,7 @@ template <int TYPE>
 hipError_t launch_type(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
     const int64_t nt = ((int64_t)s.out + kTileN - 1) / kTileN;
-    const int64_t mt = (s.rows / s.E + kTileM - 1) / kTileM;
+    const int64_t mt = (s.rows / s.E + kTileM<TYPE> - 1) / kTileM<TYPE>;
     if (s.rows >= kTileMinRows * (int64_t)s.E && s.E * mt * nt >= kTileMinTiles)
         return launch_tiles<TYPE>(s, a, stream);
     return launch_stream<TYPE>(s, a, stream);

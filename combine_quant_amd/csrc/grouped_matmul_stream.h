@@ -90,7 +90,7 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    acc[m][t] = M::mma(wv[d][t][0], wv[d][t][1], xv[d][m][0], xv[d][m][1], acc[m][t],
+                    acc[m][t] = M::mma(join(wv[d][t][0], wv[d][t][1]), join(xv[d][m][0], xv[d][m][1]), acc[m][t],
                                        wsv[d][t], xsv[d][m]);
             fetch(d, c + (d + D) * kStreamWaves);
         }

@@ -9,17 +9,34 @@ namespace {
 constexpr int kTileWaves = 8;
 constexpr int kTileThreads = kTileWaves * kWave;
 constexpr int kTileN = 256;                     // weight rows of a workgroup
-constexpr int kTileM = 256;                     // most rows of x of a workgroup
-constexpr int kTileScales = (kTileN + kTileM) * 4;
+constexpr int kTileRing = 3;                    // steps of x in LDS
 constexpr int kMaxExperts = 1024;
 constexpr int kGroupM = 8;                      // row tiles that share a sweep over the weights
 
-struct TileLds {
-    char x[2][kTileM * 128];                    // [row][128 bytes], swizzled
-    char w[2][kTileN * 128];
-    char scales[2][kTileScales];                // MX: four E8M0 bytes a row of x, then weights
+// Most rows of x of a workgroup: as many as the 160 KB of LDS take (MX keeps scales there too).
+template <int TYPE>
+constexpr int kTileM = Mm<TYPE>::kMx ? 224 : 256;
+
+template <int TYPE>
+struct TileStages {
+    char x[kTileRing][kTileM<TYPE> * 128];      // [row][128 bytes], swizzled
+    char w[kTileWaves][2][32 * 128];            // each wave's own 32 weight rows, swizzled
+    // MX: the step's four E8M0 bytes of each row of x and of each weight row
+    char xs[kTileRing][Mm<TYPE>::kMx ? 1024 : 0];
+    char ws[kTileWaves][2][Mm<TYPE>::kMx ? 256 : 0];
+};
+
+struct TileTable {
     int cum[kMaxExperts + 1];                   // tiles before each expert
     int wave_sum[kTileWaves];
+};
+
+// The table is done with before the first stage is filled.
+template <int TYPE>
+union TileLds {
+    char x[kTileRing][kTileM<TYPE> * 128];
+    TileStages<TYPE> st;
+    TileTable table;
 };
 
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t off)
@@ -33,18 +50,35 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, u
         r, (__attribute__((address_space(3))) void*)lds, 4, (int)off, 0, 0, 0);
 }
 
-// One tile: 32 * MS rows of x from row0 (of which `rows` exist), 256 weight rows from column n0.
-// Wave w: row half w / 4 (16 * MS rows), weight rows 64 * (w % 4) + 0..63 of the tile.
-template <int TYPE, int MS, bool SWIGLU>
+// Waits until at most N of the wave's global loads are outstanding (they return in order).
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// One tile: 16 * MT rows of x from row0 (of which `rows` exist), 256 weight rows from column n0.
+// Wave w owns weight rows 32 * w + 0..31 of the tile (with SwiGLU 16 gate rows and the 16 up
+// rows of the same columns) and multiplies them with every row of x.  All operands come through
+// LDS, moved there by the loads themselves: the matrix layout wants neighbouring lanes in
+// different rows, which as a load from global memory runs at 16 bytes a clock per CU (9.4 TB/s over
+// the chip, against 24 TB/s for whole 128-byte rows).
+//
+// Step k (128 bytes of every row) waits for its own operands only.  x lies in a ring of three
+// stages: the barrier of step k makes x(k) visible and frees the stage that step k - 1
+// read, which takes x(k + 2).  A wave's weights are its own, so they need no barrier: the
+// operands of step k + 1 move from LDS to registers at the start of step k, and their place takes
+// the weights of step k + 3.  Loads past the end of a row return 0 without a memory access, so
+// every step issues the same number.
+template <int TYPE, int MT, bool SWIGLU>
 __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulArgs& a, int e,
-                                             int n0, int row0, int rows, TileLds& lds)
+                                             int n0, int row0, int rows, TileStages<TYPE>& lds)
 {
     typedef Mm<TYPE> M;
     typedef typename M::Acc Acc;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, g = lane >> 4;
-    const int wn = wave & 3, wm = wave >> 2;
     const uint32_t row_bytes = (uint32_t)s.in * M::kBytes;
     const int steps = (int)((row_bytes + 127) / 128);
     const int half = SWIGLU ? s.out / 2 : s.out;
@@ -58,112 +92,166 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         make_rsrc(static_cast<const char*>(a.x) + (size_t)row0 * row_bytes, (uint32_t)rows * row_bytes);
     const uint32_t ns = (uint32_t)s.in / 32;
     const char* wsb = static_cast<const char*>(a.w_scales) + ((size_t)e * s.out + n0) * ns;
-    const __amdgpu_buffer_rsrc_t ws0 = make_rsrc(wsb, M::kMx ? (uint32_t)left * ns : 0);
-    const __amdgpu_buffer_rsrc_t ws1 =
-        make_rsrc(wsb + (size_t)half * ns, M::kMx ? (uint32_t)left * ns : 0);
+    const __amdgpu_buffer_rsrc_t wsr = make_rsrc(wsb, M::kMx ? (uint32_t)(SWIGLU ? half + left : left) * ns : 0);
     const __amdgpu_buffer_rsrc_t xs =
         make_rsrc(static_cast<const char*>(a.x_scales) + (size_t)row0 * ns,
                   M::kMx ? (uint32_t)rows * ns : 0);
 
-    // Staging: one instruction moves 8 rows of 128 bytes; lane i brings row i / 8 the 16 bytes
-    // that belong at position i % 8, which holds chunk (i % 8) ^ (row & 7).
+    // One load moves 8 rows of 128 bytes; lane i brings row i / 8 the 16 bytes that belong at
+    // position i % 8, which holds chunk (i % 8) ^ (row & 7).
     const int lr = lane >> 3;
     const uint32_t lk = (uint32_t)((lane & 7) ^ lr) * 16;
-    constexpr int kXLoads = (4 * MS + kTileWaves - 1) / kTileWaves;
+    constexpr int kBlocks = 2 * MT;                          // of 8 rows
+    constexpr int kXLoads = (kBlocks + kTileWaves - 1) / kTileWaves;
+    // (where the blocks do not go round, some waves load again what another one does, so that
+    // every wave issues the same number without a branch)
     uint32_t xoff[kXLoads], woff[4];
+    int xblk[kXLoads];
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i)
-        xoff[i] = (uint32_t)((wave + i * kTileWaves) * 8 + lr) * row_bytes + lk;
+    for (int i = 0; i < kXLoads; ++i) {
+        xblk[i] = wave + i * kTileWaves;
+        if (xblk[i] >= kBlocks) xblk[i] %= kBlocks;
+        xoff[i] = (uint32_t)(xblk[i] * 8 + lr) * row_bytes + lk;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // weight row block wave + 8 * i of 32; with SwiGLU each 64 rows hold 32 gate, 32 up
-        const int blk = wave + i * kTileWaves;
-        const int r = SWIGLU ? (blk >> 3) * 32 + (blk & 3) * 8 : blk * 8;
+        const int r = SWIGLU ? wave * 16 + (i & 1) * 8 : wave * 32 + i * 8;
         woff[i] = (uint32_t)(r + lr) * row_bytes + lk;
     }
-    const auto stage_x = [&](int step) {
+    // MX: the dword of scales of the lane's row
+    const int wsrow = SWIGLU ? wave * 16 + l16 : wave * 32 + (lane & 31);
+    const uint32_t wsoff = wsrow < left ? (uint32_t)(SWIGLU && (lane & 16) ? half + wsrow : wsrow) * ns
+                                        : kRsrcPastEnd;
+    const int xsblk = wave & 3;                              // 64 rows per load
+    const uint32_t xsoff = (uint32_t)(xsblk * 64 + lane) * ns;
+    // Load i of a step's x, and of its weights.
+    const auto fetch_x = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 128;
-        char* xl = lds.x[step & 1];
         const bool past = k + lk >= row_bytes;
-#pragma unroll
-        for (int i = 0; i < kXLoads; ++i) {
-            const int blk = wave + i * kTileWaves;
-            if ((4 * MS) % kTileWaves == 0 || blk < 4 * MS)
-                load_lds16(xr, xl + blk * 1024, past ? kRsrcPastEnd : xoff[i] + k);
-        }
-        if (M::kMx) {
-            // 64 rows of four bytes per instruction: waves 0-3 the weights, 4-7 the rows of x
-            char* sl = lds.scales[step & 1];
-            if (wave < 4) {
-                const int up = SWIGLU && lane >= 32;
-                const int r = SWIGLU ? wave * 32 + (lane & 31) : wave * 64 + lane;
-                if (!up) load_lds4(ws0, sl + 1024 + wave * 256, (uint32_t)r * ns + step * 4);
-                if (up) load_lds4(ws1, sl + 1024 + wave * 256, (uint32_t)r * ns + step * 4);
-            } else if ((wave - 4) * 2 < MS) {
-                load_lds4(xs, sl + (wave - 4) * 256,
-                          (uint32_t)((wave - 4) * 64 + lane) * ns + step * 4);
-            }
-        }
+        char* to = lds.x[step % kTileRing];
+        load_lds16(xr, to + xblk[i] * 1024, past ? kRsrcPastEnd : xoff[i] + k);
+        if (M::kMx && i == 0)
+            load_lds4(xs, lds.xs[step % kTileRing] + xsblk * 256,
+                      step < steps ? xsoff + step * 4 : kRsrcPastEnd);
     };
-    const auto stage_w = [&](int step) {
+    const auto fetch_w = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 128;
-        char* wl = lds.w[step & 1];
         const bool past = k + lk >= row_bytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int blk = wave + i * kTileWaves;
-            load_lds16(SWIGLU && (blk & 4) ? wr1 : wr0, wl + blk * 1024,
-                       past ? kRsrcPastEnd : woff[i] + k);
-        }
+        char* to = lds.w[wave][step & 1];
+        load_lds16(SWIGLU && i >= 2 ? wr1 : wr0, to + i * 1024, past ? kRsrcPastEnd : woff[i] + k);
+        if (M::kMx && i == 0)
+            load_lds4(wsr, lds.ws[wave][step & 1],
+                      step < steps && wsoff != kRsrcPastEnd ? wsoff + step * 4 : kRsrcPastEnd);
     };
 
-    Acc acc[MS][4];
-#pragma unroll
-    for (int m = 0; m < MS; ++m)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[m][t] = Acc{0, 0, 0, 0};
     const int f0 = l16 * 128 + ((g ^ (l16 & 7)) << 4);
     const int f1 = l16 * 128 + (((4 + g) ^ (l16 & 7)) << 4);
+    v8i_t w[2][2];
+    int wsc[2][2] = {{0, 0}, {0, 0}};
+    const auto read_w = [&](int par) {
+        const char* wl = lds.w[wave][par];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            w[par][t] = join(*reinterpret_cast<const v4i_t*>(wl + t * 2048 + f0),
+                             *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f1));
+            if (M::kMx)
+                wsc[par][t] = *reinterpret_cast<const uint8_t*>(lds.ws[wave][par] + (t * 16 + l16) * 4 + g);
+        }
+    };
+    Acc acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = Acc{0, 0, 0, 0};
 
-    stage_x(0);
-    stage_w(0);
-    for (int step = 0; step < steps; ++step) {
-        const int b = step & 1;
-        __syncthreads();                        // this step's operands are in LDS
-        if (step + 1 < steps) {
-            stage_x(step + 1);
-            stage_w(step + 1);
-        }
-        const char* xl = lds.x[b] + wm * MS * 2048;
-        const char* wl = lds.w[b] + wn * 8192;
-        v4i_t w0[4], w1[4];
-        int sa[4] = {0, 0, 0, 0};
+    // loads issued after those a step waits for: x(k + 1), weights(k + 2)
+    constexpr int kAhead = kXLoads + 4 + (M::kMx ? 2 : 0);
+    const auto all_x = [&](int step) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            w0[t] = *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f0);
-            w1[t] = *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f1);
-            if (M::kMx)
-                sa[t] = *reinterpret_cast<const uint8_t*>(lds.scales[b] + 1024 +
-                                                          (wn * 64 + t * 16 + l16) * 4 + g);
-        }
+        for (int i = 0; i < kXLoads; ++i) fetch_x(step, i);
+    };
+    const auto all_w = [&](int step) {
 #pragma unroll
-        for (int m = 0; m < MS; ++m) {
-            const v4i_t x0 = *reinterpret_cast<const v4i_t*>(xl + m * 2048 + f0);
-            const v4i_t x1 = *reinterpret_cast<const v4i_t*>(xl + m * 2048 + f1);
-            int sb = 0;
-            if (M::kMx)
-                sb = *reinterpret_cast<const uint8_t*>(lds.scales[b] +
-                                                       ((wm * MS + m) * 16 + l16) * 4 + g);
+        for (int i = 0; i < 4; ++i) fetch_w(step, i);
+    };
+    all_x(0);
+    all_w(0);
+    all_w(1);
+    all_x(1);
+    wait_loads<kAhead>();
+    read_w(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    all_w(2);
+    // A step's products go in groups of 32 rows: a group reads the next group's rows from LDS and
+    // issues its share of the step's loads before its own products.  (Issued together at the
+    // step's start, the loads fill the address queue and hold up the products: 1.09 ms instead of
+    // XXXX at 16384 rows x 7168 x 4096 bf16.)  The first half of the groups loads x(k + 2), the
+    // second the weights of k + 3, whose place is free once read_w has returned.
+    constexpr int kGroups = MT / 2;
+    constexpr int kXGroups = kGroups > 1 ? kGroups / 2 : 1;
+    constexpr int kWFirst = kGroups > 1 ? kGroups / 2 : 0, kWGroups = kGroups - kWFirst;
+    constexpr int kReadW = kWFirst >= 2 ? kWFirst - 2 : 0;
+    const auto one = [&](int par, int step) {
+        wait_loads<kAhead>();
+        __builtin_amdgcn_s_barrier();
+        const char* xl = lds.x[step % kTileRing];
+        const char* xsl = lds.xs[step % kTileRing];
+        v8i_t x[2][2];
+        int xsv[2][2] = {{0, 0}, {0, 0}};
+        const auto read_x = [&](int set, int group) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc[m][t] = M::mma(w0[t], w1[t], x0, x1, acc[m][t], sa[t], sb);
+            for (int i = 0; i < 2; ++i) {
+                const int m = group * 2 + i;
+                x[set][i] = join(*reinterpret_cast<const v4i_t*>(xl + m * 2048 + f0),
+                                 *reinterpret_cast<const v4i_t*>(xl + m * 2048 + f1));
+                if (M::kMx) xsv[set][i] = *reinterpret_cast<const uint8_t*>(xsl + (m * 16 + l16) * 4 + g);
+            }
+        };
+        read_x(0, 0);
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+            if (q == kReadW) read_w(par ^ 1);
+            if (q + 1 < kGroups) read_x((q + 1) & 1, q + 1);
+            if (q == kWFirst && kWFirst < kReadW + 2)
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < kXLoads; ++i)
+                if (i * kXGroups / kXLoads == q) fetch_x(step + 2, i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (kWFirst + i * kWGroups / 4 == q) fetch_w(step + 3, i);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    acc[q * 2 + i][t] = M::mma(w[par][t], x[q & 1][i], acc[q * 2 + i][t], wsc[par][t],
+                                               xsv[q & 1][i]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    int step = 0;
+    for (; step + 2 <= steps; step += 2) {
+        one(0, step);
+        one(1, step + 1);
     }
+    if (step < steps) one(0, step);
+    wait_loads<0>();                            // nothing may land in LDS after the tile
 
-    constexpr int kT = SWIGLU ? 2 : 4;
-    const int c0 = wn * (kT * 16) + g * 4;      // the lane's first column of sub-tile 0
+    constexpr int kT = SWIGLU ? 1 : 2;
+    const int c0 = wave * (kT * 16) + g * 4;    // the lane's first column
+    float ws_[2][4];
+    if (M::kRowScaled) {
 #pragma unroll
-    for (int m = 0; m < MS; ++m) {
-        const int row = (wm * MS + m) * 16 + l16;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = c0 + (SWIGLU ? 0 : t * 16) + q;
+                ws_[t][q] = c < left ? static_cast<const float*>(
+                    a.w_scales)[(size_t)e * s.out + n0 + c + (SWIGLU ? t * half : 0)] : 0.0f;
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int row = m * 16 + l16;
         if (row >= rows) continue;
         float rs = 1.0f;
         if (M::kRowScaled && a.x_scales) rs = static_cast<const float*>(a.x_scales)[row0 + row];
@@ -174,14 +262,14 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
             float y[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float r = (float)acc[m][t][q], u = 0.0f;
-                if (SWIGLU) u = (float)acc[m][(t + kT) & 3][q];
-                if (M::kRowScaled && c + q < left) {
-                    const float* sc = static_cast<const float*>(a.w_scales) + (size_t)e * s.out + n0 + c + q;
-                    r = r * sc[0] * rs;
-                    if (SWIGLU) u = u * sc[half] * rs;
+                float r = (float)acc[m][t][q];
+                if (M::kRowScaled) r = r * ws_[t][q] * rs;
+                if (SWIGLU) {
+                    float u = (float)acc[m][1][q];
+                    if (M::kRowScaled) u = u * ws_[1][q] * rs;
+                    r = silu(r) * u;
                 }
-                y[q] = SWIGLU ? silu(r) * u : r;
+                y[q] = r;
             }
             const uint2 p = make_uint2(pack_out2(y[0], y[1], s.tok_f16), pack_out2(y[2], y[3], s.tok_f16));
             if (c + 3 < left && half % 4 == 0) {
@@ -197,13 +285,14 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 }
 
 // Every workgroup counts the tiles of all experts (ragged counts live on the device), then
-// finds its own.  An expert's rows are cut into as few tiles of at most 256 rows as possible,
+// finds its own.  An expert's rows are cut into as few tiles of at most kTileM rows as possible,
 // all of nearly the same height.  Consecutive tiles go to one XCD (workgroups are dealt to the
 // XCDs in turn), so that the tiles of an expert share its weights in that XCD's L2.
 template <int TYPE, bool SWIGLU>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, MatmulArgs a)
 {
-    __shared__ TileLds lds;
+    __shared__ TileLds<TYPE> lds;
+    constexpr int kRows = kTileM<TYPE>;
     const int half = SWIGLU ? s.out / 2 : s.out;
     constexpr int kCols = SWIGLU ? kTileN / 2 : kTileN;
     const int nt = (half + kCols - 1) / kCols;
@@ -216,10 +305,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
     if (e0 < s.E) {
         const int b = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 - 1);
         const int m = expert_end(s, a.ep_recv_count, a.recv_offsets, e0);
-        t0 = m > b ? (m - b + kTileM - 1) / kTileM * nt : 0;
+        t0 = m > b ? (m - b + kRows - 1) / kRows * nt : 0;
         if (e0 + 1 < s.E) {
             const int f = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 + 1);
-            t1 = f > m ? (f - m + kTileM - 1) / kTileM * nt : 0;
+            t1 = f > m ? (f - m + kRows - 1) / kRows * nt : 0;
         }
     }
     int sum = t0 + t1;
@@ -228,15 +317,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
         const int o = __shfl_up(sum, off, kWave);
         if (lane >= off) sum += o;
     }
-    if (lane == kWave - 1) lds.wave_sum[wave] = sum;
+    if (lane == kWave - 1) lds.table.wave_sum[wave] = sum;
     __syncthreads();
-    for (int w = 0; w < wave; ++w) sum += lds.wave_sum[w];
-    if (e0 < s.E) lds.cum[e0 + 1] = sum - t1;
-    if (e0 + 1 < s.E) lds.cum[e0 + 2] = sum;
-    if (threadIdx.x == 0) lds.cum[0] = 0;
+    for (int w = 0; w < wave; ++w) sum += lds.table.wave_sum[w];
+    if (e0 < s.E) lds.table.cum[e0 + 1] = sum - t1;
+    if (e0 + 1 < s.E) lds.table.cum[e0 + 2] = sum;
+    if (threadIdx.x == 0) lds.table.cum[0] = 0;
     __syncthreads();
 
-    const int total = lds.cum[s.E];
+    const int total = lds.table.cum[s.E];
     const int chunk = (total + 7) / 8;
     const int slot = blockIdx.x >> 3;
     const int tile = (int)(blockIdx.x & 7) * chunk + slot;
@@ -244,13 +333,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
     int lo = 0, hi = s.E;                       // cum[lo] <= tile < cum[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (lds.cum[mid] <= tile) lo = mid; else hi = mid;
+        if (lds.table.cum[mid] <= tile) lo = mid; else hi = mid;
     }
     const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int idx = __builtin_amdgcn_readfirstlane(tile - lds.cum[lo]);
+    const int idx = __builtin_amdgcn_readfirstlane(tile - lds.table.cum[lo]);
+    __syncthreads();                            // the table gives way to the stages
     const int begin = expert_end(s, a.ep_recv_count, a.recv_offsets, e - 1);
     const int count = expert_end(s, a.ep_recv_count, a.recv_offsets, e) - begin;
-    const int mt = (count + kTileM - 1) / kTileM;
+    const int mt = (count + kRows - 1) / kRows;
     const int height = ((count + mt - 1) / mt + 31) / 32 * 32;
     const int band = idx / (kGroupM * nt), in_band = idx - band * kGroupM * nt;
     const int bm = mt - band * kGroupM < kGroupM ? mt - band * kGroupM : kGroupM;
@@ -259,14 +349,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
     const int rows = count - r0 < height ? count - r0 : height;
     if (rows <= 0) return;
     switch ((rows + 31) / 32) {
-    case 1: tile_product<TYPE, 1, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
-    case 2: tile_product<TYPE, 2, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
-    case 3: tile_product<TYPE, 3, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
-    case 4: tile_product<TYPE, 4, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
-    case 5: tile_product<TYPE, 5, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
-    case 6: tile_product<TYPE, 6, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
-    case 7: tile_product<TYPE, 7, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
-    default: tile_product<TYPE, 8, SWIGLU>(s, a, e, n0, begin + r0, rows, lds); break;
+    case 1: tile_product<TYPE, 2, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    case 2: tile_product<TYPE, 4, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    case 3: tile_product<TYPE, 6, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    case 4: tile_product<TYPE, 8, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    case 5: tile_product<TYPE, 10, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    case 6: tile_product<TYPE, 12, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    case 7: tile_product<TYPE, 14, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    default:
+        if constexpr (kRows > 224) tile_product<TYPE, 16, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st);
+        break;
     }
 }
 
@@ -276,7 +368,7 @@ hipError_t launch_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t s
     const int64_t half = s.swiglu ? s.out / 2 : s.out;
     const int64_t cols = s.swiglu ? kTileN / 2 : kTileN;
     const int64_t active = s.rows < s.E ? s.rows : s.E;
-    const int64_t tiles = (s.rows / kTileM + active) * ((half + cols - 1) / cols);
+    const int64_t tiles = (s.rows / kTileM<TYPE> + active) * ((half + cols - 1) / cols);
     const dim3 grid((unsigned)((tiles + 7) / 8 * 8));
     if (s.swiglu)
         tile_kernel<TYPE, true><<<grid, kTileThreads, 0, stream>>>(s, a);
