@@ -1,0 +1,120 @@
+// experts_tiles.h -- tiles of the experts' products: how ragged rows are cut and dealt out, and
+// loads that move their data to LDS by themselves.
+#pragma once
+
+#include "experts_device.h"
+
+namespace moe_dc {
+namespace {
+
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = kTileWaves * kWave;
+constexpr int kMaxExperts = 1024;
+constexpr int kGroupM = 8;                      // row tiles that share a sweep over the weights
+
+struct TileTable {
+    int cum[kMaxExperts + 1];                   // tiles before each expert
+    int wave_sum[kTileWaves];
+};
+
+struct Tile {
+    int e;                                      // expert
+    int n0;                                     // first output column
+    int row0, rows;                             // rows of x
+};
+
+// Workgroups that suffice for any counts of s.rows rows (tiles of `height` rows, `cols` columns).
+inline unsigned tile_grid(const MatmulShape& s, int height, int cols)
+{
+    const int64_t half = s.swiglu ? s.out / 2 : s.out;
+    const int64_t active = s.rows < s.E ? s.rows : s.E;
+    const int64_t tiles = (s.rows / height + active) * ((half + cols - 1) / cols);
+    return (unsigned)((tiles + 7) / 8 * 8);
+}
+
+// The workgroup's tile.  The ragged counts live on the device, so every workgroup counts the
+// tiles of all experts, then finds its own.  An expert's rows are cut into as few tiles of at
+// most ROWS rows as possible, all of nearly the same height (a multiple of 32).  Consecutive
+// tiles go to one XCD (workgroups are dealt to the XCDs in turn), so that the tiles of an expert
+// share its weights and its rows in that XCD's L2.
+template <int ROWS, int COLS>
+__device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs& a, int columns,
+                                          TileTable& table, Tile* out)
+{
+    const int nt = (columns + COLS - 1) / COLS;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = threadIdx.x / kWave;
+
+    // experts 2 * thread and 2 * thread + 1
+    const int e0 = threadIdx.x * 2;
+    int t0 = 0, t1 = 0;
+    if (e0 < s.E) {
+        const int b = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 - 1);
+        const int m = expert_end(s, a.ep_recv_count, a.recv_offsets, e0);
+        t0 = m > b ? (m - b + ROWS - 1) / ROWS * nt : 0;
+        if (e0 + 1 < s.E) {
+            const int f = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 + 1);
+            t1 = f > m ? (f - m + ROWS - 1) / ROWS * nt : 0;
+        }
+    }
+    int sum = t0 + t1;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int o = __shfl_up(sum, off, kWave);
+        if (lane >= off) sum += o;
+    }
+    if (lane == kWave - 1) table.wave_sum[wave] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) sum += table.wave_sum[w];
+    if (e0 < s.E) table.cum[e0 + 1] = sum - t1;
+    if (e0 + 1 < s.E) table.cum[e0 + 2] = sum;
+    if (threadIdx.x == 0) table.cum[0] = 0;
+    __syncthreads();
+
+    const int total = table.cum[s.E];
+    const int chunk = (total + 7) / 8;
+    const int slot = blockIdx.x >> 3;
+    const int tile = (int)(blockIdx.x & 7) * chunk + slot;
+    if (slot >= chunk || tile >= total) return false;
+    int lo = 0, hi = s.E;                       // cum[lo] <= tile < cum[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (table.cum[mid] <= tile) lo = mid; else hi = mid;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    const int idx = __builtin_amdgcn_readfirstlane(tile - table.cum[lo]);
+    __syncthreads();                            // the table's LDS is free again
+    const int begin = expert_end(s, a.ep_recv_count, a.recv_offsets, e - 1);
+    const int count = expert_end(s, a.ep_recv_count, a.recv_offsets, e) - begin;
+    const int mt = (count + ROWS - 1) / ROWS;
+    const int height = ((count + mt - 1) / mt + 31) / 32 * 32;
+    const int band = idx / (kGroupM * nt), in_band = idx - band * kGroupM * nt;
+    const int bm = mt - band * kGroupM < kGroupM ? mt - band * kGroupM : kGroupM;
+    const int r0 = (band * kGroupM + in_band % bm) * height;
+    out->e = e;
+    out->n0 = in_band / bm * COLS;
+    out->row0 = begin + r0;
+    out->rows = count - r0 < height ? count - r0 : height;
+    return out->rows > 0;
+}
+
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)lds, 16, (int)off, 0, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)lds, 4, (int)off, 0, 0, 0);
+}
+
+// Waits until at most N of the wave's global loads are outstanding (they return in order).
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+}  // namespace
+}  // namespace moe_dc

@@ -1,17 +1,13 @@
 // grouped_matmul_tile.h -- the experts' products for many rows per expert.
 #pragma once
 
-#include "experts_device.h"
+#include "experts_tiles.h"
 
 namespace moe_dc {
 namespace {
 
-constexpr int kTileWaves = 8;
-constexpr int kTileThreads = kTileWaves * kWave;
 constexpr int kTileN = 256;                     // weight rows of a workgroup
 constexpr int kTileRing = 3;                    // steps of x in LDS
-constexpr int kMaxExperts = 1024;
-constexpr int kGroupM = 8;                      // row tiles that share a sweep over the weights
 
 // Most rows of x of a workgroup: as many as the 160 KB of LDS take (MX keeps scales there too).
 template <int TYPE>
@@ -26,11 +22,6 @@ struct TileStages {
     char ws[kTileWaves][2][Mm<TYPE>::kMx ? 256 : 0];
 };
 
-struct TileTable {
-    int cum[kMaxExperts + 1];                   // tiles before each expert
-    int wave_sum[kTileWaves];
-};
-
 // The table is done with before the first stage is filled.
 template <int TYPE>
 union TileLds {
@@ -38,24 +29,6 @@ union TileLds {
     TileStages<TYPE> st;
     TileTable table;
 };
-
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t off)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, (__attribute__((address_space(3))) void*)lds, 16, (int)off, 0, 0, 0);
-}
-__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t off)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, (__attribute__((address_space(3))) void*)lds, 4, (int)off, 0, 0, 0);
-}
-
-// Waits until at most N of the wave's global loads are outstanding (they return in order).
-template <int N>
-__device__ __forceinline__ void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
 
 // One tile: 16 * MT rows of x from row0 (of which `rows` exist), 256 weight rows from column n0.
 // Wave w owns weight rows 32 * w + 0..31 of the tile (with SwiGLU 16 gate rows and the 16 up
@@ -71,9 +44,10 @@ __device__ __forceinline__ void wait_loads()
 // the weights of step k + 3.  Loads past the end of a row return 0 without a memory access, so
 // every step issues the same number.
 template <int TYPE, int MT, bool SWIGLU>
-__device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulArgs& a, int e,
-                                             int n0, int row0, int rows, TileStages<TYPE>& lds)
+__device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulArgs& a,
+                                             const Tile& tile, TileStages<TYPE>& lds)
 {
+    const int e = tile.e, n0 = tile.n0, row0 = tile.row0, rows = tile.rows;
     typedef Mm<TYPE> M;
     typedef typename M::Acc Acc;
     const int lane = threadIdx.x & (kWave - 1);
@@ -284,80 +258,24 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     }
 }
 
-// Every workgroup counts the tiles of all experts (ragged counts live on the device), then
-// finds its own.  An expert's rows are cut into as few tiles of at most kTileM rows as possible,
-// all of nearly the same height.  Consecutive tiles go to one XCD (workgroups are dealt to the
-// XCDs in turn), so that the tiles of an expert share its weights in that XCD's L2.
 template <int TYPE, bool SWIGLU>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, MatmulArgs a)
 {
     __shared__ TileLds<TYPE> lds;
     constexpr int kRows = kTileM<TYPE>;
-    const int half = SWIGLU ? s.out / 2 : s.out;
-    constexpr int kCols = SWIGLU ? kTileN / 2 : kTileN;
-    const int nt = (half + kCols - 1) / kCols;
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = threadIdx.x / kWave;
-
-    // experts 2 * thread and 2 * thread + 1
-    const int e0 = threadIdx.x * 2;
-    int t0 = 0, t1 = 0;
-    if (e0 < s.E) {
-        const int b = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 - 1);
-        const int m = expert_end(s, a.ep_recv_count, a.recv_offsets, e0);
-        t0 = m > b ? (m - b + kRows - 1) / kRows * nt : 0;
-        if (e0 + 1 < s.E) {
-            const int f = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 + 1);
-            t1 = f > m ? (f - m + kRows - 1) / kRows * nt : 0;
-        }
-    }
-    int sum = t0 + t1;
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const int o = __shfl_up(sum, off, kWave);
-        if (lane >= off) sum += o;
-    }
-    if (lane == kWave - 1) lds.table.wave_sum[wave] = sum;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) sum += lds.table.wave_sum[w];
-    if (e0 < s.E) lds.table.cum[e0 + 1] = sum - t1;
-    if (e0 + 1 < s.E) lds.table.cum[e0 + 2] = sum;
-    if (threadIdx.x == 0) lds.table.cum[0] = 0;
-    __syncthreads();
-
-    const int total = lds.table.cum[s.E];
-    const int chunk = (total + 7) / 8;
-    const int slot = blockIdx.x >> 3;
-    const int tile = (int)(blockIdx.x & 7) * chunk + slot;
-    if (slot >= chunk || tile >= total) return;
-    int lo = 0, hi = s.E;                       // cum[lo] <= tile < cum[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (lds.table.cum[mid] <= tile) lo = mid; else hi = mid;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int idx = __builtin_amdgcn_readfirstlane(tile - lds.table.cum[lo]);
-    __syncthreads();                            // the table gives way to the stages
-    const int begin = expert_end(s, a.ep_recv_count, a.recv_offsets, e - 1);
-    const int count = expert_end(s, a.ep_recv_count, a.recv_offsets, e) - begin;
-    const int mt = (count + kRows - 1) / kRows;
-    const int height = ((count + mt - 1) / mt + 31) / 32 * 32;
-    const int band = idx / (kGroupM * nt), in_band = idx - band * kGroupM * nt;
-    const int bm = mt - band * kGroupM < kGroupM ? mt - band * kGroupM : kGroupM;
-    const int n0 = in_band / bm * kCols;
-    const int r0 = (band * kGroupM + in_band % bm) * height;
-    const int rows = count - r0 < height ? count - r0 : height;
-    if (rows <= 0) return;
-    switch ((rows + 31) / 32) {
-    case 1: tile_product<TYPE, 2, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
-    case 2: tile_product<TYPE, 4, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
-    case 3: tile_product<TYPE, 6, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
-    case 4: tile_product<TYPE, 8, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
-    case 5: tile_product<TYPE, 10, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
-    case 6: tile_product<TYPE, 12, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
-    case 7: tile_product<TYPE, 14, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st); break;
+    Tile t;
+    if (!find_tile<kRows, SWIGLU ? kTileN / 2 : kTileN>(s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t))
+        return;
+    switch ((t.rows + 31) / 32) {
+    case 1: tile_product<TYPE, 2, SWIGLU>(s, a, t, lds.st); break;
+    case 2: tile_product<TYPE, 4, SWIGLU>(s, a, t, lds.st); break;
+    case 3: tile_product<TYPE, 6, SWIGLU>(s, a, t, lds.st); break;
+    case 4: tile_product<TYPE, 8, SWIGLU>(s, a, t, lds.st); break;
+    case 5: tile_product<TYPE, 10, SWIGLU>(s, a, t, lds.st); break;
+    case 6: tile_product<TYPE, 12, SWIGLU>(s, a, t, lds.st); break;
+    case 7: tile_product<TYPE, 14, SWIGLU>(s, a, t, lds.st); break;
     default:
-        if constexpr (kRows > 224) tile_product<TYPE, 16, SWIGLU>(s, a, e, n0, begin + r0, rows, lds.st);
+        if constexpr (kRows > 224) tile_product<TYPE, 16, SWIGLU>(s, a, t, lds.st);
         break;
     }
 }
@@ -365,11 +283,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
 template <int TYPE>
 hipError_t launch_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
-    const int64_t half = s.swiglu ? s.out / 2 : s.out;
-    const int64_t cols = s.swiglu ? kTileN / 2 : kTileN;
-    const int64_t active = s.rows < s.E ? s.rows : s.E;
-    const int64_t tiles = (s.rows / kTileM<TYPE> + active) * ((half + cols - 1) / cols);
-    const dim3 grid((unsigned)((tiles + 7) / 8 * 8));
+    const dim3 grid(tile_grid(s, kTileM<TYPE>, s.swiglu ? kTileN / 2 : kTileN));
     if (s.swiglu)
         tile_kernel<TYPE, true><<<grid, kTileThreads, 0, stream>>>(s, a);
     else

@@ -1,0 +1,348 @@
+// grouped_matmul_w4_tile.h -- 4-bit products for many rows per expert.
+//
+// A workgroup multiplies up to 128 rows of x with 256 weight rows, in steps of 128 elements;
+// wave w owns weight rows 32 * w + 0..31 (with SwiGLU 16 gate rows and the 16 up rows of the same
+// columns) and takes every row of x.  x (256 bytes a row and step) lies in a ring of three LDS
+// stages, a wave's codes (64 bytes a row and step) in a ring of two of its own; loads move both
+// there by themselves.  Each step decodes the codes of the next one to 16-bit floats in
+// registers, a quarter with each part of its own products, so that the conversions run
+// beside the matrix instructions.
+//
+// x is the A operand (rows of the result) and the weights B (columns): lane l holds column
+// l % 16 and rows (l / 16) * 4 + 0..3, hence one scale per lane and column tile.
+#pragma once
+
+#include "grouped_matmul_w4.h"
+
+namespace moe_dc {
+namespace {
+
+constexpr int kW4TileM = 128;
+constexpr int kW4TileN = 256;
+constexpr int kW4Ring = 3;
+constexpr int kW4TileMinRows = 24;
+constexpr int kW4TileMinTiles = 192;
+
+struct W4Stages {
+    char x[kW4Ring][2][kW4TileM * 128];         // [64 elements][row][128 bytes], swizzled
+    char w[kTileWaves][2][32 * 64];             // each wave's own weight rows, swizzled
+};
+
+union W4Lds {
+    W4Stages st;
+    TileTable table;
+};
+
+// int4 codes as bf16 exactly, in the order 0 4 1 5 2 6 3 7: low code l of a pair of shorts.  The
+// sign-and-magnitude byte of code c (c = u - 16 for u > 7) is an E4M3 subnormal (or 2^-6 for
+// 8), worth c * 2^-9; the conversion multiplies by 2^9.
+__device__ __forceinline__ uint32_t int4_bytes(uint32_t low3, uint32_t sign)
+{
+    // low3: bits 0-2 of each byte's code, sign: its bit 3 moved to bit 0.  Negative codes become
+    // 0x88 - low3 = (low3 ^ 7) + 0x81.
+    return (low3 ^ ((sign << 3) - sign)) + ((sign << 7) | sign);
+}
+
+template <bool F16, bool E2M1, bool SCALED>
+__device__ __forceinline__ v4i_t decode_tile(uint32_t w, float scale)
+{
+    v4i_t r;
+    if constexpr (E2M1) {
+        const float m = SCALED ? scale : 1.0f;
+        if constexpr (F16) {
+            r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 0));
+            r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 1));
+            r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 2));
+            r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 3));
+        } else {
+            r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 0));
+            r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 1));
+            r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 2));
+            r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 3));
+        }
+        return r;
+    } else if constexpr (F16) {
+        return decode<true, false>(w);          // order 0 4 1 5 2 6 3 7
+    } else {
+        const uint32_t v = w >> 4;
+        const uint32_t even = int4_bytes(w & 0x07070707u, (w >> 3) & 0x01010101u);   // 0 2 4 6
+        const uint32_t odd = int4_bytes(v & 0x07070707u, (v >> 3) & 0x01010101u);    // 1 3 5 7
+        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, false));
+        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, false));
+        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, true));
+        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, true));
+        return r;                               // order 0 2 1 3 4 6 5 7
+    }
+}
+
+// x in the order of the decoded codes.
+template <bool F16, bool E2M1>
+__device__ __forceinline__ v4i_t tile_order(v4i_t x)
+{
+    if constexpr (E2M1) {
+        return x;
+    } else if constexpr (F16) {
+        return pair_order(x);
+    } else {
+        v4i_t r;
+        r.x = (int)__builtin_amdgcn_perm((uint32_t)x.y, (uint32_t)x.x, 0x05040100u);
+        r.y = (int)__builtin_amdgcn_perm((uint32_t)x.y, (uint32_t)x.x, 0x07060302u);
+        r.z = (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.z, 0x05040100u);
+        r.w = (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.z, 0x07060302u);
+        return r;
+    }
+}
+
+template <bool F16, bool E2M1, int STEPS, int MT, bool SWIGLU>
+__device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const MatmulArgs& a,
+                                                const Tile& tile, W4Stages& lds)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, g = lane >> 4;
+    const uint32_t xrow = (uint32_t)s.in * 2, wrow = (uint32_t)s.in / 2;
+    const int steps = (s.in + 127) / 128;
+    const int half = SWIGLU ? s.out / 2 : s.out;
+    constexpr int kCols = SWIGLU ? kW4TileN / 2 : kW4TileN;
+    const int left = half - tile.n0 < kCols ? half - tile.n0 : kCols;
+    const size_t first = (size_t)tile.e * s.out + tile.n0;
+    const char* wbase = static_cast<const char*>(a.w) + first * wrow;
+    const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(wbase, (uint32_t)left * wrow);
+    const __amdgpu_buffer_rsrc_t wr1 = make_rsrc(wbase + (size_t)half * wrow, (uint32_t)left * wrow);
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(
+        static_cast<const char*>(a.x) + (size_t)tile.row0 * xrow, (uint32_t)tile.rows * xrow);
+    constexpr int kSize = E2M1 ? 1 : 2;                      // bytes of a scale
+    constexpr int kParts = 4 / STEPS;                        // scales of a row and step
+    const int ns = s.in / (STEPS * 32);
+    const char* sbase = static_cast<const char*>(a.w_scales) + first * ns * kSize;
+    const __amdgpu_buffer_rsrc_t sr0 = make_rsrc(sbase, (uint32_t)left * ns * kSize);
+    const __amdgpu_buffer_rsrc_t sr1 =
+        make_rsrc(sbase + (size_t)half * ns * kSize, (uint32_t)left * ns * kSize);
+    // bf16 holds every E2M1 code times a power of two, so its scale enters with the conversion.
+    constexpr bool kFolded = E2M1 && !F16;
+
+    const int lr = lane >> 3;
+    const uint32_t lk = (uint32_t)((lane & 7) ^ lr) * 16;
+    constexpr int kXLoads = MT / 2;                          // 2 halves of 2 * MT blocks, 8 waves
+    uint32_t xoff[kXLoads];
+    int xto[kXLoads];
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) {
+        const int b = wave + i * kTileWaves;                 // block of 8 rows: half b / (2 MT)
+        const int hb = b / (2 * MT), rb = b % (2 * MT);
+        xto[i] = hb * kW4TileM * 128 + rb * 1024;
+        xoff[i] = (uint32_t)(rb * 8 + lr) * xrow + hb * 128 + lk;
+    }
+    // Codes: a load moves 16 rows of 64 bytes; lane i brings row i / 4 the 16 bytes of position
+    // i % 4, which holds chunk (i % 4) ^ (row / 4 & 3).
+    const int wr = lane >> 2;
+    const uint32_t wk = (uint32_t)((lane & 3) ^ ((wr >> 2) & 3)) * 16;
+    const uint32_t woff0 = (uint32_t)(wave * (SWIGLU ? 16 : 32) + wr) * wrow + wk;
+    const uint32_t woff1 = SWIGLU ? woff0 : woff0 + 16 * wrow;
+    const uint32_t soff0 = (uint32_t)(wave * (SWIGLU ? 16 : 32) + l16) * ns * kSize;
+    const uint32_t soff1 = SWIGLU ? soff0 : soff0 + 16 * ns * kSize;
+
+    const auto fetch_x = [&](int step, int i) {
+        const uint32_t k = (uint32_t)step * 256;
+        // the offset within the row is below xrow (rows end inside a step)
+        const int b = wave + i * kTileWaves;
+        const bool past = k + (b / (2 * MT)) * 128 + lk >= xrow;
+        load_lds16(xr, lds.x[step % kW4Ring][0] + xto[i], past ? kRsrcPastEnd : xoff[i] + k);
+    };
+    const auto fetch_w = [&](int step) {
+        const uint32_t k = (uint32_t)step * 64;
+        const bool past = k + wk >= wrow;
+        char* to = lds.w[wave][step & 1];
+        load_lds16(wr0, to, past ? kRsrcPastEnd : woff0 + k);
+        load_lds16(SWIGLU ? wr1 : wr0, to + 1024, past ? kRsrcPastEnd : woff1 + k);
+    };
+    float scale[2][2][kParts];
+    const auto fetch_scale = [&](int par, int step) {
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) {
+            const bool past = step * kParts + j >= ns;
+            const uint32_t k = (uint32_t)(step * kParts + j) * kSize;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int off = (int)(past ? kRsrcPastEnd : (t ? soff1 : soff0) + k);
+                const __amdgpu_buffer_rsrc_t r = SWIGLU && t ? sr1 : sr0;
+                if constexpr (E2M1) {
+                    const uint32_t b = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
+                    scale[par][t][j] = __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+                } else {
+                    const uint32_t b = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+                    scale[par][t][j] = F16 ? f16_lo(b) : bf16_lo(b);
+                }
+            }
+        }
+    };
+
+    // The lane's dword of step j of row l16: chunk j, dword g.
+    uint32_t raw[2][4];
+    const auto read_raw = [&](int step) {
+        const char* wl = lds.w[wave][step & 1] + l16 * 64 + g * 4;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                raw[t][j] = *reinterpret_cast<const uint32_t*>(wl + t * 1024 + ((j ^ (l16 >> 2)) << 4));
+    };
+    v4i_t w[2][2][4];
+    const auto decode_part = [&](int par, int j) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            w[par][t][j] = decode_tile<F16, E2M1, kFolded>(raw[t][j], kFolded ? scale[par][t][j / STEPS] : 1.0f);
+    };
+
+    v4f_t acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = v4f_t{0, 0, 0, 0};
+    const int f0 = l16 * 128 + ((g ^ (l16 & 7)) << 4);
+    const int f1 = l16 * 128 + (((4 + g) ^ (l16 & 7)) << 4);
+
+    constexpr int kScales = 2 * kParts;
+    // Before step 0: its codes decoded, the codes of step 1 in registers, x(0), x(1) and the codes
+    // of step 2 on their way.
+    fetch_w(0);
+    fetch_w(1);
+    fetch_scale(0, 0);
+    fetch_scale(1, 1);
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) fetch_x(0, i);
+    wait_loads<kXLoads>();
+    read_raw(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) decode_part(0, j);
+    read_raw(1);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) fetch_x(1, i);
+    fetch_w(2);
+    wait_loads<kXLoads + 2>();
+
+    const auto one = [&](int par, int step) {
+        // x(step): issued after it are the codes of step + 1, then scales, x(step + 1) and
+        // the codes of step + 2
+        wait_loads<2 + kScales + kXLoads + 2>();
+        __builtin_amdgcn_s_barrier();
+        const char* xl = lds.x[step % kW4Ring][0];
+        v4i_t x[2][4];
+        const auto read_x = [&](int set, int m) {
+            const char* p = xl + m * 2048;
+            x[set][0] = *reinterpret_cast<const v4i_t*>(p + f0);
+            x[set][1] = *reinterpret_cast<const v4i_t*>(p + f1);
+            x[set][2] = *reinterpret_cast<const v4i_t*>(p + kW4TileM * 128 + f0);
+            x[set][3] = *reinterpret_cast<const v4i_t*>(p + kW4TileM * 128 + f1);
+        };
+        read_x(0, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (m + 1 < MT) read_x((m + 1) & 1, m + 1);
+#pragma unroll
+            for (int i = 0; i < kXLoads; ++i)
+                if (i * MT / kXLoads == m) fetch_x(step + 2, i);
+            // (the place of step + 1's codes, which were read before this step's first rows)
+            if (m == MT - 1) fetch_w(step + 3);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j * MT / 4 == m) decode_part(par ^ 1, j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[m & 1][j] = tile_order<F16, E2M1>(x[m & 1][j]);
+            if constexpr (kFolded) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) acc[m][t] = mma16<F16>(x[m & 1][j], w[par][t][j], acc[m][t]);
+            } else {
+                v4f_t sum[kParts][2];
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    sum[p][0] = sum[p][1] = v4f_t{0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            sum[p][t] = mma16<F16>(x[m & 1][p * STEPS + j], w[par][t][p * STEPS + j], sum[p][t]);
+                }
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[m][t][r] = __builtin_fmaf(sum[p][t][r], scale[par][t][p], acc[m][t][r]);
+                // (keeps the additions here: postponed, the sums of all rows stay in registers)
+                asm volatile("" : "+v"(acc[m][0]), "+v"(acc[m][1]));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // The codes of step + 2 (after them: this step's x(step + 2) and codes of step + 3), and
+        // the scales of step + 2 in place of this step's.
+        wait_loads<kXLoads + 2>();
+        read_raw(step + 2);
+        fetch_scale(par, step + 2);
+    };
+    int step = 0;
+    for (; step + 2 <= steps; step += 2) {
+        one(0, step);
+        one(1, step + 1);
+    }
+    if (step < steps) one(0, step);
+    wait_loads<0>();                            // nothing may land in LDS after the tile
+
+    constexpr int kT = SWIGLU ? 1 : 2;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            const int c = wave * (kT * 16) + t * 16 + l16;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = m * 16 + g * 4 + r;
+                const float y = SWIGLU ? silu(acc[m][0][r]) * acc[m][1][r] : acc[m][t][r];
+                if (row < tile.rows && c < left)
+                    static_cast<uint16_t*>(a.out)[(size_t)(tile.row0 + row) * half + tile.n0 + c] =
+                        (uint16_t)pack_out2(y, 0.0f, F16);
+            }
+        }
+}
+
+template <bool F16, bool E2M1, int STEPS, bool SWIGLU>
+__global__ __launch_bounds__(kTileThreads, 2) void w4_tile_kernel(MatmulShape s, MatmulArgs a)
+{
+    __shared__ W4Lds lds;
+    Tile t;
+    if (!find_tile<kW4TileM, SWIGLU ? kW4TileN / 2 : kW4TileN>(s, a, SWIGLU ? s.out / 2 : s.out,
+                                                               lds.table, &t))
+        return;
+    switch ((t.rows + 31) / 32) {
+    case 1: w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU>(s, a, t, lds.st); break;
+    case 2: w4_tile_product<F16, E2M1, STEPS, 4, SWIGLU>(s, a, t, lds.st); break;
+    case 3: w4_tile_product<F16, E2M1, STEPS, 6, SWIGLU>(s, a, t, lds.st); break;
+    default: w4_tile_product<F16, E2M1, STEPS, 8, SWIGLU>(s, a, t, lds.st); break;
+    }
+}
+
+template <bool F16, bool E2M1, int STEPS>
+hipError_t launch_w4_tile(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+{
+    const dim3 grid(tile_grid(s, kW4TileM, s.swiglu ? kW4TileN / 2 : kW4TileN));
+    if (s.swiglu)
+        w4_tile_kernel<F16, E2M1, STEPS, true><<<grid, kTileThreads, 0, stream>>>(s, a);
+    else
+        w4_tile_kernel<F16, E2M1, STEPS, false><<<grid, kTileThreads, 0, stream>>>(s, a);
+    return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_w4_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+{
+    if (s.w4 == MOE_W4_E2M1) return launch_w4_tile<F16, true, 1>(s, a, stream);
+    if (s.group == 32) return launch_w4_tile<F16, false, 1>(s, a, stream);
+    if (s.group == 64) return launch_w4_tile<F16, false, 2>(s, a, stream);
+    return launch_w4_tile<F16, false, 4>(s, a, stream);
+}
+
+}  // namespace
+}  // namespace moe_dc

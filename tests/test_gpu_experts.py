@@ -121,6 +121,23 @@ def test_product_many_rows(kind):
     _run_product(kind, 2, [513, 1281, 0, 2], 640, 1029, False, seed=6)
 
 
+# Rows per expert that give every tile height, several tiles per expert and empty experts; with 32
+# experts and more than 1536 weight rows there are tiles enough for the tile kernels.
+RAGGED = [0, 1, 33, 64, 65, 97, 130, 161, 193, 225, 256, 257, 300, 511, 513, 769,
+          31, 32, 0, 0, 16, 15, 2, 90, 224, 128, 129, 5, 48, 70, 0, 449]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("steps,N,swiglu", [
+    (0, 1600, False), (1, 1666, True), (2, 1541, False), (8, 1602, True), (25, 1537, False),
+    (40, 2054, True),
+])
+def test_product_tiles(kind, steps, N, swiglu):
+    """Inner sizes of steps + 1 pieces of the type's granularity through the tile kernels."""
+    step = 128 if kind.startswith("mx") else 24 if kind in ("bf16", "f16") else 48
+    _run_product(kind, 4, RAGGED, step * (steps + 1), N, swiglu, seed=steps)
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3", "e5m2"])
 def test_product_without_row_scales(kind):
     """x_scales may be absent (static quantization): every row scale is 1."""
@@ -243,6 +260,16 @@ def test_4bit_odd_sizes(token, weight, group, I, N, swiglu):
 @pytest.mark.parametrize("weight,group", W4)
 def test_4bit_many_rows(token, weight, group):
     _run_w4(token, weight, group, 2, [700, 0, 257, 512, 1, 1025, 385, 255], 896, 520, True, seed=5)
+
+
+@pytest.mark.parametrize("token", ["bf16", "f16"])
+@pytest.mark.parametrize("weight,group", W4)
+@pytest.mark.parametrize("groups,N,swiglu", [
+    (1, 1600, False), (2, 1666, True), (3, 1541, False), (7, 1602, True), (13, 1537, False),
+    (20, 2054, True),
+])
+def test_4bit_tiles(token, weight, group, groups, N, swiglu):
+    _run_w4(token, weight, group, 4, RAGGED, group * groups, N, swiglu, seed=groups)
 
 
 def test_4bit_every_code():
