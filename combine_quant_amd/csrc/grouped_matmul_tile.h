@@ -11,15 +11,14 @@ constexpr int kTileRing = 3;                    // steps of x in LDS
 
 // Most rows of x of a workgroup: as many as the 160 KB of LDS take (MX keeps scales there too).
 template <int TYPE>
-constexpr int kTileM = Mm<TYPE>::kMx ? 224 : 256;
+constexpr int kTileM = Mm<TYPE>::kMx ? 192 : 256;
 
 template <int TYPE>
 struct TileStages {
     char x[kTileRing][kTileM<TYPE> * 128];      // [row][128 bytes], swizzled
     char w[kTileWaves][2][32 * 128];            // each wave's own 32 weight rows, swizzled
-    // MX: the step's four E8M0 bytes of each row of x and of each weight row
-    char xs[kTileRing][Mm<TYPE>::kMx ? 1024 : 0];
-    char ws[kTileWaves][2][Mm<TYPE>::kMx ? 256 : 0];
+    // MX: the E8M0 bytes of four steps, 16 of each row of x, then of each weight row
+    char scales[2][Mm<TYPE>::kMx ? (kTileM<TYPE> + kTileN) * 16 : 0];
 };
 
 // The table is done with before the first stage is filled.
@@ -66,10 +65,6 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         make_rsrc(static_cast<const char*>(a.x) + (size_t)row0 * row_bytes, (uint32_t)rows * row_bytes);
     const uint32_t ns = (uint32_t)s.in / 32;
     const char* wsb = static_cast<const char*>(a.w_scales) + ((size_t)e * s.out + n0) * ns;
-    const __amdgpu_buffer_rsrc_t wsr = make_rsrc(wsb, M::kMx ? (uint32_t)(SWIGLU ? half + left : left) * ns : 0);
-    const __amdgpu_buffer_rsrc_t xs =
-        make_rsrc(static_cast<const char*>(a.x_scales) + (size_t)row0 * ns,
-                  M::kMx ? (uint32_t)rows * ns : 0);
 
     // One load moves 8 rows of 128 bytes; lane i brings row i / 8 the 16 bytes that belong at
     // position i % 8, which holds chunk (i % 8) ^ (row & 7).
@@ -92,44 +87,52 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         const int r = SWIGLU ? wave * 16 + (i & 1) * 8 : wave * 32 + i * 8;
         woff[i] = (uint32_t)(r + lr) * row_bytes + lk;
     }
-    // MX: the dword of scales of the lane's row
-    const int wsrow = SWIGLU ? wave * 16 + l16 : wave * 32 + (lane & 31);
-    const uint32_t wsoff = wsrow < left ? (uint32_t)(SWIGLU && (lane & 16) ? half + wsrow : wsrow) * ns
-                                        : kRsrcPastEnd;
-    const int xsblk = wave & 3;                              // 64 rows per load
-    const uint32_t xsoff = (uint32_t)(xsblk * 64 + lane) * ns;
+    // MX: every fourth step a wave brings 16 bytes of scales of 64 rows: waves 0-2 rows of x,
+    // waves 3-6 weight rows (wave 7 the same as wave 6).  Rows are ns bytes, ns a multiple of 4.
+    const bool sx = wave * 64 < kTileM<TYPE>;
+    const int sblk = sx ? wave : (wave < 6 ? wave : 6) - kTileM<TYPE> / 64;
+    const int srow = sblk * 64 + lane;
+    const int scol = SWIGLU ? srow / 32 * 16 + (srow & 15) : srow;      // of the weight row
+    const bool sok = sx ? srow < rows : scol < left;
+    const uint32_t soff = (uint32_t)(sx ? srow : SWIGLU && (srow & 16) ? half + scol : scol) * ns;
+    const __amdgpu_buffer_rsrc_t sr = make_rsrc(
+        sx ? static_cast<const char*>(a.x_scales) + (size_t)row0 * ns : wsb,
+        !M::kMx ? 0 : (uint32_t)(sx ? rows : SWIGLU ? half + left : left) * ns);
+    const int sto = (sx ? 0 : kTileM<TYPE> * 16) + sblk * 1024;
+    const auto fetch_scales = [&](int window) {
+        // one dword (a step's bytes) at a time at the end of a row, which need not fill 16 bytes
+        const uint32_t k = (uint32_t)window * 16;
+        char* to = lds.scales[window & 1] + sto;
+        load_lds16(sr, to, sok && k < ns ? soff + k : kRsrcPastEnd);
+    };
     // Load i of a step's x, and of its weights.
     const auto fetch_x = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 128;
         const bool past = k + lk >= row_bytes;
         char* to = lds.x[step % kTileRing];
         load_lds16(xr, to + xblk[i] * 1024, past ? kRsrcPastEnd : xoff[i] + k);
-        if (M::kMx && i == 0)
-            load_lds4(xs, lds.xs[step % kTileRing] + xsblk * 256,
-                      step < steps ? xsoff + step * 4 : kRsrcPastEnd);
     };
     const auto fetch_w = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 128;
         const bool past = k + lk >= row_bytes;
         char* to = lds.w[wave][step & 1];
         load_lds16(SWIGLU && i >= 2 ? wr1 : wr0, to + i * 1024, past ? kRsrcPastEnd : woff[i] + k);
-        if (M::kMx && i == 0)
-            load_lds4(wsr, lds.ws[wave][step & 1],
-                      step < steps && wsoff != kRsrcPastEnd ? wsoff + step * 4 : kRsrcPastEnd);
     };
 
     const int f0 = l16 * 128 + ((g ^ (l16 & 7)) << 4);
     const int f1 = l16 * 128 + (((4 + g) ^ (l16 & 7)) << 4);
     v8i_t w[2][2];
     int wsc[2][2] = {{0, 0}, {0, 0}};
-    const auto read_w = [&](int par) {
+    const auto read_w = [&](int par, int step) {
         const char* wl = lds.w[wave][par];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             w[par][t] = join(*reinterpret_cast<const v4i_t*>(wl + t * 2048 + f0),
                              *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f1));
             if (M::kMx)
-                wsc[par][t] = *reinterpret_cast<const uint8_t*>(lds.ws[wave][par] + (t * 16 + l16) * 4 + g);
+                wsc[par][t] = *reinterpret_cast<const uint8_t*>(
+                    lds.scales[step >> 2 & 1] + (kTileM<TYPE> + wave * 32 + t * 16 + l16) * 16 +
+                    (step & 3) * 4 + g);
         }
     };
     Acc acc[MT][2];
@@ -137,7 +140,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = Acc{0, 0, 0, 0};
 
     // loads issued after those a step waits for: x(k + 1), weights(k + 2)
-    constexpr int kAhead = kXLoads + 4 + (M::kMx ? 2 : 0);
+    constexpr int kAhead = kXLoads + 4;
     const auto all_x = [&](int step) {
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) fetch_x(step, i);
@@ -146,12 +149,14 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 #pragma unroll
         for (int i = 0; i < 4; ++i) fetch_w(step, i);
     };
+    if (M::kMx) fetch_scales(0);
     all_x(0);
     all_w(0);
     all_w(1);
     all_x(1);
     wait_loads<kAhead>();
-    read_w(0);
+    if (M::kMx) __builtin_amdgcn_s_barrier();   // the scales come from other waves
+    read_w(0, 0);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     all_w(2);
     // A step's products go in groups of 32 rows: a group reads the next group's rows from LDS and
@@ -163,11 +168,13 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     constexpr int kXGroups = kGroups > 1 ? kGroups / 2 : 1;
     constexpr int kWFirst = kGroups > 1 ? kGroups / 2 : 0, kWGroups = kGroups - kWFirst;
     constexpr int kReadW = kWFirst >= 2 ? kWFirst - 2 : 0;
-    const auto one = [&](int par, int step) {
+    const auto one = [&](int phase, int step) {              // phase: step modulo the unrolling
+        const int par = phase & 1;
         wait_loads<kAhead>();
         __builtin_amdgcn_s_barrier();
         const char* xl = lds.x[step % kTileRing];
-        const char* xsl = lds.xs[step % kTileRing];
+        const char* xsl = lds.scales[step >> 2 & 1] + phase * 4;
+        if (M::kMx && phase == 0) fetch_scales((step >> 2) + 1);
         v8i_t x[2][2];
         int xsv[2][2] = {{0, 0}, {0, 0}};
         const auto read_x = [&](int set, int group) {
@@ -176,13 +183,13 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                 const int m = group * 2 + i;
                 x[set][i] = join(*reinterpret_cast<const v4i_t*>(xl + m * 2048 + f0),
                                  *reinterpret_cast<const v4i_t*>(xl + m * 2048 + f1));
-                if (M::kMx) xsv[set][i] = *reinterpret_cast<const uint8_t*>(xsl + (m * 16 + l16) * 4 + g);
+                if (M::kMx) xsv[set][i] = *reinterpret_cast<const uint8_t*>(xsl + (m * 16 + l16) * 16 + g);
             }
         };
         read_x(0, 0);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-            if (q == kReadW) read_w(par ^ 1);
+            if (q == kReadW) read_w(par ^ 1, step + 1);
             if (q + 1 < kGroups) read_x((q + 1) & 1, q + 1);
             if (q == kWFirst && kWFirst < kReadW + 2)
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -202,12 +209,15 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    constexpr int kUnroll = M::kMx ? 4 : 2;
     int step = 0;
-    for (; step + 2 <= steps; step += 2) {
-        one(0, step);
-        one(1, step + 1);
+    for (; step + kUnroll <= steps; step += kUnroll) {
+#pragma unroll
+        for (int r = 0; r < kUnroll; ++r) one(r, step + r);
     }
-    if (step < steps) one(0, step);
+#pragma unroll
+    for (int r = 0; r < kUnroll - 1; ++r)
+        if (step + r < steps) one(r, step + r);
     wait_loads<0>();                            // nothing may land in LDS after the tile
 
     constexpr int kT = SWIGLU ? 1 : 2;
@@ -273,9 +283,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
     case 4: tile_product<TYPE, 8, SWIGLU>(s, a, t, lds.st); break;
     case 5: tile_product<TYPE, 10, SWIGLU>(s, a, t, lds.st); break;
     case 6: tile_product<TYPE, 12, SWIGLU>(s, a, t, lds.st); break;
-    case 7: tile_product<TYPE, 14, SWIGLU>(s, a, t, lds.st); break;
     default:
-        if constexpr (kRows > 224) tile_product<TYPE, 16, SWIGLU>(s, a, t, lds.st);
+        if constexpr (kRows > 192) {
+            if (t.rows <= 224)
+                tile_product<TYPE, 14, SWIGLU>(s, a, t, lds.st);
+            else
+                tile_product<TYPE, 16, SWIGLU>(s, a, t, lds.st);
+        }
         break;
     }
 }
