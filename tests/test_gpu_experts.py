@@ -346,6 +346,22 @@ def test_router(W, BS, E, Z, K, groups, keep, top, with_bias, sigmoid):
 
 
 @pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("W,BS,E,Z,K,groups,keep,top", [
+    (4, 512, 256, 0, 8, 8, 4, 2), (16, 131, 16, 0, 3, 1, 1, 1), (8, 300, 512, 4, 16, 1, 1, 1),
+    (5, 411, 180, 1, 16, 1, 1, 1), (4, 512, 252, 4, 12, 64, 20, 1), (8, 257, 576, 0, 9, 18, 5, 2),
+])
+def test_router_many_tokens(W, BS, E, Z, K, groups, keep, top, with_bias, sigmoid):
+    """Tokens enough for four to share a wave, the last wave partly empty."""
+    g = torch.Generator().manual_seed(W + K)
+    n = E + Z
+    logits = torch.randn((W * BS, n), generator=g) * 2
+    logits[::7] = (logits[::7] * 4).round() / 4                 # many equal logits in some rows
+    bias = torch.randn((n,), generator=g) * 0.1 if with_bias else None
+    _run_gate(W, BS, E, Z, K, logits, bias, sigmoid, groups, keep, top, True, 2.5)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("groups,keep,top", [(1, 1, 1), (8, 3, 2), (4, 2, 1)])
 def test_router_ties_go_to_the_lower_id(sigmoid, groups, keep, top):
     g = torch.Generator().manual_seed(9)
