@@ -145,6 +145,8 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
         return fail(MOE_ERR_INVALID_ARG, "weight_scales is required for scaling %d", mm->scaling);
     if (mm->scaling == MOE_MM_SCALE_MX && !x_scales)
         return fail(MOE_ERR_INVALID_ARG, "x_scales is required for MX rows");
+    if (!aligned(x_scales, 4) || !aligned(weight_scales, 4))
+        return fail(MOE_ERR_INVALID_ARG, "x_scales and weight_scales must be 4-byte aligned");
     return launched(launch_grouped_matmul(s, a, static_cast<hipStream_t>(stream)),
                     "grouped matmul launch");
 }
@@ -175,6 +177,8 @@ moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm,
     st = check_pointers(a);
     if (st != MOE_OK) return st;
     if (!weight_scales) return fail(MOE_ERR_INVALID_ARG, "weight_scales is required");
+    if (!aligned(weight_scales, 4))
+        return fail(MOE_ERR_INVALID_ARG, "weight_scales must be 4-byte aligned");
     return launched(moe_dc::launch_grouped_matmul_w4(s, a, static_cast<hipStream_t>(stream)),
                     "4-bit grouped matmul launch");
 }

@@ -32,6 +32,17 @@ inline unsigned tile_grid(const MatmulShape& s, int height, int cols)
     return (unsigned)((tiles + 7) / 8 * 8);
 }
 
+// Whether tiles of `height` rows and `cols` columns are enough work for the chip, in the mean over
+// the experts that can have rows.
+constexpr int kMinTiles = 192;                  // of 256 CUs, one workgroup each
+inline bool tiles_suffice(const MatmulShape& s, int height, int cols)
+{
+    const int64_t half = s.swiglu ? s.out / 2 : s.out;
+    const int64_t active = s.rows < s.E ? s.rows : s.E;
+    if (active == 0) return false;
+    return active * ((s.rows / active + height - 1) / height) * ((half + cols - 1) / cols) >= kMinTiles;
+}
+
 // The workgroup's tile.  The ragged counts live on the device, so every workgroup counts the
 // tiles of all experts, then finds its own.  An expert's rows are cut into as few tiles of at
 // most ROWS rows as possible, all of nearly the same height (a multiple of 32).  Consecutive

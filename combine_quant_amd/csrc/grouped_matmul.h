@@ -7,15 +7,10 @@
 namespace moe_dc {
 namespace {
 
-constexpr int kTileMinRows = 24;                // mean rows per expert from which tiles are used
-constexpr int kTileMinTiles = 192;              // and tiles enough for most of the 256 CUs
-
 template <int TYPE>
 hipError_t launch_type(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
-    const int64_t nt = ((int64_t)s.out + kTileN - 1) / kTileN;
-    const int64_t mt = (s.rows / s.E + kTileM<TYPE> - 1) / kTileM<TYPE>;
-    if (s.rows >= kTileMinRows * (int64_t)s.E && s.E * mt * nt >= kTileMinTiles)
+    if (tiles_suffice(s, kTileM<TYPE>, s.swiglu ? kTileN / 2 : kTileN))
         return launch_tiles<TYPE>(s, a, stream);
     return launch_stream<TYPE>(s, a, stream);
 }

@@ -169,9 +169,7 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_kernel(MatmulShape s, Mat
 template <bool F16>
 hipError_t launch_token(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
-    const int64_t nt = ((int64_t)s.out + kW4TileN - 1) / kW4TileN;
-    const int64_t mt = (s.rows / s.E + kW4TileM - 1) / kW4TileM;
-    if (s.rows >= kW4TileMinRows * (int64_t)s.E && s.E * mt * nt >= kW4TileMinTiles)
+    if (tiles_suffice(s, kW4TileM, s.swiglu ? kW4TileN / 2 : kW4TileN))
         return launch_w4_tiles<F16>(s, a, stream);
     const int half = s.swiglu ? s.out / 2 : s.out;
     const int per = s.swiglu ? 16 : 32;

@@ -20,8 +20,6 @@ namespace {
 constexpr int kW4TileM = 128;
 constexpr int kW4TileN = 256;
 constexpr int kW4Ring = 3;
-constexpr int kW4TileMinRows = 24;
-constexpr int kW4TileMinTiles = 192;
 
 struct W4Stages {
     char x[kW4Ring][2][kW4TileM * 128];         // [64 elements][row][128 bytes], swizzled
@@ -111,13 +109,20 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const __amdgpu_buffer_rsrc_t wr1 = make_rsrc(wbase + (size_t)half * wrow, (uint32_t)left * wrow);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(
         static_cast<const char*>(a.x) + (size_t)tile.row0 * xrow, (uint32_t)tile.rows * xrow);
+    // Scales are read as whole dwords (the tensor begins at one, rows begin anywhere): a step's
+    // scales of a row lie in the last dword of the step before and the kDwords loaded for it.
     constexpr int kSize = E2M1 ? 1 : 2;                      // bytes of a scale
     constexpr int kParts = 4 / STEPS;                        // scales of a row and step
-    const int ns = s.in / (STEPS * 32);
-    const char* sbase = static_cast<const char*>(a.w_scales) + first * ns * kSize;
-    const __amdgpu_buffer_rsrc_t sr0 = make_rsrc(sbase, (uint32_t)left * ns * kSize);
-    const __amdgpu_buffer_rsrc_t sr1 =
-        make_rsrc(sbase + (size_t)half * ns * kSize, (uint32_t)left * ns * kSize);
+    constexpr int kStepBytes = kParts * kSize;               // 2, 4 or 8
+    constexpr int kDwords = kStepBytes == 8 ? 2 : 1;
+    const uint32_t srow = (uint32_t)(s.in / (STEPS * 32)) * kSize;      // bytes of a row
+    const size_t sfirst = first * srow, sup = (size_t)half * srow;
+    const char* sbase = static_cast<const char*>(a.w_scales);
+    const auto scale_rsrc = [&](size_t at) {
+        return make_rsrc(sbase + (at & ~(size_t)3), ((uint32_t)(at & 3) + (uint32_t)left * srow + 3) & ~3u);
+    };
+    const __amdgpu_buffer_rsrc_t sr0 = scale_rsrc(sfirst);
+    const __amdgpu_buffer_rsrc_t sr1 = scale_rsrc(sfirst + sup);
     // bf16 holds every E2M1 code times a power of two, so its scale enters with the conversion.
     constexpr bool kFolded = E2M1 && !F16;
 
@@ -139,9 +144,10 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const uint32_t wk = (uint32_t)((lane & 3) ^ ((wr >> 2) & 3)) * 16;
     const uint32_t woff0 = (uint32_t)(wave * (SWIGLU ? 16 : 32) + wr) * wrow + wk;
     const uint32_t woff1 = SWIGLU ? woff0 : woff0 + 16 * wrow;
-    const uint32_t soff0 = (uint32_t)(wave * (SWIGLU ? 16 : 32) + l16) * ns * kSize;
-    const uint32_t soff1 = SWIGLU ? soff0 : soff0 + 16 * ns * kSize;
-
+    // the lane's row of scales, as bytes from the resource's base
+    const uint32_t sat0 = (uint32_t)(sfirst & 3) + (uint32_t)(wave * (SWIGLU ? 16 : 32) + l16) * srow;
+    const uint32_t sat1 = SWIGLU ? (uint32_t)((sfirst + sup) & 3) + (uint32_t)(wave * 16 + l16) * srow
+                                 : sat0 + 16 * srow;
     const auto fetch_x = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 256;
         // the offset within the row is below xrow (rows end inside a step)
@@ -156,23 +162,43 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
         load_lds16(wr0, to, past ? kRsrcPastEnd : woff0 + k);
         load_lds16(SWIGLU ? wr1 : wr0, to + 1024, past ? kRsrcPastEnd : woff1 + k);
     };
-    float scale[2][2][kParts];
+    uint32_t sdw[2][2][kDwords], carry[2];
+    const auto scale_dword = [&](int t, uint32_t byte) {     // of the lane's row, past its end too
+        const uint32_t off = (t ? sat1 : sat0) + byte;
+        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(SWIGLU && t ? sr1 : sr0, (int)(off & ~3u), 0, 0);
+    };
     const auto fetch_scale = [&](int par, int step) {
 #pragma unroll
-        for (int j = 0; j < kParts; ++j) {
-            const bool past = step * kParts + j >= ns;
-            const uint32_t k = (uint32_t)(step * kParts + j) * kSize;
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int off = (int)(past ? kRsrcPastEnd : (t ? soff1 : soff0) + k);
-                const __amdgpu_buffer_rsrc_t r = SWIGLU && t ? sr1 : sr0;
+            for (int d = 0; d < kDwords; ++d)
+                sdw[par][t][d] = scale_dword(t, (uint32_t)step * kStepBytes + (kStepBytes == 2 ? 0 : 4) + d * 4);
+    };
+    float scale[2][2][kParts];
+    const auto take_scale = [&](int par, int step) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t at = (t ? sat1 : sat0) + (uint32_t)step * kStepBytes;
+            uint32_t v[kDwords];
+            if constexpr (kStepBytes == 2) {
+                v[0] = sdw[par][t][0] >> ((at & 2) * 8);
+            } else {
+                v[0] = __builtin_amdgcn_alignbyte(sdw[par][t][0], carry[t], at & 3);
+                if constexpr (kDwords == 2)
+                    v[1] = __builtin_amdgcn_alignbyte(sdw[par][t][1], sdw[par][t][0], at & 3);
+                carry[t] = sdw[par][t][kDwords - 1];
+            }
+#pragma unroll
+            for (int j = 0; j < kParts; ++j) {
                 if constexpr (E2M1) {
-                    const uint32_t b = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
+                    const uint32_t b = (v[0] >> (8 * j)) & 255u;
                     scale[par][t][j] = __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
                 } else {
-                    const uint32_t b = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+                    const uint32_t b = (v[j / 2] >> (16 * (j & 1))) & 0xFFFFu;
                     scale[par][t][j] = F16 ? f16_lo(b) : bf16_lo(b);
                 }
+                // past the row's end its codes and rows of x are 0, and the scale must be finite
+                if (step * kParts + j >= s.in / (STEPS * 32)) scale[par][t][j] = 0.0f;
             }
         }
     };
@@ -200,17 +226,20 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const int f0 = l16 * 128 + ((g ^ (l16 & 7)) << 4);
     const int f1 = l16 * 128 + (((4 + g) ^ (l16 & 7)) << 4);
 
-    constexpr int kScales = 2 * kParts;
+    constexpr int kScales = 2 * kDwords;                     // loads of scales a step
     // Before step 0: its codes decoded, the codes of step 1 in registers, x(0), x(1) and the codes
     // of step 2 on their way.
     fetch_w(0);
     fetch_w(1);
+    carry[0] = kStepBytes == 2 ? 0u : scale_dword(0, 0);
+    carry[1] = kStepBytes == 2 ? 0u : scale_dword(1, 0);
     fetch_scale(0, 0);
     fetch_scale(1, 1);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) fetch_x(0, i);
     wait_loads<kXLoads>();
     read_raw(0);
+    take_scale(0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) decode_part(0, j);
     read_raw(1);
@@ -235,13 +264,15 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
             x[set][3] = *reinterpret_cast<const v4i_t*>(p + kW4TileM * 128 + f1);
         };
         read_x(0, 0);
+        take_scale(par ^ 1, step + 1);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             if (m + 1 < MT) read_x((m + 1) & 1, m + 1);
 #pragma unroll
             for (int i = 0; i < kXLoads; ++i)
                 if (i * MT / kXLoads == m) fetch_x(step + 2, i);
-            // (the place of step + 1's codes, which were read before this step's first rows)
+            // (the place of step + 1's codes, which were read before this step's first rows, and
+            // those have arrived by the time of the second rows)
             if (m == MT - 1) fetch_w(step + 3);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
