@@ -2,11 +2,13 @@
 //
 // A workgroup multiplies up to 128 rows of x with 256 weight rows, in steps of 128 elements;
 // wave w owns weight rows 32 * w + 0..31 (with SwiGLU 16 gate rows and the 16 up rows of the same
-// columns) and takes every row of x.  x (256 bytes a row and step) lies in a ring of three LDS
-// stages, a wave's codes (64 bytes a row and step) in a ring of two of its own; loads move both
-// there by themselves.  Each step decodes the codes of the next one to 16-bit floats in
-// registers, a quarter with each part of its own products, so that the conversions run
-// beside the matrix instructions.
+// columns) and takes every row of x.  x (256 bytes a row and step), a wave's codes (64 bytes a
+// row and step) and its scales lie in LDS rings, moved there by the loads themselves; the rings are
+// as deep as LDS allows, three steps for 128 rows, five for 32, where a step is short against the
+// memory's latency.  (No load goes to a register: the wait for it would be one for every load
+// before it too.)  Each step decodes the codes of the next one to 16-bit floats in registers, a
+// part with each part of its own products, so that the conversions run beside the
+// matrix instructions.
 //
 // x is the A operand (rows of the result) and the weights B (columns): lane l holds column
 // l % 16 and rows (l / 16) * 4 + 0..3, hence one scale per lane and column tile.
@@ -19,81 +21,78 @@ namespace {
 
 constexpr int kW4TileM = 128;
 constexpr int kW4TileN = 256;
-constexpr int kW4Ring = 3;
+constexpr int kW4LdsBytes = 163840;
 
+// Steps held in LDS by tiles of MT * 16 rows.
+constexpr int w4_ring(int mt) { return mt <= 2 ? 5 : mt <= 4 ? 4 : 3; }
+
+template <int MT>
 struct W4Stages {
-    char x[kW4Ring][2][kW4TileM * 128];         // [64 elements][row][128 bytes], swizzled
-    char w[kTileWaves][2][32 * 64];             // each wave's own weight rows, swizzled
+    char x[w4_ring(MT)][2][MT * 16 * 128];      // [64 elements][row][128 bytes], swizzled
+    char w[kTileWaves][w4_ring(MT)][32 * 64];   // each wave's own weight rows, swizzled
+    // dwords of scales: of each of the wave's rows the one a step's scales begin in, then the
+    // next; then (8 bytes of scales a step) the one after
+    uint32_t s[kTileWaves][w4_ring(MT)][128];
 };
 
 union W4Lds {
-    W4Stages st;
+    W4Stages<2> s2;
+    W4Stages<4> s4;
+    W4Stages<6> s6;
+    W4Stages<8> s8;
     TileTable table;
 };
+static_assert(sizeof(W4Lds) <= kW4LdsBytes, "LDS of a workgroup");
 
-// int4 codes as bf16 exactly, in the order 0 4 1 5 2 6 3 7: low code l of a pair of shorts.  The
-// sign-and-magnitude byte of code c (c = u - 16 for u > 7) is an E4M3 subnormal (or 2^-6 for
-// 8), worth c * 2^-9; the conversion multiplies by 2^9.
+// Four int4 codes as E4M3 bytes worth code * 2^-9 (subnormals, and 2^-6 for 8), from the codes' low three
+// bits and their sign bits moved to bit 0: negative codes become 0x88 - low3 = (low3 ^ 7) + 0x81.
 __device__ __forceinline__ uint32_t int4_bytes(uint32_t low3, uint32_t sign)
 {
-    // low3: bits 0-2 of each byte's code, sign: its bit 3 moved to bit 0.  Negative codes become
-    // 0x88 - low3 = (low3 ^ 7) + 0x81.
-    return (low3 ^ ((sign << 3) - sign)) + ((sign << 7) | sign);
+    const uint32_t seven = (sign << 2) | ((sign << 1) | sign);
+    return (low3 ^ seven) + ((sign << 7) | sign);
 }
 
-template <bool F16, bool E2M1, bool SCALED>
+// Eight codes of a dword as 16-bit floats exactly, in their order.  SURPLUS (int4 for bf16): instead
+// 136 + code, in the order 0 4 1 5 2 6 3 7, which takes a third of the instructions.
+template <bool F16, bool E2M1, bool SURPLUS>
 __device__ __forceinline__ v4i_t decode_tile(uint32_t w, float scale)
 {
     v4i_t r;
-    if constexpr (E2M1) {
-        const float m = SCALED ? scale : 1.0f;
-        if constexpr (F16) {
-            r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 0));
-            r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 1));
-            r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 2));
-            r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, m, 3));
-        } else {
-            r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 0));
-            r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 1));
-            r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 2));
-            r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, m, 3));
-        }
-        return r;
+    if constexpr (E2M1 && F16) {
+        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+    } else if constexpr (E2M1) {
+        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+    } else if constexpr (SURPLUS) {
+        r = decode<false, false>(w);
     } else if constexpr (F16) {
-        return decode<true, false>(w);          // order 0 4 1 5 2 6 3 7
+        const v4i_t p = decode<true, false>(w);              // 0 4, 1 5, 2 6, 3 7
+        r.x = (int)__builtin_amdgcn_perm((uint32_t)p.y, (uint32_t)p.x, 0x05040100u);
+        r.y = (int)__builtin_amdgcn_perm((uint32_t)p.w, (uint32_t)p.z, 0x05040100u);
+        r.z = (int)__builtin_amdgcn_perm((uint32_t)p.y, (uint32_t)p.x, 0x07060302u);
+        r.w = (int)__builtin_amdgcn_perm((uint32_t)p.w, (uint32_t)p.z, 0x07060302u);
     } else {
         const uint32_t v = w >> 4;
         const uint32_t even = int4_bytes(w & 0x07070707u, (w >> 3) & 0x01010101u);   // 0 2 4 6
         const uint32_t odd = int4_bytes(v & 0x07070707u, (v >> 3) & 0x01010101u);    // 1 3 5 7
-        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, false));
-        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, false));
-        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, true));
-        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, true));
-        return r;                               // order 0 2 1 3 4 6 5 7
+        const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u);           // 0 1 2 3
+        const uint32_t hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);           // 4 5 6 7
+        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
+        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
+        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
+        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
     }
-}
-
-// x in the order of the decoded codes.
-template <bool F16, bool E2M1>
-__device__ __forceinline__ v4i_t tile_order(v4i_t x)
-{
-    if constexpr (E2M1) {
-        return x;
-    } else if constexpr (F16) {
-        return pair_order(x);
-    } else {
-        v4i_t r;
-        r.x = (int)__builtin_amdgcn_perm((uint32_t)x.y, (uint32_t)x.x, 0x05040100u);
-        r.y = (int)__builtin_amdgcn_perm((uint32_t)x.y, (uint32_t)x.x, 0x07060302u);
-        r.z = (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.z, 0x05040100u);
-        r.w = (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.z, 0x07060302u);
-        return r;
-    }
+    return r;
 }
 
 template <bool F16, bool E2M1, int STEPS, int MT, bool SWIGLU>
 __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const MatmulArgs& a,
-                                                const Tile& tile, W4Stages& lds)
+                                                const Tile& tile, W4Stages<MT>& lds)
 {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -109,22 +108,25 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const __amdgpu_buffer_rsrc_t wr1 = make_rsrc(wbase + (size_t)half * wrow, (uint32_t)left * wrow);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(
         static_cast<const char*>(a.x) + (size_t)tile.row0 * xrow, (uint32_t)tile.rows * xrow);
-    // Scales are read as whole dwords (the tensor begins at one, rows begin anywhere): a step's
-    // scales of a row lie in the last dword of the step before and the kDwords loaded for it.
+    // Scales are read as whole dwords (the tensor begins at one, rows begin anywhere).
     constexpr int kSize = E2M1 ? 1 : 2;                      // bytes of a scale
     constexpr int kParts = 4 / STEPS;                        // scales of a row and step
     constexpr int kStepBytes = kParts * kSize;               // 2, 4 or 8
-    constexpr int kDwords = kStepBytes == 8 ? 2 : 1;
+    constexpr int kSLoads = kStepBytes == 8 ? 2 : 1;
     const uint32_t srow = (uint32_t)(s.in / (STEPS * 32)) * kSize;      // bytes of a row
-    const size_t sfirst = first * srow, sup = (size_t)half * srow;
-    const char* sbase = static_cast<const char*>(a.w_scales);
-    const auto scale_rsrc = [&](size_t at) {
-        return make_rsrc(sbase + (at & ~(size_t)3), ((uint32_t)(at & 3) + (uint32_t)left * srow + 3) & ~3u);
-    };
-    const __amdgpu_buffer_rsrc_t sr0 = scale_rsrc(sfirst);
-    const __amdgpu_buffer_rsrc_t sr1 = scale_rsrc(sfirst + sup);
+    const size_t sfirst = first * srow;
+    const __amdgpu_buffer_rsrc_t sr =
+        make_rsrc(static_cast<const char*>(a.w_scales) + (sfirst & ~(size_t)3),
+                  ((uint32_t)(sfirst & 3) + (uint32_t)(SWIGLU ? half + left : left) * srow + 3) & ~3u);
     // bf16 holds every E2M1 code times a power of two, so its scale enters with the conversion.
     constexpr bool kFolded = E2M1 && !F16;
+    // int4 for bf16: with few rows the conversions bound the tile, and the surplus 136 * sum(x) of the
+    // short decoding leaves through the sums' start value, a product with constant -136 shared by
+    // both column tiles (half as many matrix instructions again, which are idle here; with many rows
+    // they are not).
+    constexpr bool kSurplus = !E2M1 && !F16 && MT == 2;
+    const int neg136 = (int)0xC308C308u;                    // bf16 -136, twice
+    const v4i_t minus = {neg136, neg136, neg136, neg136};
 
     const int lr = lane >> 3;
     const uint32_t lk = (uint32_t)((lane & 7) ^ lr) * 16;
@@ -135,7 +137,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     for (int i = 0; i < kXLoads; ++i) {
         const int b = wave + i * kTileWaves;                 // block of 8 rows: half b / (2 MT)
         const int hb = b / (2 * MT), rb = b % (2 * MT);
-        xto[i] = hb * kW4TileM * 128 + rb * 1024;
+        xto[i] = hb * MT * 2048 + rb * 1024;
         xoff[i] = (uint32_t)(rb * 8 + lr) * xrow + hb * 128 + lk;
     }
     // Codes: a load moves 16 rows of 64 bytes; lane i brings row i / 4 the 16 bytes of position
@@ -144,49 +146,62 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const uint32_t wk = (uint32_t)((lane & 3) ^ ((wr >> 2) & 3)) * 16;
     const uint32_t woff0 = (uint32_t)(wave * (SWIGLU ? 16 : 32) + wr) * wrow + wk;
     const uint32_t woff1 = SWIGLU ? woff0 : woff0 + 16 * wrow;
-    // the lane's row of scales, as bytes from the resource's base
-    const uint32_t sat0 = (uint32_t)(sfirst & 3) + (uint32_t)(wave * (SWIGLU ? 16 : 32) + l16) * srow;
-    const uint32_t sat1 = SWIGLU ? (uint32_t)((sfirst + sup) & 3) + (uint32_t)(wave * 16 + l16) * srow
-                                 : sat0 + 16 * srow;
+    // Byte of the resource where the scales of the wave's row r (0..31) begin.
+    const auto scale_at = [&](int r) {
+        const uint32_t row = SWIGLU ? (uint32_t)(wave * 16 + (r & 15)) + (r & 16 ? (uint32_t)half : 0u)
+                                    : (uint32_t)(wave * 32 + r);
+        return (uint32_t)(sfirst & 3) + row * srow;
+    };
+    const uint32_t sfetch = scale_at(lane & 31);
+    const uint32_t suse[2] = {scale_at(l16), scale_at(16 + l16)};
+
+    constexpr int kRing = w4_ring(MT);
     const auto fetch_x = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 256;
         // the offset within the row is below xrow (rows end inside a step)
         const int b = wave + i * kTileWaves;
         const bool past = k + (b / (2 * MT)) * 128 + lk >= xrow;
-        load_lds16(xr, lds.x[step % kW4Ring][0] + xto[i], past ? kRsrcPastEnd : xoff[i] + k);
+        load_lds16(xr, lds.x[step % kRing][0] + xto[i], past ? kRsrcPastEnd : xoff[i] + k);
     };
     const auto fetch_w = [&](int step) {
         const uint32_t k = (uint32_t)step * 64;
         const bool past = k + wk >= wrow;
-        char* to = lds.w[wave][step & 1];
+        char* to = lds.w[wave][step % kRing];
         load_lds16(wr0, to, past ? kRsrcPastEnd : woff0 + k);
         load_lds16(SWIGLU ? wr1 : wr0, to + 1024, past ? kRsrcPastEnd : woff1 + k);
+        const uint32_t d = (sfetch + (uint32_t)step * kStepBytes) & ~3u;
+        char* st = reinterpret_cast<char*>(lds.s[wave][step % kRing]);
+        load_lds4(sr, st, d + (lane >> 5) * 4);
+        if constexpr (kSLoads == 2) load_lds4(sr, st + 256, d + 8);
     };
-    uint32_t sdw[2][2][kDwords], carry[2];
-    const auto scale_dword = [&](int t, uint32_t byte) {     // of the lane's row, past its end too
-        const uint32_t off = (t ? sat1 : sat0) + byte;
-        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(SWIGLU && t ? sr1 : sr0, (int)(off & ~3u), 0, 0);
-    };
-    const auto fetch_scale = [&](int par, int step) {
+
+    // The codes and scales of a step, from LDS: of row l16 (t = 0) and row 16 + l16, the dword g of
+    // chunk j for 32-element step j.
+    uint32_t raw[2][4], sraw[2][3];
+    const auto read_raw = [&](int step) {
+        const char* wl = lds.w[wave][step % kRing] + l16 * 64 + g * 4;
+        const uint32_t* st = lds.s[wave][step % kRing] + l16;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
-            for (int d = 0; d < kDwords; ++d)
-                sdw[par][t][d] = scale_dword(t, (uint32_t)step * kStepBytes + (kStepBytes == 2 ? 0 : 4) + d * 4);
+            for (int j = 0; j < 4; ++j)
+                raw[t][j] = *reinterpret_cast<const uint32_t*>(wl + t * 1024 + ((j ^ (l16 >> 2)) << 4));
+            sraw[t][0] = st[t * 16];
+            if (kStepBytes >= 4) sraw[t][1] = st[32 + t * 16];
+            if (kStepBytes == 8) sraw[t][2] = st[64 + t * 16];
+        }
     };
     float scale[2][2][kParts];
     const auto take_scale = [&](int par, int step) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t at = (t ? sat1 : sat0) + (uint32_t)step * kStepBytes;
-            uint32_t v[kDwords];
+            const uint32_t at = suse[t] + (uint32_t)step * kStepBytes;
+            uint32_t v[2];
             if constexpr (kStepBytes == 2) {
-                v[0] = sdw[par][t][0] >> ((at & 2) * 8);
+                v[0] = sraw[t][0] >> ((at & 2) * 8);
             } else {
-                v[0] = __builtin_amdgcn_alignbyte(sdw[par][t][0], carry[t], at & 3);
-                if constexpr (kDwords == 2)
-                    v[1] = __builtin_amdgcn_alignbyte(sdw[par][t][1], sdw[par][t][0], at & 3);
-                carry[t] = sdw[par][t][kDwords - 1];
+                v[0] = __builtin_amdgcn_alignbyte(sraw[t][1], sraw[t][0], at & 3);
+                if constexpr (kStepBytes == 8) v[1] = __builtin_amdgcn_alignbyte(sraw[t][2], sraw[t][1], at & 3);
             }
 #pragma unroll
             for (int j = 0; j < kParts; ++j) {
@@ -202,22 +217,11 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
             }
         }
     };
-
-    // The lane's dword of step j of row l16: chunk j, dword g.
-    uint32_t raw[2][4];
-    const auto read_raw = [&](int step) {
-        const char* wl = lds.w[wave][step & 1] + l16 * 64 + g * 4;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                raw[t][j] = *reinterpret_cast<const uint32_t*>(wl + t * 1024 + ((j ^ (l16 >> 2)) << 4));
-    };
     v4i_t w[2][2][4];
     const auto decode_part = [&](int par, int j) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            w[par][t][j] = decode_tile<F16, E2M1, kFolded>(raw[t][j], kFolded ? scale[par][t][j / STEPS] : 1.0f);
+            w[par][t][j] = decode_tile<F16, E2M1, kSurplus>(raw[t][j], kFolded ? scale[par][t][j / STEPS] : 1.0f);
     };
 
     v4f_t acc[MT][2];
@@ -226,42 +230,43 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const int f0 = l16 * 128 + ((g ^ (l16 & 7)) << 4);
     const int f1 = l16 * 128 + (((4 + g) ^ (l16 & 7)) << 4);
 
-    constexpr int kScales = 2 * kDwords;                     // loads of scales a step
-    // Before step 0: its codes decoded, the codes of step 1 in registers, x(0), x(1) and the codes
-    // of step 2 on their way.
+    // Before step 0: its codes decoded, the codes of step 1 in registers, every stage but one of x
+    // and all places of codes filled or on their way.  In step k the place of x(k - 1) takes x(k +
+    // ring - 1), and that of the codes of k + 1 (in registers) those of k + 1 + ring.
+    constexpr int kStep = kXLoads + 2 + kSLoads;             // loads of a step
+    const auto all_x = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) fetch_x(step, i);
+    };
     fetch_w(0);
     fetch_w(1);
-    carry[0] = kStepBytes == 2 ? 0u : scale_dword(0, 0);
-    carry[1] = kStepBytes == 2 ? 0u : scale_dword(1, 0);
-    fetch_scale(0, 0);
-    fetch_scale(1, 1);
+    all_x(0);
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) fetch_x(0, i);
-    wait_loads<kXLoads>();
+    for (int i = 2; i < kRing; ++i) {
+        fetch_w(i);
+        all_x(i - 1);
+    }
+    wait_loads<kXLoads + (kRing - 2) * kStep>();
     read_raw(0);
     take_scale(0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) decode_part(0, j);
     read_raw(1);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < kXLoads; ++i) fetch_x(1, i);
-    fetch_w(2);
-    wait_loads<kXLoads + 2>();
+    fetch_w(kRing);
 
     const auto one = [&](int par, int step) {
-        // x(step): issued after it are the codes of step + 1, then scales, x(step + 1) and
-        // the codes of step + 2
-        wait_loads<2 + kScales + kXLoads + 2>();
+        // x(step): issued after it are the rest of its step's loads, and ring - 2 whole steps
+        wait_loads<2 + kSLoads + (kRing - 2) * kStep>();
         __builtin_amdgcn_s_barrier();
-        const char* xl = lds.x[step % kW4Ring][0];
+        const char* xl = lds.x[step % kRing][0];
         v4i_t x[2][4];
         const auto read_x = [&](int set, int m) {
             const char* p = xl + m * 2048;
             x[set][0] = *reinterpret_cast<const v4i_t*>(p + f0);
             x[set][1] = *reinterpret_cast<const v4i_t*>(p + f1);
-            x[set][2] = *reinterpret_cast<const v4i_t*>(p + kW4TileM * 128 + f0);
-            x[set][3] = *reinterpret_cast<const v4i_t*>(p + kW4TileM * 128 + f1);
+            x[set][2] = *reinterpret_cast<const v4i_t*>(p + MT * 2048 + f0);
+            x[set][3] = *reinterpret_cast<const v4i_t*>(p + MT * 2048 + f1);
         };
         read_x(0, 0);
         take_scale(par ^ 1, step + 1);
@@ -270,16 +275,17 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
             if (m + 1 < MT) read_x((m + 1) & 1, m + 1);
 #pragma unroll
             for (int i = 0; i < kXLoads; ++i)
-                if (i * MT / kXLoads == m) fetch_x(step + 2, i);
+                if (i * MT / kXLoads == m) fetch_x(step + kRing - 1, i);
             // (the place of step + 1's codes, which were read before this step's first rows, and
             // those have arrived by the time of the second rows)
-            if (m == MT - 1) fetch_w(step + 3);
+            if (m == MT - 1) fetch_w(step + 1 + kRing);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j * MT / 4 == m) decode_part(par ^ 1, j);
+            if constexpr (kSurplus)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[m & 1][j] = tile_order<F16, E2M1>(x[m & 1][j]);
+                for (int j = 0; j < 4; ++j) x[m & 1][j] = pair_order(x[m & 1][j]);
             if constexpr (kFolded) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -289,7 +295,12 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
                 v4f_t sum[kParts][2];
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) {
-                    sum[p][0] = sum[p][1] = v4f_t{0, 0, 0, 0};
+                    sum[p][0] = v4f_t{0, 0, 0, 0};
+                    if constexpr (kSurplus)
+#pragma unroll
+                        for (int j = 0; j < STEPS; ++j)
+                            sum[p][0] = mma16<F16>(x[m & 1][p * STEPS + j], minus, sum[p][0]);
+                    sum[p][1] = sum[p][0];
 #pragma unroll
                     for (int j = 0; j < STEPS; ++j)
 #pragma unroll
@@ -308,11 +319,9 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        // The codes of step + 2 (after them: this step's x(step + 2) and codes of step + 3), and
-        // the scales of step + 2 in place of this step's.
-        wait_loads<kXLoads + 2>();
+        // the codes of step + 2: issued after them are ring - 1 whole steps
+        wait_loads<(kRing - 1) * kStep>();
         read_raw(step + 2);
-        fetch_scale(par, step + 2);
     };
     int step = 0;
     for (; step + 2 <= steps; step += 2) {
@@ -348,10 +357,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void w4_tile_kernel(MatmulShape s,
                                                                lds.table, &t))
         return;
     switch ((t.rows + 31) / 32) {
-    case 1: w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU>(s, a, t, lds.st); break;
-    case 2: w4_tile_product<F16, E2M1, STEPS, 4, SWIGLU>(s, a, t, lds.st); break;
-    case 3: w4_tile_product<F16, E2M1, STEPS, 6, SWIGLU>(s, a, t, lds.st); break;
-    default: w4_tile_product<F16, E2M1, STEPS, 8, SWIGLU>(s, a, t, lds.st); break;
+    case 1: w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU>(s, a, t, lds.s2); break;
+    case 2: w4_tile_product<F16, E2M1, STEPS, 4, SWIGLU>(s, a, t, lds.s4); break;
+    case 3: w4_tile_product<F16, E2M1, STEPS, 6, SWIGLU>(s, a, t, lds.s6); break;
+    default: w4_tile_product<F16, E2M1, STEPS, 8, SWIGLU>(s, a, t, lds.s8); break;
     }
 }
 
