@@ -48,7 +48,7 @@ inline bool tiles_suffice(const MatmulShape& s, int height, int cols)
 // most ROWS rows as possible, all of nearly the same height (a multiple of 32).  Consecutive
 // tiles go to one XCD (workgroups are dealt to the XCDs in turn), so that the tiles of an expert
 // share its weights and its rows in that XCD's L2.
-template <int ROWS, int COLS>
+template <int ROWS, int COLS, int WAVES = kTileWaves>
 __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs& a, int columns,
                                           TileTable& table, Tile* out)
 {
@@ -56,19 +56,19 @@ __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = threadIdx.x / kWave;
 
-    // experts 2 * thread and 2 * thread + 1
-    const int e0 = threadIdx.x * 2;
-    int t0 = 0, t1 = 0;
-    if (e0 < s.E) {
-        const int b = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 - 1);
-        const int m = expert_end(s, a.ep_recv_count, a.recv_offsets, e0);
-        t0 = m > b ? (m - b + ROWS - 1) / ROWS * nt : 0;
-        if (e0 + 1 < s.E) {
-            const int f = expert_end(s, a.ep_recv_count, a.recv_offsets, e0 + 1);
-            t1 = f > m ? (f - m + ROWS - 1) / ROWS * nt : 0;
-        }
+    // kPer experts per thread
+    constexpr int kPer = kMaxExperts / (WAVES * kWave);
+    const int e0 = threadIdx.x * kPer;
+    int tiles[kPer];
+    int sum = 0;
+    int from = e0 < s.E ? expert_end(s, a.ep_recv_count, a.recv_offsets, e0 - 1) : 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int end = e0 + i < s.E ? expert_end(s, a.ep_recv_count, a.recv_offsets, e0 + i) : from;
+        tiles[i] = end > from ? (end - from + ROWS - 1) / ROWS * nt : 0;
+        sum += tiles[i];
+        from = end;
     }
-    int sum = t0 + t1;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
         const int o = __shfl_up(sum, off, kWave);
@@ -77,8 +77,11 @@ __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs
     if (lane == kWave - 1) table.wave_sum[wave] = sum;
     __syncthreads();
     for (int w = 0; w < wave; ++w) sum += table.wave_sum[w];
-    if (e0 < s.E) table.cum[e0 + 1] = sum - t1;
-    if (e0 + 1 < s.E) table.cum[e0 + 2] = sum;
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i) {
+        if (e0 + i < s.E) table.cum[e0 + i + 1] = sum;
+        sum -= tiles[i];
+    }
     if (threadIdx.x == 0) table.cum[0] = 0;
     __syncthreads();
 

@@ -169,8 +169,12 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_kernel(MatmulShape s, Mat
 template <bool F16>
 hipError_t launch_token(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
+    // few rows per expert: the smaller tiles, where they are enough
+    const int64_t active = s.rows < s.E ? s.rows : s.E;
+    if (s.rows <= kW4SmallM * active && tiles_suffice(s, kW4SmallM, s.swiglu ? kW4SmallN / 2 : kW4SmallN))
+        return launch_w4_tiles<F16>(s, a, true, stream);
     if (tiles_suffice(s, kW4TileM, s.swiglu ? kW4TileN / 2 : kW4TileN))
-        return launch_w4_tiles<F16>(s, a, stream);
+        return launch_w4_tiles<F16>(s, a, false, stream);
     const int half = s.swiglu ? s.out / 2 : s.out;
     const int per = s.swiglu ? 16 : 32;
     int64_t z = (s.rows / s.E + 63) / 64;

@@ -1,7 +1,7 @@
 // grouped_matmul_w4_tile.h -- 4-bit products for many rows per expert.
 //
-// A workgroup multiplies up to 128 rows of x with 256 weight rows, in steps of 128 elements;
-// wave w owns weight rows 32 * w + 0..31 (with SwiGLU 16 gate rows and the 16 up rows of the same
+// A workgroup of eight waves multiplies up to 128 rows of x with 256 weight rows, or one of four
+// waves up to 32 rows with 128, in steps of 128 elements; wave w owns weight rows 32 * w + 0..31 (with SwiGLU 16 gate rows and the 16 up rows of the same
 // columns) and takes every row of x.  x (256 bytes a row and step), a wave's codes (64 bytes a
 // row and step) and its scales lie in LDS rings, moved there by the loads themselves; the rings are
 // as deep as LDS allows, three steps for 128 rows, five for 32, where a step is short against the
@@ -19,30 +19,37 @@
 namespace moe_dc {
 namespace {
 
-constexpr int kW4TileM = 128;
+constexpr int kW4TileM = 128;                   // rows of x and weight rows of a workgroup
 constexpr int kW4TileN = 256;
+constexpr int kW4SmallM = 32;                   // and of the smaller one, two to a CU
+constexpr int kW4SmallN = 128;
+constexpr int kW4SmallWaves = 4;
 constexpr int kW4LdsBytes = 163840;
 
 // Steps held in LDS by tiles of MT * 16 rows.
-constexpr int w4_ring(int mt) { return mt <= 2 ? 5 : mt <= 4 ? 4 : 3; }
+constexpr int w4_ring(int mt) { return mt <= 4 ? 4 : 3; }
 
-template <int MT>
+template <int MT, int WAVES>
 struct W4Stages {
     char x[w4_ring(MT)][2][MT * 16 * 128];      // [64 elements][row][128 bytes], swizzled
-    char w[kTileWaves][w4_ring(MT)][32 * 64];   // each wave's own weight rows, swizzled
+    char w[WAVES][w4_ring(MT)][32 * 64];        // each wave's own weight rows, swizzled
     // dwords of scales: of each of the wave's rows the one a step's scales begin in, then the
     // next; then (8 bytes of scales a step) the one after
-    uint32_t s[kTileWaves][w4_ring(MT)][128];
+    uint32_t s[WAVES][w4_ring(MT)][128];
 };
 
 union W4Lds {
-    W4Stages<2> s2;
-    W4Stages<4> s4;
-    W4Stages<6> s6;
-    W4Stages<8> s8;
+    W4Stages<2, kTileWaves> s2;
+    W4Stages<4, kTileWaves> s4;
+    W4Stages<6, kTileWaves> s6;
+    W4Stages<8, kTileWaves> s8;
     TileTable table;
 };
-static_assert(sizeof(W4Lds) <= kW4LdsBytes, "LDS of a workgroup");
+union W4SmallLds {
+    W4Stages<2, kW4SmallWaves> st;
+    TileTable table;
+};
+static_assert(sizeof(W4Lds) <= kW4LdsBytes && 2 * sizeof(W4SmallLds) <= kW4LdsBytes, "LDS of a CU");
 
 // Four int4 codes as E4M3 bytes worth code * 2^-9 (subnormals, and 2^-6 for 8), from the codes' low three
 // bits and their sign bits moved to bit 0: negative codes become 0x88 - low3 = (low3 ^ 7) + 0x81.
@@ -90,9 +97,9 @@ __device__ __forceinline__ v4i_t decode_tile(uint32_t w, float scale)
     return r;
 }
 
-template <bool F16, bool E2M1, int STEPS, int MT, bool SWIGLU>
+template <bool F16, bool E2M1, int STEPS, int MT, bool SWIGLU, int WAVES>
 __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const MatmulArgs& a,
-                                                const Tile& tile, W4Stages<MT>& lds)
+                                                const Tile& tile, W4Stages<MT, WAVES>& lds)
 {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -100,7 +107,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const uint32_t xrow = (uint32_t)s.in * 2, wrow = (uint32_t)s.in / 2;
     const int steps = (s.in + 127) / 128;
     const int half = SWIGLU ? s.out / 2 : s.out;
-    constexpr int kCols = SWIGLU ? kW4TileN / 2 : kW4TileN;
+    constexpr int kCols = SWIGLU ? WAVES * 16 : WAVES * 32;
     const int left = half - tile.n0 < kCols ? half - tile.n0 : kCols;
     const size_t first = (size_t)tile.e * s.out + tile.n0;
     const char* wbase = static_cast<const char*>(a.w) + first * wrow;
@@ -130,12 +137,12 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
 
     const int lr = lane >> 3;
     const uint32_t lk = (uint32_t)((lane & 7) ^ lr) * 16;
-    constexpr int kXLoads = MT / 2;                          // 2 halves of 2 * MT blocks, 8 waves
+    constexpr int kXLoads = 4 * MT / WAVES;                  // 2 halves of 2 * MT blocks of 8 rows
     uint32_t xoff[kXLoads];
     int xto[kXLoads];
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
-        const int b = wave + i * kTileWaves;                 // block of 8 rows: half b / (2 MT)
+        const int b = wave + i * WAVES;                 // block of 8 rows: half b / (2 MT)
         const int hb = b / (2 * MT), rb = b % (2 * MT);
         xto[i] = hb * MT * 2048 + rb * 1024;
         xoff[i] = (uint32_t)(rb * 8 + lr) * xrow + hb * 128 + lk;
@@ -159,7 +166,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const auto fetch_x = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 256;
         // the offset within the row is below xrow (rows end inside a step)
-        const int b = wave + i * kTileWaves;
+        const int b = wave + i * WAVES;
         const bool past = k + (b / (2 * MT)) * 128 + lk >= xrow;
         load_lds16(xr, lds.x[step % kRing][0] + xto[i], past ? kRsrcPastEnd : xoff[i] + k);
     };
@@ -357,31 +364,48 @@ __global__ __launch_bounds__(kTileThreads, 2) void w4_tile_kernel(MatmulShape s,
                                                                lds.table, &t))
         return;
     switch ((t.rows + 31) / 32) {
-    case 1: w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU>(s, a, t, lds.s2); break;
-    case 2: w4_tile_product<F16, E2M1, STEPS, 4, SWIGLU>(s, a, t, lds.s4); break;
-    case 3: w4_tile_product<F16, E2M1, STEPS, 6, SWIGLU>(s, a, t, lds.s6); break;
-    default: w4_tile_product<F16, E2M1, STEPS, 8, SWIGLU>(s, a, t, lds.s8); break;
+    case 1: w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU, kTileWaves>(s, a, t, lds.s2); break;
+    case 2: w4_tile_product<F16, E2M1, STEPS, 4, SWIGLU, kTileWaves>(s, a, t, lds.s4); break;
+    case 3: w4_tile_product<F16, E2M1, STEPS, 6, SWIGLU, kTileWaves>(s, a, t, lds.s6); break;
+    default: w4_tile_product<F16, E2M1, STEPS, 8, SWIGLU, kTileWaves>(s, a, t, lds.s8); break;
     }
 }
 
-template <bool F16, bool E2M1, int STEPS>
-hipError_t launch_w4_tile(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+template <bool F16, bool E2M1, int STEPS, bool SWIGLU>
+__global__ __launch_bounds__(kW4SmallWaves * kWave, 2) void w4_small_kernel(MatmulShape s, MatmulArgs a)
 {
-    const dim3 grid(tile_grid(s, kW4TileM, s.swiglu ? kW4TileN / 2 : kW4TileN));
-    if (s.swiglu)
+    __shared__ W4SmallLds lds;
+    Tile t;
+    if (find_tile<kW4SmallM, SWIGLU ? kW4SmallN / 2 : kW4SmallN, kW4SmallWaves>(
+            s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t))
+        w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU, kW4SmallWaves>(s, a, t, lds.st);
+}
+
+template <bool F16, bool E2M1, int STEPS>
+hipError_t launch_w4_tile(const MatmulShape& s, const MatmulArgs& a, bool small, hipStream_t stream)
+{
+    const int rows = small ? kW4SmallM : kW4TileM, n = small ? kW4SmallN : kW4TileN;
+    const dim3 grid(tile_grid(s, rows, s.swiglu ? n / 2 : n));
+    if (small) {
+        if (s.swiglu)
+            w4_small_kernel<F16, E2M1, STEPS, true><<<grid, kW4SmallWaves * kWave, 0, stream>>>(s, a);
+        else
+            w4_small_kernel<F16, E2M1, STEPS, false><<<grid, kW4SmallWaves * kWave, 0, stream>>>(s, a);
+    } else if (s.swiglu) {
         w4_tile_kernel<F16, E2M1, STEPS, true><<<grid, kTileThreads, 0, stream>>>(s, a);
-    else
+    } else {
         w4_tile_kernel<F16, E2M1, STEPS, false><<<grid, kTileThreads, 0, stream>>>(s, a);
+    }
     return hipGetLastError();
 }
 
 template <bool F16>
-hipError_t launch_w4_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+hipError_t launch_w4_tiles(const MatmulShape& s, const MatmulArgs& a, bool small, hipStream_t stream)
 {
-    if (s.w4 == MOE_W4_E2M1) return launch_w4_tile<F16, true, 1>(s, a, stream);
-    if (s.group == 32) return launch_w4_tile<F16, false, 1>(s, a, stream);
-    if (s.group == 64) return launch_w4_tile<F16, false, 2>(s, a, stream);
-    return launch_w4_tile<F16, false, 4>(s, a, stream);
+    if (s.w4 == MOE_W4_E2M1) return launch_w4_tile<F16, true, 1>(s, a, small, stream);
+    if (s.group == 32) return launch_w4_tile<F16, false, 1>(s, a, small, stream);
+    if (s.group == 64) return launch_w4_tile<F16, false, 2>(s, a, small, stream);
+    return launch_w4_tile<F16, false, 4>(s, a, small, stream);
 }
 
 }  // namespace

@@ -272,6 +272,26 @@ def test_4bit_tiles(token, weight, group, groups, N, swiglu):
     _run_w4(token, weight, group, 4, RAGGED, group * groups, N, swiglu, seed=groups)
 
 
+# A few rows per expert on many experts: the tiles of one decode step (one expert has a prompt's).
+FEW = [1, 0, 2, 33, 16, 17, 0, 5, 1, 1, 31, 32, 3, 70, 0, 8, 4, 12, 15, 64, 2, 2, 0, 9, 24, 25, 6, 7, 1, 0, 11, 130]
+
+
+@pytest.mark.parametrize("token", ["bf16", "f16"])
+@pytest.mark.parametrize("weight,group", W4)
+@pytest.mark.parametrize("groups,N,swiglu", [
+    (1, 1600, False), (2, 1666, True), (5, 1541, False), (9, 1602, True), (24, 1537, False),
+])
+def test_4bit_few_rows(token, weight, group, groups, N, swiglu):
+    _run_w4(token, weight, group, 4, FEW, group * groups, N, swiglu, seed=groups)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("steps,N,swiglu", [(0, 1600, False), (3, 1666, True), (30, 1541, False)])
+def test_product_few_rows(kind, steps, N, swiglu):
+    step = 128 if kind.startswith("mx") else 24 if kind in ("bf16", "f16") else 48
+    _run_product(kind, 4, FEW, step * (steps + 1), N, swiglu, seed=steps)
+
+
 def test_4bit_every_code():
     """Each code alone against a one-hot row gives code * scale exactly."""
     for token, weight, group in (("bf16", "int4", 32), ("f16", "int4", 32), ("bf16", "e2m1", 32),
