@@ -46,7 +46,8 @@ union W4Lds {
     TileTable table;
 };
 union W4SmallLds {
-    W4Stages<2, kW4SmallWaves> st;
+    W4Stages<1, kW4SmallWaves> s1;
+    W4Stages<2, kW4SmallWaves> s2;
     TileTable table;
 };
 static_assert(sizeof(W4Lds) <= kW4LdsBytes && 2 * sizeof(W4SmallLds) <= kW4LdsBytes, "LDS of a CU");
@@ -131,7 +132,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     // short decoding leaves through the sums' start value, a product with constant -136 shared by
     // both column tiles (half as many matrix instructions again, which are idle here; with many rows
     // they are not).
-    constexpr bool kSurplus = !E2M1 && !F16 && MT == 2;
+    constexpr bool kSurplus = !E2M1 && !F16 && MT <= 2;
     const int neg136 = (int)0xC308C308u;                    // bf16 -136, twice
     const v4i_t minus = {neg136, neg136, neg136, neg136};
 
@@ -285,7 +286,10 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
                 if (i * MT / kXLoads == m) fetch_x(step + kRing - 1, i);
             // (the place of step + 1's codes, which were read before this step's first rows, and
             // those have arrived by the time of the second rows)
-            if (m == MT - 1) fetch_w(step + 1 + kRing);
+            if (m == MT - 1) {
+                if (MT == 1) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                fetch_w(step + 1 + kRing);
+            }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -376,9 +380,13 @@ __global__ __launch_bounds__(kW4SmallWaves * kWave, 2) void w4_small_kernel(Matm
 {
     __shared__ W4SmallLds lds;
     Tile t;
-    if (find_tile<kW4SmallM, SWIGLU ? kW4SmallN / 2 : kW4SmallN, kW4SmallWaves>(
+    if (!find_tile<kW4SmallM, SWIGLU ? kW4SmallN / 2 : kW4SmallN, kW4SmallWaves>(
             s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t))
-        w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU, kW4SmallWaves>(s, a, t, lds.st);
+        return;
+    if (t.rows <= 16)
+        w4_tile_product<F16, E2M1, STEPS, 1, SWIGLU, kW4SmallWaves>(s, a, t, lds.s1);
+    else
+        w4_tile_product<F16, E2M1, STEPS, 2, SWIGLU, kW4SmallWaves>(s, a, t, lds.s2);
 }
 
 template <bool F16, bool E2M1, int STEPS>
