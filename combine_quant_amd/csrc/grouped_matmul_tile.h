@@ -24,7 +24,6 @@ struct TileStages {
 // The table is done with before the first stage is filled.
 template <int TYPE>
 union TileLds {
-    char x[kTileRing][kTileM<TYPE> * 128];
     TileStages<TYPE> st;
     TileTable table;
 };
