@@ -44,13 +44,25 @@ inline bool tiles_suffice(const MatmulShape& s, int height, int cols)
     return active * ((s.rows / active + height - 1) / height) * ((half + cols - 1) / cols) >= kMinTiles;
 }
 
+// The place of this workgroup among `total` tiles, or -1.  Workgroup b runs on XCD b % 8.  Each XCD takes
+// 32 consecutive tiles (one per CU) at a time, so that the tiles of an expert share its weights and its rows
+// in that XCD's L2 while experts with many and with few rows are spread over the XCDs; the last tiles
+// are shared out evenly.
+__device__ __forceinline__ int tile_of_workgroup(int total)
+{
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    const int full = total / 256, rest = total % 256;
+    if (slot < full * 32) return (slot / 32) * 256 + xcd * 32 + slot % 32;
+    const int share = (rest + 7) / 8, r = slot - full * 32;
+    return r < share && xcd * share + r < rest ? full * 256 + xcd * share + r : -1;
+}
+
 // The workgroup's tile.  The ragged counts live on the device, so every workgroup counts the tiles of
 // all experts, then finds its own: for up to 128 experts each wave by itself (lane l counts
 // experts l * per + 0..per - 1; 71 -> 65 us at 32 experts, 512 rows x 2048 x 7168 int4), for more the
 // workgroup's threads together through LDS (228 -> 201 us at 1024 experts, 4096 rows x 2048 x 512
 // E4M3).  An expert's rows are cut into as few tiles of at most ROWS rows as possible, all of nearly the
-// same height (a multiple of 32).  Consecutive tiles go to one XCD (workgroups are dealt to the XCDs in
-// turn), so that the tiles of an expert share its weights and its rows in that XCD's L2.
+// same height (a multiple of 32).
 template <int ROWS, int COLS, int WAVES = kTileWaves>
 __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs& a, int columns,
                                           TileTable& table, Tile* out)
@@ -82,10 +94,8 @@ __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs
             if (lane >= off) upto += o;
         }
         const int total = lane_value(upto, kWave - 1);
-        const int chunk = (total + 7) / 8;
-        const int slot = blockIdx.x >> 3;
-        const int tile = (int)(blockIdx.x & 7) * chunk + slot;
-        if (slot >= chunk || tile >= total) return false;
+        const int tile = tile_of_workgroup(total);
+        if (tile < 0) return false;
         const uint64_t holds = __ballot(upto > tile && upto - sum <= tile);
         const int src = __ffsll((unsigned long long)holds) - 1;
         int rest = tile - (upto - sum), found = -1, first = 0, rows = 0;
@@ -138,10 +148,8 @@ __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs
         __syncthreads();
 
         const int total = table.cum[s.E];
-        const int chunk = (total + 7) / 8;
-        const int slot = blockIdx.x >> 3;
-        const int tile = (int)(blockIdx.x & 7) * chunk + slot;
-        if (slot >= chunk || tile >= total) return false;
+        const int tile = tile_of_workgroup(total);
+        if (tile < 0) return false;
         int lo = 0, hi = s.E;                       // cum[lo] <= tile < cum[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
