@@ -217,7 +217,7 @@ moe_status moe_gate_topk(const moe_dc_config* cfg, const moe_gate* gate, const f
         return fail(MOE_ERR_INVALID_ARG, "a required tensor pointer is NULL");
     const moe_dc::GateShape s{sh.W * sh.BS, n, sh.K, gate->score == MOE_SCORE_SIGMOID ? 1 : 0,
                               g, gate->group_keep, gate->group_top, gate->renormalize,
-                              gate->factor};
+                              gate->factor, (1u << 21) / (uint32_t)(n / g) + 1};
     return launched(moe_dc::launch_gate_topk(s, logits, bias, expert_ids, expert_scales,
                                              static_cast<hipStream_t>(stream)),
                     "router kernel launch");

@@ -57,6 +57,10 @@ struct GateShape {
     int32_t groups, keep, top;
     int32_t renormalize;
     float factor;
+    uint32_t group_magic;    // 2^21 / (n / groups) + 1
+
+    // id / (n / groups) for id < n <= 2048: exact, since id * (n / groups) <= 2^21 with a group limit
+    __host__ __device__ int group_of(int id) const { return (int)(((uint32_t)id * group_magic) >> 21); }
 };
 
 hipError_t launch_gate_topk(const GateShape& s, const float* logits, const float* bias,

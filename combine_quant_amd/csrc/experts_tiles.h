@@ -61,7 +61,7 @@ __device__ __forceinline__ int tile_of_workgroup(int total)
 // experts l * per + 0..per - 1; 71 -> 65 us at 32 experts, 512 rows x 2048 x 7168 int4), for more the
 // workgroup's threads together through LDS (228 -> 201 us at 1024 experts, 4096 rows x 2048 x 512
 // E4M3).  An expert's rows are cut into as few tiles of at most ROWS rows as possible, all of nearly the
-// same height (a multiple of 32).
+// same height (a multiple of 16).
 template <int ROWS, int COLS, int WAVES = kTileWaves>
 __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs& a, int columns,
                                           TileTable& table, Tile* out)
@@ -161,7 +161,7 @@ __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs
         count = expert_end(s, a.ep_recv_count, a.recv_offsets, e) - begin;
     }
     const int mt = (count + ROWS - 1) / ROWS;
-    const int height = ((count + mt - 1) / mt + 31) / 32 * 32;
+    const int height = ((count + mt - 1) / mt + 15) / 16 * 16;
     const int band = idx / (kGroupM * nt), in_band = idx - band * kGroupM * nt;
     const int bm = mt - band * kGroupM < kGroupM ? mt - band * kGroupM : kGroupM;
     const int r0 = (band * kGroupM + in_band % bm) * height;
@@ -181,6 +181,19 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, u
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         r, (__attribute__((address_space(3))) void*)lds, 4, (int)off, 0, 0, 0);
+}
+
+// Four tokens to columns c..c+3 of a row of `half`, of which `left` belong to the tile.
+__device__ __forceinline__ void store_columns(uint16_t* row, int c, int left, int half, uint2 p)
+{
+    if (c + 3 < left && half % 4 == 0) {
+        *reinterpret_cast<uint2*>(row + c) = p;
+    } else {
+        if (c < left) row[c] = (uint16_t)p.x;
+        if (c + 1 < left) row[c + 1] = (uint16_t)(p.x >> 16);
+        if (c + 2 < left) row[c + 2] = (uint16_t)p.y;
+        if (c + 3 < left) row[c + 3] = (uint16_t)(p.y >> 16);
+    }
 }
 
 // Waits until at most N of the wave's global loads are outstanding (they return in order).

@@ -87,11 +87,10 @@ __device__ __forceinline__ bool precedes(float a, int ia, float b, int ib)
 __device__ __noinline__ int plain_token(const GateShape& s, const float* __restrict__ z, uint64_t kept)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    const int size = s.n / s.groups;
     uint32_t out = 0;                                      // the lane's ids that are out of play
     if (s.groups > 1)
         for (int i = 0, id = lane; id < s.n; ++i, id += kWave)
-            if (!((kept >> (id / size)) & 1)) out |= 1u << i;
+            if (!((kept >> s.group_of(id)) & 1)) out |= 1u << i;
     int chosen = 0;
     for (int k = 0; k < s.K; ++k) {
         float best = 0.0f;
@@ -206,7 +205,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
     for (int i = 0; i < CH; ++i) {
         const int id = id_of(i);
         bool in = id < s.n;
-        if (s.groups > 1) in = in && ((kept >> (id / size)) & 1);
+        if (s.groups > 1) in = in && ((kept >> s.group_of(id)) & 1);
         again |= in && v[i] != v[i];
         // (a number's key has bit 31 or bits of 23-30 set, so clearing low bits leaves it in play)
         const uint32_t k = in ? (choice_key(v[i]) & ~kSlots) | (uint32_t)(kSlots - i) : 0u;
@@ -384,6 +383,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
         double value = -INFINITY;
         if (lane < s.groups) {
             double a = -INFINITY, b = -INFINITY;
+#pragma unroll 8
             for (int j = 0; j < size; ++j) {
                 const double w = mine[lane * size + j];
                 if (w > a) {
@@ -395,16 +395,20 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
             }
             value = s.top == 2 ? a + b : a;
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (lane < s.groups) mine[lane] = value;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         int ahead = 0;
+#pragma unroll 8
         for (int g = 0; g < s.groups; ++g) {
-            const double other = __shfl(value, g, kWave);
+            const double other = mine[g];
             if (other > value || (other == value && g < lane)) ++ahead;
         }
         const uint64_t kept = __ballot(lane < s.groups && ahead < s.keep);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int id = lane + i * kWave;
-            if (id < s.n && !((kept >> (id / size)) & 1)) key[i] = 0u;
+            if (id < s.n && !((kept >> s.group_of(id)) & 1)) key[i] = 0u;
         }
     }
 

@@ -158,12 +158,12 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     read_w(0, 0);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     all_w(2);
-    // A step's products go in groups of 32 rows: a group reads the next group's rows from LDS and
+    // A step's products go in groups of 32 rows (the last one perhaps 16): a group reads the next group's rows from LDS and
     // issues its share of the step's loads before its own products.  (Issued together at the
     // step's start, the loads fill the address queue and hold up the products: 1.09 ms instead of
     // XXXX at 16384 rows x 7168 x 4096 bf16.)  The first half of the groups loads x(k + 2), the
     // second the weights of k + 3, whose place is free once read_w has returned.
-    constexpr int kGroups = MT / 2;
+    constexpr int kGroups = (MT + 1) / 2;
     constexpr int kXGroups = kGroups > 1 ? kGroups / 2 : 1;
     constexpr int kWFirst = kGroups > 1 ? kGroups / 2 : 0, kWGroups = kGroups - kWFirst;
     constexpr int kReadW = kWFirst >= 2 ? kWFirst - 2 : 0;
@@ -180,6 +180,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int m = group * 2 + i;
+                if (m >= MT) break;
                 x[set][i] = join(*reinterpret_cast<const v4i_t*>(xl + m * 2048 + f0),
                                  *reinterpret_cast<const v4i_t*>(xl + m * 2048 + f1));
                 if (M::kMx) xsv[set][i] = *reinterpret_cast<const uint8_t*>(xsl + (m * 16 + l16) * 16 + g);
@@ -200,7 +201,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                 if (kWFirst + i * kWGroups / 4 == q) fetch_w(step + 3, i);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2 && q * 2 + i < MT; ++i)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     acc[q * 2 + i][t] = M::mma(w[par][t], x[q & 1][i], acc[q * 2 + i][t], wsc[par][t],
@@ -255,14 +256,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                 y[q] = r;
             }
             const uint2 p = make_uint2(pack_out2(y[0], y[1], s.tok_f16), pack_out2(y[2], y[3], s.tok_f16));
-            if (c + 3 < left && half % 4 == 0) {
-                *reinterpret_cast<uint2*>(o + c) = p;
-            } else {
-                if (c < left) o[c] = (uint16_t)p.x;
-                if (c + 1 < left) o[c + 1] = (uint16_t)(p.x >> 16);
-                if (c + 2 < left) o[c + 2] = (uint16_t)p.y;
-                if (c + 3 < left) o[c + 3] = (uint16_t)(p.y >> 16);
-            }
+            store_columns(o, c, left, half, p);
         }
     }
 }
@@ -275,20 +269,26 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
     Tile t;
     if (!find_tile<kRows, SWIGLU ? kTileN / 2 : kTileN>(s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t))
         return;
-    switch ((t.rows + 31) / 32) {
-    case 1: tile_product<TYPE, 2, SWIGLU>(s, a, t, lds.st); break;
-    case 2: tile_product<TYPE, 4, SWIGLU>(s, a, t, lds.st); break;
-    case 3: tile_product<TYPE, 6, SWIGLU>(s, a, t, lds.st); break;
-    case 4: tile_product<TYPE, 8, SWIGLU>(s, a, t, lds.st); break;
-    case 5: tile_product<TYPE, 10, SWIGLU>(s, a, t, lds.st); break;
-    case 6: tile_product<TYPE, 12, SWIGLU>(s, a, t, lds.st); break;
+    switch ((t.rows + 15) / 16) {
+    case 1: tile_product<TYPE, 1, SWIGLU>(s, a, t, lds.st); break;
+    case 2: tile_product<TYPE, 2, SWIGLU>(s, a, t, lds.st); break;
+    case 3: tile_product<TYPE, 3, SWIGLU>(s, a, t, lds.st); break;
+    case 4: tile_product<TYPE, 4, SWIGLU>(s, a, t, lds.st); break;
+    case 5: tile_product<TYPE, 5, SWIGLU>(s, a, t, lds.st); break;
+    case 6: tile_product<TYPE, 6, SWIGLU>(s, a, t, lds.st); break;
+    case 7: tile_product<TYPE, 7, SWIGLU>(s, a, t, lds.st); break;
+    case 8: tile_product<TYPE, 8, SWIGLU>(s, a, t, lds.st); break;
+    case 9: tile_product<TYPE, 9, SWIGLU>(s, a, t, lds.st); break;
+    case 10: tile_product<TYPE, 10, SWIGLU>(s, a, t, lds.st); break;
+    case 11: tile_product<TYPE, 11, SWIGLU>(s, a, t, lds.st); break;
+    case 12: tile_product<TYPE, 12, SWIGLU>(s, a, t, lds.st); break;
     default:
-        if constexpr (kRows > 192) {
-            if (t.rows <= 224)
-                tile_product<TYPE, 14, SWIGLU>(s, a, t, lds.st);
-            else
-                tile_product<TYPE, 16, SWIGLU>(s, a, t, lds.st);
-        }
+        if constexpr (kRows > 192) switch ((t.rows + 15) / 16) {
+            case 13: tile_product<TYPE, 13, SWIGLU>(s, a, t, lds.st); break;
+            case 14: tile_product<TYPE, 14, SWIGLU>(s, a, t, lds.st); break;
+            case 15: tile_product<TYPE, 15, SWIGLU>(s, a, t, lds.st); break;
+            default: tile_product<TYPE, 16, SWIGLU>(s, a, t, lds.st); break;
+            }
         break;
     }
 }
