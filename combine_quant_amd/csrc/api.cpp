@@ -397,6 +397,6 @@ moe_status moe_combine_int8(const moe_dc_config* cfg, const int8_t* codes,
 
 const char* moe_dc_last_error(void) { return g_last_error.c_str(); }
 
-const char* moe_dc_version(void) { return "moe_dc 0.4.0 (gfx950)"; }
+const char* moe_dc_version(void) { return "moe_dc 0.5.0 (gfx950)"; }
 
 }  // extern "C"

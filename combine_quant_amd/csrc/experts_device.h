@@ -32,11 +32,11 @@ __device__ __forceinline__ v4i_t load_chunk(__amdgpu_buffer_rsrc_t r, uint32_t o
     return __builtin_bit_cast(v4i_t, v);
 }
 
-// Row types.  All products walk rows in chunks of 128 bytes; lane l of a wave holds, of row
-// l % 16, the 16 bytes at (l / 16) * 16 and the 16 bytes at 64 + (l / 16) * 16 of the chunk, which
-// is the operand layout of every instruction used here (two of K = 32 for 16-bit types, two
-// of K = 64 for int8, one of K = 128 for fp8).  The result of A (16 weight rows) times B (16 rows of
-// x) has, in lane l, row l % 16 of x and weight rows (l / 16) * 4 + 0..3.
+// Row types.  All products walk rows in chunks of 128 bytes; lane l of a wave holds, of row l %
+// 16, the 16 bytes at (l / 16) * 16 and the 16 bytes at 64 + (l / 16) * 16 of the chunk, which is
+// the operand layout of every instruction used here (two of K = 32 for 16-bit types, two of K =
+// 64 for int8, one of K = 128 for fp8).  The result of A (16 weight rows) times B (16 rows of x)
+// has, in lane l, row l % 16 of x and weight rows (l / 16) * 4 + 0..3.
 template <int TYPE>
 struct Mm {
     static constexpr bool kMx = TYPE == kMmMxE4m3 || TYPE == kMmMxE5m2;

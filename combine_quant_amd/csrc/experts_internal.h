@@ -59,7 +59,8 @@ struct GateShape {
     float factor;
     uint32_t group_magic;    // 2^21 / (n / groups) + 1
 
-    // id / (n / groups) for id < n <= 2048: exact, since id * (n / groups) <= 2^21 with a group limit
+    // id / (n / groups) for id < n <= 2048: exact, since id * (n / groups) <= 2^21 with a group
+    // limit
     __host__ __device__ int group_of(int id) const { return (int)(((uint32_t)id * group_magic) >> 21); }
 };
 

@@ -33,8 +33,8 @@ inline unsigned tile_grid(const MatmulShape& s, int height, int cols)
     return (unsigned)((tiles + 7) / 8 * 8);
 }
 
-// Whether there are at least `least` tiles of `height` rows and `cols` columns, in the mean over the
-// experts that can have rows.
+// Whether there are at least `least` tiles of `height` rows and `cols` columns, in the mean over
+// the experts that can have rows.
 inline bool tiles_suffice(const MatmulShape& s, int height, int cols, int least)
 {
     const int64_t half = s.swiglu ? s.out / 2 : s.out;
@@ -43,10 +43,10 @@ inline bool tiles_suffice(const MatmulShape& s, int height, int cols, int least)
     return active * ((s.rows / active + height - 1) / height) * ((half + cols - 1) / cols) >= least;
 }
 
-// The place of this workgroup among `total` tiles, or -1.  Workgroup b runs on XCD b % 8.  Each XCD takes
-// 32 consecutive tiles (one per CU) at a time, so that the tiles of an expert share its weights and its rows
-// in that XCD's L2 while experts with many and with few rows are spread over the XCDs; the last tiles
-// are shared out evenly.
+// The place of this workgroup among `total` tiles, or -1.  Workgroup b runs on XCD b % 8.  Each
+// XCD takes 32 consecutive tiles (one per CU) at a time, so that the tiles of an expert share its
+// weights and its rows in that XCD's L2 while experts with many and with few rows are spread over
+// the XCDs; the last tiles are shared out evenly.
 __device__ __forceinline__ int tile_of_workgroup(int total)
 {
     const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
@@ -56,12 +56,12 @@ __device__ __forceinline__ int tile_of_workgroup(int total)
     return r < share && xcd * share + r < rest ? full * 256 + xcd * share + r : -1;
 }
 
-// The workgroup's tile.  The ragged counts live on the device, so every workgroup counts the tiles of
-// all experts, then finds its own: for up to 128 experts each wave by itself (lane l counts
-// experts l * per + 0..per - 1; 71 -> 65 us at 32 experts, 512 rows x 2048 x 7168 int4), for more the
-// workgroup's threads together through LDS (228 -> 201 us at 1024 experts, 4096 rows x 2048 x 512
-// E4M3).  An expert's rows are cut into as few tiles of at most ROWS rows as possible, all of nearly the
-// same height (a multiple of 16).
+// The workgroup's tile.  The ragged counts live on the device, so every workgroup counts the
+// tiles of all experts, then finds its own: for up to 128 experts each wave by itself (lane l
+// counts experts l * per + 0..per - 1; 71 -> 65 us at 32 experts, 512 rows x 2048 x 7168 int4),
+// for more the workgroup's threads together through LDS (228 -> 201 us at 1024 experts, 4096 rows
+// x 2048 x 512 E4M3).  An expert's rows are cut into as few tiles of at most ROWS rows as
+// possible, all of nearly the same height (a multiple of 16).
 template <int ROWS, int COLS, int WAVES = kTileWaves>
 __device__ __forceinline__ bool find_tile(const MatmulShape& s, const MatmulArgs& a, int columns,
                                           TileTable& table, Tile* out)
@@ -183,10 +183,11 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, u
         r, (__attribute__((address_space(3))) void*)lds, 4, (int)off, 0, 0, 0);
 }
 
-// Four tokens to columns c..c+3 of a row of `half`, of which `left` belong to the tile.
-__device__ __forceinline__ void store_columns(uint16_t* row, int c, int left, int half, uint2 p)
+// Four tokens to columns c..c+3 of a row, of which `left` are the tile's (rows begin at any
+// token).
+__device__ __forceinline__ void store_columns(uint16_t* row, int c, int left, uint2 p)
 {
-    if (c + 3 < left && half % 4 == 0) {
+    if (c + 3 < left && (reinterpret_cast<uintptr_t>(row + c) & 7) == 0) {
         *reinterpret_cast<uint2*>(row + c) = p;
     } else {
         if (c < left) row[c] = (uint16_t)p.x;
@@ -194,6 +195,14 @@ __device__ __forceinline__ void store_columns(uint16_t* row, int c, int left, in
         if (c + 2 < left) row[c + 2] = (uint16_t)p.y;
         if (c + 3 < left) row[c + 3] = (uint16_t)(p.y >> 16);
     }
+}
+
+// A workgroup barrier that leaves loads on their way: what other waves' loads put into LDS is
+// there for those that each wave has waited for (wait_loads) before it.
+__device__ __forceinline__ void meet()
+{
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");              // no LDS access moves above it
 }
 
 // Waits until at most N of the wave's global loads are outstanding (they return in order).

@@ -5,18 +5,19 @@
 //
 // gate_scores_kernel (a bias, or groups measured by sums of scores): one wave per token forms the
 // choices in binary64 and orders them through a 32-bit key of their binary32 rounding: rounding
-// never reverses an order, so a key that is alone at the top is the best choice, found by one 32-bit
-// wave maximum; only keys that tie are compared in binary64, then by id.  19.5 us for 8192 tokens x
-// 256 ids, K = 8, 8 groups (8.9 MB): bound by its instructions, half of them the binary64
-// exponentials.
+// never reverses an order, so a key that is alone at the top is the best choice, found by one
+// 32-bit wave maximum; only keys that tie are compared in binary64, then by id.  19.5 us for 8192
+// tokens x 256 ids, K = 8, 8 groups (8.9 MB): bound by its instructions, half of them the
+// binary64 exponentials.
 //
 // gate_logits_kernel (the logits themselves are compared, which is the order of the scores): the
-// scores are needed only for the K chosen.  LANES lanes per token; each lane first sorts its DEPTH
-// largest keys (its slot in a key's low bits), and a round takes the largest head among the
-// lanes and moves the winner's list up; with tokens enough to fill the chip, one wave
-// serves four tokens of 16 lanes each.  Keys that agree but for the slot bits are settled by the
-// logits and ids of the K + 2 candidates, and if that is not enough (many equal logits) by the whole wave
-// in a plain loop.  16384 tokens x 516 ids, K = 16 (34 MB): 33 us, against 54 us by the first kernel.
+// scores are needed only for the K chosen.  LANES lanes per token; each lane first sorts its
+// DEPTH largest keys (its slot in a key's low bits), and a round takes the largest head among the
+// lanes and moves the winner's list up; with tokens enough to fill the chip, one wave serves four
+// tokens of 16 lanes each.  Keys that agree but for the slot bits are settled by the logits and
+// ids of the K + 2 candidates, and if that is not enough (many equal logits) by the whole wave in
+// a plain loop.  16384 tokens x 516 ids, K = 16 (34 MB): 33 us, against 54 us by the first
+// kernel.
 #include "experts_internal.h"
 #include "dc_device.h"
 
@@ -25,7 +26,9 @@ namespace {
 
 constexpr int kGateWaves = 4;
 constexpr int kGateMaxIds = 2048;
-constexpr int kGateQuarterTokens = 2048;        // tokens from which a wave serves four
+// Tokens from which a wave serves four (16384 x 516, K = 16: 33 us, against 52 with a wave each;
+// below, waves would be too few for the CUs).
+constexpr int kGateQuarterTokens = 2048;
 // Order-preserving keys: 0 is kept for ids out of play, 1 for NaN.
 __device__ __forceinline__ uint32_t choice_key(float f)
 {
@@ -120,8 +123,8 @@ __device__ __noinline__ int plain_token(const GateShape& s, const float* __restr
 // Slots of a lane are held in the low kSlotBits bits of its keys.
 constexpr int slot_bits(int ch) { return ch <= 4 ? 2 : ch <= 8 ? 3 : ch <= 16 ? 4 : ch <= 32 ? 5 : 6; }
 
-// CH: ids per lane: lane l of a token's LANES holds ids l + LANES * i.  DEPTH: keys a lane sorts at a
-// time.
+// CH: ids per lane: lane l of a token's LANES holds ids l + LANES * i.  DEPTH: keys a lane sorts
+// at a time.
 template <int LANES, int CH, int DEPTH>
 __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
     GateShape s, const float* __restrict__ logits, int32_t* __restrict__ expert_ids,
@@ -165,8 +168,8 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
     uint64_t kept = ~0ull;
     const int size = s.n / s.groups;
     if (s.groups > 1) {
-        // A group's value is its largest logit (group_top 1); 64 / LANES groups per lane.  A group
-        // counts the groups ahead of it and the keep first ones stay.
+        // A group's value is its largest logit (group_top 1); 64 / LANES groups per lane.  A
+        // group counts the groups ahead of it and the keep first ones stay.
         float* mine = mem + sub * s.n;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -207,7 +210,8 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
         bool in = id < s.n;
         if (s.groups > 1) in = in && ((kept >> s.group_of(id)) & 1);
         again |= in && v[i] != v[i];
-        // (a number's key has bit 31 or bits of 23-30 set, so clearing low bits leaves it in play)
+        // (a number's key has bit 31 or bits of 23-30 set, so clearing low bits leaves it in
+        // play)
         const uint32_t k = in ? (choice_key(v[i]) & ~kSlots) | (uint32_t)(kSlots - i) : 0u;
         v[i] = __uint_as_float(k);
     }
@@ -495,8 +499,8 @@ template <int LANES, int CH>
 hipError_t launch_depth(const GateShape& s, const float* logits, int32_t* ids, float* scales,
                         hipStream_t stream)
 {
-    // A list that runs out is sorted anew: with four keys in 0.2 % of the tokens for K = 8, with six in
-    // 0.1 % for K = 16.
+    // A list that runs out is sorted anew: with four keys in 0.2 % of the tokens for K = 8, with
+    // six in 0.1 % for K = 16.
     if (CH <= 4 || s.K <= 8) return launch_logits<LANES, CH, 4>(s, logits, ids, scales, stream);
     return launch_logits<LANES, CH, 6>(s, logits, ids, scales, stream);
 }

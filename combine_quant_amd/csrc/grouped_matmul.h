@@ -7,9 +7,9 @@
 namespace moe_dc {
 namespace {
 
-// Fewer tiles leave CUs idle, more the streaming kernel's narrow column blocks use.  bf16, inner size 4096,
-// 8 experts: 32 tiles 29.7 us against 21.8 by streaming (8 rows an expert), 44.5 against 38.7 (64
-// rows); 64 tiles 29.7 against 34.9, 45.7 against 73.1.
+// Fewer tiles leave CUs idle, more the streaming kernel's narrow column blocks use.  bf16, inner
+// size 4096, 8 experts: 32 tiles 29.7 us against 21.8 by streaming (8 rows an expert), 44.5
+// against 38.7 (64 rows); 64 tiles 29.7 against 34.9, 45.7 against 73.1.
 constexpr int kTileLeast = 56;
 
 template <int TYPE>

@@ -1,8 +1,11 @@
-// grouped_matmul_stream.h -- the experts' products for few rows per expert.
+// grouped_matmul_stream.h -- the experts' products where tiles are too few for the chip.
 //
-// A workgroup takes NT * 16 weight rows of one expert and walks their inner dimension once, its
-// four waves taking 128-byte chunks in turn, straight from global memory into matrix registers;
-// the waves' sums meet in LDS at the end.
+// A workgroup takes 32 weight rows of one expert (with SwiGLU 16 gate and 16 up rows) and walks
+// their inner dimension once, its four waves taking 128-byte chunks in turn, straight from global
+// memory into matrix registers; the waves' sums meet in LDS at the end.  Bound by latency: 64
+// rows on 8 experts x 1024 x 1024 bf16 (17 MB) take 6 us, 333 rows on 12 experts x 1144 x 777
+// fp16 11 us.  (Loads in the matrix layout run at 16 bytes a clock per CU, which is why larger
+// products go through LDS.)
 #pragma once
 
 #include "experts_device.h"

@@ -166,9 +166,10 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_kernel(MatmulShape s, Mat
     }
 }
 
-// Fewer tiles leave CUs idle, more the streaming kernel's narrow column blocks use.  int4, inner size 4096, 8
-// experts: with 8 rows an expert 128 small tiles take 18.0 us against 16.3 by streaming, 256
-// 19.6 against 28.0; with 64 rows 64 tiles 58.7 against 51.4, 128 60.0 against 93.1.
+// Fewer tiles leave CUs idle, more the streaming kernel's narrow column blocks use.  int4, inner
+// size 4096, 8 experts: with 8 rows an expert 128 small tiles take 18.0 us against 16.3 by
+// streaming, 256 19.6 against 28.0; with 64 rows 64 tiles 58.7 against 51.4, 128 60.0 against
+// 93.1.
 constexpr int kSmallLeast = 144;
 constexpr int kW4TileLeast = 80;
 

@@ -1,17 +1,24 @@
-// grouped_matmul_w4_tile.h -- 4-bit products for many rows per expert.
+// grouped_matmul_w4_tile.h -- 4-bit products in tiles.
 //
 // A workgroup of eight waves multiplies up to 128 rows of x with 256 weight rows, or one of four
-// waves up to 32 rows with 128, in steps of 128 elements; wave w owns weight rows 32 * w + 0..31 (with SwiGLU 16 gate rows and the 16 up rows of the same
-// columns) and takes every row of x.  x (256 bytes a row and step), a wave's codes (64 bytes a
-// row and step) and its scales lie in LDS rings, moved there by the loads themselves; the rings are
-// as deep as LDS allows, three steps for 128 rows, five for 32, where a step is short against the
-// memory's latency.  (No load goes to a register: the wait for it would be one for every load
-// before it too.)  Each step decodes the codes of the next one to 16-bit floats in registers, a
-// part with each part of its own products, so that the conversions run beside the
-// matrix instructions.
+// waves up to 32 rows with 128, in steps of 128 elements; wave w owns weight rows 32 * w + 0..31
+// (with SwiGLU 16 gate rows and the 16 up rows of the same columns) and takes every row of x.  x
+// (256 bytes a row and step), a wave's codes (64 bytes a row and step) and its scales lie in LDS
+// rings, moved there by the loads themselves; the rings are three steps deep for 96 and 128 rows,
+// four below, where a step is short against the memory's latency.  (No load goes to a register:
+// the wait for it would be one for every load before it too; with the scales in registers, loaded
+// one by one, 512 rows on 32 experts x 7168 x 4096 E2M1 took 285 us instead of 150.)  Each step
+// decodes the codes of the next one to 16-bit floats in registers, a part with each part of its
+// own products, so that the conversions run beside the matrix instructions.
 //
-// x is the A operand (rows of the result) and the weights B (columns): lane l holds column
-// l % 16 and rows (l / 16) * 4 + 0..3, hence one scale per lane and column tile.
+// Few rows are bound by the instructions that turn codes into operands, 230 a wave and step,
+// above the bytes: 16 rows on 16 of 64 experts x 7168 x 4096 int4 (227 MB) take 50 us, 32 experts
+// with 16 rows each (493 MB) 134 us, 3.7 TB/s.  With many rows the matrix units are the bound:
+// 4096 rows on 32 experts x 2048 x 7168 E2M1 take 200 us, 600 Tflop/s, of which 10 us a tile are
+// its start and end, as inner size 2048 is only 16 steps; at 8192 it is 740 Tflop/s.
+//
+// x is the A operand (rows of the result) and the weights B (columns): lane l holds column l % 16
+// and rows (l / 16) * 4 + 0..3, hence one scale per lane and column tile.
 #pragma once
 
 #include "grouped_matmul_w4.h"
@@ -52,16 +59,17 @@ union W4SmallLds {
 };
 static_assert(sizeof(W4Lds) <= kW4LdsBytes && 2 * sizeof(W4SmallLds) <= kW4LdsBytes, "LDS of a CU");
 
-// Four int4 codes as E4M3 bytes worth code * 2^-9 (subnormals, and 2^-6 for 8), from the codes' low three
-// bits and their sign bits moved to bit 0: negative codes become 0x88 - low3 = (low3 ^ 7) + 0x81.
+// Four int4 codes as E4M3 bytes worth code * 2^-9 (subnormals, and 2^-6 for 8), from the codes'
+// low three bits and their sign bits moved to bit 0: negative codes become 0x88 - low3 = (low3 ^
+// 7) + 0x81.
 __device__ __forceinline__ uint32_t int4_bytes(uint32_t low3, uint32_t sign)
 {
     const uint32_t seven = (sign << 2) | ((sign << 1) | sign);
     return (low3 ^ seven) + ((sign << 7) | sign);
 }
 
-// Eight codes of a dword as 16-bit floats exactly, in their order.  SURPLUS (int4 for bf16): instead
-// 136 + code, in the order 0 4 1 5 2 6 3 7, which takes a third of the instructions.
+// Eight codes of a dword as 16-bit floats exactly, in their order.  SURPLUS (int4 for bf16):
+// instead 136 + code, in the order 0 4 1 5 2 6 3 7, which takes a third of the instructions.
 template <bool F16, bool E2M1, bool SURPLUS>
 __device__ __forceinline__ v4i_t decode_tile(uint32_t w, float scale)
 {
@@ -128,10 +136,10 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
                   ((uint32_t)(sfirst & 3) + (uint32_t)(SWIGLU ? half + left : left) * srow + 3) & ~3u);
     // bf16 holds every E2M1 code times a power of two, so its scale enters with the conversion.
     constexpr bool kFolded = E2M1 && !F16;
-    // int4 for bf16: with few rows the conversions bound the tile, and the surplus 136 * sum(x) of the
-    // short decoding leaves through the sums' start value, a product with constant -136 shared by
-    // both column tiles (half as many matrix instructions again, which are idle here; with many rows
-    // they are not).
+    // int4 for bf16: with few rows the conversions bound the tile, and the surplus 136 * sum(x)
+    // of the short decoding leaves through the sums' start value, a product with constant -136
+    // shared by both column tiles (half as many matrix instructions again, which are idle here;
+    // with many rows they are not).
     constexpr bool kSurplus = !E2M1 && !F16 && MT <= 2;
     const int neg136 = (int)0xC308C308u;                    // bf16 -136, twice
     const v4i_t minus = {neg136, neg136, neg136, neg136};
@@ -183,8 +191,8 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
         if constexpr (kSLoads == 2) load_lds4(sr, st + 256, d + 8);
     };
 
-    // The codes and scales of a step, from LDS: of row l16 (t = 0) and row 16 + l16, the dword g of
-    // chunk j for 32-element step j.
+    // The codes and scales of a step, from LDS: of row l16 (t = 0) and row 16 + l16, the dword g
+    // of chunk j for 32-element step j.
     uint32_t raw[2][4], sraw[2][3];
     const auto read_raw = [&](int step) {
         const char* wl = lds.w[wave][step % kRing] + l16 * 64 + g * 4;
@@ -238,9 +246,9 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const int f0 = l16 * 128 + ((g ^ (l16 & 7)) << 4);
     const int f1 = l16 * 128 + (((4 + g) ^ (l16 & 7)) << 4);
 
-    // Before step 0: its codes decoded, the codes of step 1 in registers, every stage but one of x
-    // and all places of codes filled or on their way.  In step k the place of x(k - 1) takes x(k +
-    // ring - 1), and that of the codes of k + 1 (in registers) those of k + 1 + ring.
+    // Before step 0: its codes decoded, the codes of step 1 in registers, every stage but one of
+    // x and all places of codes filled or on their way.  In step k the place of x(k - 1) takes
+    // x(k + ring - 1), and that of the codes of k + 1 (in registers) those of k + 1 + ring.
     constexpr int kStep = kXLoads + 2 + kSLoads;             // loads of a step
     const auto all_x = [&](int step) {
 #pragma unroll
@@ -266,7 +274,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const auto one = [&](int par, int step) {
         // x(step): issued after it are the rest of its step's loads, and ring - 2 whole steps
         wait_loads<2 + kSLoads + (kRing - 2) * kStep>();
-        __builtin_amdgcn_s_barrier();
+        meet();
         const char* xl = lds.x[step % kRing][0];
         v4i_t x[2][4];
         const auto read_x = [&](int set, int m) {
