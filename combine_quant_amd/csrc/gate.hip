@@ -398,6 +398,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
                 }
             }
             value = s.top == 2 ? a + b : a;
+            if (value != value) value = -INFINITY;         // infinities of both signs
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (lane < s.groups) mine[lane] = value;

@@ -75,6 +75,8 @@ __device__ __forceinline__ void w4_tile(const MatmulShape& s, const MatmulArgs& 
                     const uint32_t b = static_cast<const uint16_t*>(a.w_scales)[so + gi];
                     sc[t][j] = F16 ? f16_lo(b) : bf16_lo(b);
                 }
+                // past the row's end the sum is 0, and its scale must be finite
+                if (c * (4 / STEPS) + j >= ns) sc[t][j] = 0.0f;
             }
         }
 #pragma unroll

@@ -432,7 +432,9 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
  *   weight         bytes [E][N][I/2], two codes per byte
  *   weight_scales  int4: token type [E][N][I/group_size]; E2M1: E8M0 bytes [E][N][I/32]
  * I must be a multiple of group_size.  The codes enter the matrix instructions exactly; each
- * group's sum is formed in fp32, multiplied by its scale and added in fp32.  x must be finite.
+ * group's sum is formed in fp32, multiplied by its scale and added in fp32.  (E2M1 codes may
+ * enter as bf16 code * scale, which is exact for scale bytes up to 252; with 253 or 254 the
+ * larger codes may turn infinite.)  x must be finite.
  * Everything else as for moe_grouped_matmul. */
 moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm, const void* x,
                                  const void* weight, const void* weight_scales,
@@ -471,7 +473,7 @@ typedef struct {
  *   bias           fp32 [n] or NULL
  *   expert_ids     int32 [W][BS][K]
  *   expert_scales  fp32 [W][BS][K]
- * A NaN choice ranks below every number; a softmax row without a finite logit (or with a NaN
+ * A NaN choice or group value ranks below every number; a softmax row without a finite logit (or with a NaN
  * or +infinity) has weights 0 or NaN, and its ids are distinct and in range all the same.
  * K may not exceed the ids of the kept groups. */
 moe_status moe_gate_topk(const moe_dc_config* cfg, const moe_gate* gate, const float* logits,

@@ -315,6 +315,78 @@ def test_4bit_every_code():
         assert torch.equal(out[:128].double(), ref.w4_to_f64(w, ws, weight, group)[0].t())
 
 
+def _check_extremes(out, x, w, ranges, rows):
+    """x and w are not negative, so no partial sum exceeds the result: above fp32's range it is
+    infinite, and below it the usual bound holds, with 2^-125 more where the result or its last
+    sum may be subnormal (2^-126 in the sum, and as much in the rounding)."""
+    y, err = ref.product(x, w, ranges, False, cut=True)
+    got = out[:rows].double()
+    nan = torch.isnan(y)
+    assert nan.any() and torch.equal(torch.isnan(got), nan)
+    big = y >= 2.0 ** 128
+    assert big.any() and torch.isinf(got[big]).all()
+    rest = y < 2.0 ** 127
+    tol = err + 2.0 ** -8 * (y + err) + 2.0 ** -125
+    assert (y[rest] < 2.0 ** -100).any() and ((got - y).abs()[rest] <= tol[rest]).all()
+
+
+@pytest.mark.parametrize("counts,N", [([60, 0, 29, 5], 70), ([70, 0, 129, 5] * 8, 1600)])
+def test_mx_scales_to_the_ends_of_their_range(counts, N):
+    W, I = 2, 256
+    cfg = _config(W, counts, extra=0)
+    cap, rows, E = cfg.expand_rows_capacity, sum(counts), len(counts)
+    g = _gen(11)
+    erc, off, ranges = ref.pack_counts(counts, W)
+    x = torch.rand((cap, I), generator=g, device=DEV).add(0.1).to(torch.float8_e4m3fn)
+    w = torch.rand((E, N, I), generator=g, device=DEV).add(0.1).to(torch.float8_e4m3fn)
+    ends = torch.tensor([0, 1, 2, 40, 64, 100, 127, 150, 190, 220, 253, 254, 255], device=DEV, dtype=torch.uint8)
+    xs = ends[torch.arange(cap, device=DEV) % 13][:, None].expand(cap, I // 32).contiguous()
+    ws = ends[torch.arange(E * N, device=DEV) % 13].view(E, N, 1).expand(E, N, I // 32).contiguous()
+    out = cq.grouped_matmul(cfg, _desc("mx_e4m3", I, N, False), x, w, erc.to(DEV), off.to(DEV),
+                            x_scales=xs, weight_scales=ws)
+    nan = float("nan")
+    vx = ref.codes_to_f64(x, xs).masked_fill((xs == 255)[:, :1], nan)[:rows]
+    vw = ref.codes_to_f64(w, ws).masked_fill((ws == 255)[:, :, :1], nan)
+    _check_extremes(out, vx, vw, ranges, rows)
+
+
+@pytest.mark.parametrize("counts,N", [([60, 0, 29, 5], 70), ([70, 0, 129, 5] * 8, 1600),
+                                      ([16, 0, 9, 5] * 8, 1600)])
+def test_e2m1_scales_to_the_ends_of_their_range(counts, N):
+    W, I = 2, 256
+    cfg = _config(W, counts, extra=0)
+    cap, rows, E = cfg.expand_rows_capacity, sum(counts), len(counts)
+    g = _gen(12)
+    erc, off, ranges = ref.pack_counts(counts, W)
+    ends = torch.tensor([0, 1, 2, 3, 40, 64, 100, 127, 150, 190, 220, 252, 255], device=DEV, dtype=torch.uint8)
+    powers = torch.tensor([-100, -60, 0, 3, 60, 110], device=DEV)[torch.arange(cap, device=DEV) % 6]
+    x = torch.rand((cap, I), generator=g, device=DEV).add(0.1).mul(2.0 ** powers[:, None]).bfloat16()
+    w = torch.randint(0, 256, (E, N, I // 2), generator=g, device=DEV, dtype=torch.uint8) & 0x77
+    ws = ends[torch.arange(E * N, device=DEV) % 13].view(E, N, 1).expand(E, N, I // 32).contiguous()
+    mm = cq.make_matmul(I, N, weight_dtype=cq.MOE_W4_E2M1, group_size=32)
+    out = cq.grouped_matmul_w4(cfg, mm, x, w, ws, erc.to(DEV), off.to(DEV))
+    vw = ref.w4_to_f64(w, ws, "e2m1", 32).masked_fill((ws == 255)[:, :, :1], float("nan"))
+    _check_extremes(out, x[:rows].double(), vw, ranges, rows)
+
+
+@pytest.mark.parametrize("token", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 64])
+def test_4bit_infinite_last_scale(token, group):
+    """The last group of a row that ends inside a chunk of 128 has an infinite scale."""
+    dt = torch.float16 if token == "f16" else torch.bfloat16
+    W, counts, N, I = 2, [5, 0, 18, 2], 33, 128 + group
+    cfg = _config(W, counts, f16=token == "f16", extra=0)
+    erc, off, _ = ref.pack_counts(counts, W)
+    x = torch.ones((cfg.expand_rows_capacity, I), dtype=dt, device=DEV)
+    w = torch.full((4, N, I // 2), 0x11, dtype=torch.uint8, device=DEV)
+    w[:, 1::2] = 0xFF                                                # -1
+    ws = torch.ones((4, N, I // group), dtype=dt, device=DEV)
+    ws[..., -1] = float("inf")
+    mm = cq.make_matmul(I, N, weight_dtype=cq.MOE_W4_INT4, group_size=group)
+    out = cq.grouped_matmul_w4(cfg, mm, x, w, ws, erc.to(DEV), off.to(DEV))[:25].float()
+    assert (out[:, ::2] == float("inf")).all() and (out[:, 1::2] == -float("inf")).all()
+
+
 def test_4bit_weights_past_32_bits():
     W, E, I, N = 2, 140, 8192, 8192
     counts = [0] * (E - 1) + [2]
@@ -429,3 +501,18 @@ def test_router_masked_rows():
                     assert ids[4].tolist() == [0, 1, 2, 7]
                 else:
                     assert ids[1].tolist() == [0, 1, 2, 3] and (w[1] == 0.25).all()
+
+
+def test_router_infinite_biases():
+    """A group whose two best choices are infinities of both signs has no value: it comes last."""
+    z = torch.randn((6, 64), generator=torch.Generator().manual_seed(3))
+    bias = torch.full((64,), -math.inf)
+    bias[16:32] = 0.0
+    bias[3] = math.inf
+    cfg = cq.make_config(2, 64, 3, 1024, 4)
+    for score in (cq.MOE_SCORE_SOFTMAX, cq.MOE_SCORE_SIGMOID):
+        gate = cq.make_gate(score, 4, 1, 2, True)
+        ids, w = cq.gate_topk(cfg, gate, z.view(2, 3, 64).to(DEV), bias.to(DEV))
+        ids = ids.view(6, 4).cpu()
+        assert torch.equal(ids.long(), z[:, 16:32].topk(4, 1).indices + 16)
+        assert torch.isfinite(w).all()
