@@ -58,6 +58,43 @@ __device__ __forceinline__ double exp2_fine(double t)
     return t < -1100.0 ? 0.0 : __builtin_ldexp(1.0 + (double)(p * f), (int)r);
 }
 
+// e^x for x <= 0 (or NaN) to about an ulp: x = k ln 2 + f, Taylor series of e^f to the 13th power
+// for |f| <= ln(2) / 2 (remainder 4.2e-18).
+__device__ __forceinline__ double exp_below(double x)
+{
+    const double k = __builtin_rint(x * 1.4426950408889634);
+    double f = __builtin_fma(-k, 0.6931471805599453, x);
+    f = __builtin_fma(-k, 2.3190468138462996e-17, f);     // ln 2 less its binary64 value
+    double p = 1.0 / 6227020800.0;
+    p = __builtin_fma(p, f, 1.0 / 479001600.0);
+    p = __builtin_fma(p, f, 1.0 / 39916800.0);
+    p = __builtin_fma(p, f, 1.0 / 3628800.0);
+    p = __builtin_fma(p, f, 1.0 / 362880.0);
+    p = __builtin_fma(p, f, 1.0 / 40320.0);
+    p = __builtin_fma(p, f, 1.0 / 5040.0);
+    p = __builtin_fma(p, f, 1.0 / 720.0);
+    p = __builtin_fma(p, f, 1.0 / 120.0);
+    p = __builtin_fma(p, f, 1.0 / 24.0);
+    p = __builtin_fma(p, f, 1.0 / 6.0);
+    p = __builtin_fma(p, f, 0.5);
+    p = __builtin_fma(p, f, 1.0);
+    p = __builtin_fma(p, f, 1.0);
+    return x < -760.0 ? 0.0 : __builtin_ldexp(p, (int)k);
+}
+
+// 1 / (1 + e^-z) as (1 or t) / (1 + t) with t = e^-|z|: the divisor lies in [1, 2], so its
+// reciprocal needs no scaling; two Newton steps, and one on the quotient.
+__device__ __forceinline__ double sigmoid(double z)
+{
+    const double t = exp_below(-__builtin_fabs(z));
+    const double d = 1.0 + t, num = z < 0.0 ? t : 1.0;
+    double y = __builtin_amdgcn_rcp(d);
+    y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+    y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+    const double q = num * y;
+    return __builtin_fma(__builtin_fma(-d, q, num), y, q);
+}
+
 template <int LANES, typename T>
 __device__ __forceinline__ T group_sum(T v)
 {
@@ -75,8 +112,8 @@ __device__ __forceinline__ float group_max(float v)
 
 __device__ __forceinline__ double fine_score(const GateShape& s, float z, double peak, double total)
 {
-    if (s.sigmoid) return 1.0 / (1.0 + exp(-(double)z));
-    return peak > -INFINITY ? exp((double)z - peak) / total : 0.0;
+    if (s.sigmoid) return sigmoid((double)z);
+    return peak > -INFINITY ? exp_below((double)z - peak) / total : 0.0;
 }
 
 // a is chosen before b: the larger one, NaN last, then the lower id.
@@ -358,12 +395,12 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
         double part = 0.0;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
-            if (lane + i * kWave < s.n && top > -INFINITY) part += exp((double)v[i] - peak);
+            if (lane + i * kWave < s.n && top > -INFINITY) part += exp_below((double)v[i] - peak);
         total = wave_sum(part);
     }
     const auto score = [&](float x) -> double {
-        if (s.sigmoid) return 1.0 / (1.0 + exp(-(double)x));
-        return top > -INFINITY ? exp((double)x - peak) / total : 0.0;
+        if (s.sigmoid) return sigmoid((double)x);
+        return top > -INFINITY ? exp_below((double)x - peak) / total : 0.0;
     };
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -374,46 +411,49 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
     }
 
     if (s.groups > 1) {
-        // A group's value from its group_top best choices, one group per lane; then each group
-        // counts the groups ahead of it and the keep first ones stay.
+        // A group's value from its group_top best choices, 2^shift lanes sharing a group; then
+        // each group counts the groups ahead of it and the keep first ones stay.
         const int size = s.n / s.groups;
         double* mine = group_lds + (size_t)wave * s.n;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int id = lane + i * kWave;
-            if (id < s.n) mine[id] = WIDE ? c[i] : s.top == 2 ? score(v[i]) : (double)v[i];
+            const double w = WIDE ? c[i] : s.top == 2 ? score(v[i]) : (double)v[i];
+            if (id < s.n) mine[id] = w == w ? w : -INFINITY;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        double value = -INFINITY;
-        if (lane < s.groups) {
-            double a = -INFINITY, b = -INFINITY;
-#pragma unroll 8
-            for (int j = 0; j < size; ++j) {
-                const double w = mine[lane * size + j];
-                if (w > a) {
-                    b = a;
-                    a = w;
-                } else if (w > b) {
-                    b = w;
-                }
+        int shift = 0;
+        while ((s.groups << (shift + 1)) <= kWave) ++shift;
+        const int share = 1 << shift, group = lane >> shift;
+        double a = -INFINITY, b = -INFINITY;
+        if (group < s.groups)
+#pragma unroll 4
+            for (int j = lane & (share - 1); j < size; j += share) {
+                const double w = mine[group * size + j];
+                b = fmax(b, fmin(a, w));
+                a = fmax(a, w);
             }
-            value = s.top == 2 ? a + b : a;
-            if (value != value) value = -INFINITY;         // infinities of both signs
+        for (int off = 1; off < share; off <<= 1) {
+            const double oa = __shfl_xor(a, off, kWave), ob = __shfl_xor(b, off, kWave);
+            b = fmax(fmin(a, oa), fmax(b, ob));
+            a = fmax(a, oa);
         }
+        double value = s.top == 2 ? a + b : a;
+        if (value != value) value = -INFINITY;             // infinities of both signs
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (lane < s.groups) mine[lane] = value;
+        if (group < s.groups) mine[group] = value;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         int ahead = 0;
 #pragma unroll 8
         for (int g = 0; g < s.groups; ++g) {
             const double other = mine[g];
-            if (other > value || (other == value && g < lane)) ++ahead;
+            if (other > value || (other == value && g < group)) ++ahead;
         }
-        const uint64_t kept = __ballot(lane < s.groups && ahead < s.keep);
+        const uint64_t kept = __ballot(group < s.groups && ahead < s.keep);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int id = lane + i * kWave;
-            if (id < s.n && !((kept >> s.group_of(id)) & 1)) key[i] = 0u;
+            if (id < s.n && !((kept >> (s.group_of(id) << shift)) & 1)) key[i] = 0u;
         }
     }
 
