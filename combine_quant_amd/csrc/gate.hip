@@ -6,9 +6,12 @@
 // gate_scores_kernel (a bias, or groups measured by sums of scores): one wave per token forms the
 // choices in binary64 and orders them through a 32-bit key of their binary32 rounding: rounding
 // never reverses an order, so a key that is alone at the top is the best choice, found by one
-// 32-bit wave maximum; only keys that tie are compared in binary64, then by id.  19.5 us for 8192
-// tokens x 256 ids, K = 8, 8 groups (8.9 MB): bound by its instructions, half of them the
-// binary64 exponentials.
+// 32-bit wave maximum; only keys that tie are compared in binary64, then by id.  17 us for 8192
+// tokens x 256 ids, K = 8, 8 groups (8.9 MB), 6.8 us for 2 tokens: bound by its instructions and,
+// with few tokens, by one wave's latency.  (With the library's exponential, one lane to a group
+// and the winner's id by a lane shuffle it took 20.3 and 9.1 us; 16 lanes a token need half the
+// instructions but leave two waves a SIMD, which wait: 19.8 us, and 25.6 against 29.3 from 16384
+// tokens on.)
 //
 // gate_logits_kernel (the logits themselves are compared, which is the order of the scores): the
 // scores are needed only for the K chosen.  LANES lanes per token; each lane first sorts its
@@ -457,8 +460,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
         }
     }
 
-    int my_id = 0;               // lane k < K: the k-th choice and its score
-    double my_score = 0.0;
+    int my_id = 0;                                         // lane k < K: the k-th choice
     for (int k = 0; k < s.K; ++k) {
         uint32_t best = 0;
 #pragma unroll
@@ -502,22 +504,17 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
             }
             winner = bid & (kWave - 1);
         }
-        float x = 0.0f;
+        winner = __builtin_amdgcn_readfirstlane(winner);
+        const int id = lane_value(lane + slot * kWave, winner);
+        if (lane == k) my_id = id;
+        if (lane == winner) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (i == slot) {
-                x = v[i];
-                if (lane == winner) key[i] = 0u;
-            }
-        const int id = __shfl(lane + slot * kWave, winner, kWave);
-        const float xw = __shfl(x, winner, kWave);
-        if (lane == k) {
-            my_id = id;
-            my_score = (double)xw;
+            for (int i = 0; i < CH; ++i)
+                if (i == slot) key[i] = 0u;
         }
     }
     // The K scores, one per lane.
-    double w = lane < s.K ? score((float)my_score) : 0.0;
+    double w = lane < s.K ? score(z[my_id]) : 0.0;
     if (s.renormalize) w = w / (wave_sum(w) + 1e-20);
     if (lane < s.K) {
         expert_ids[(size_t)token * s.K + lane] = my_id;
