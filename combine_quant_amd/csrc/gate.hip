@@ -127,13 +127,14 @@ __device__ __forceinline__ bool precedes(float a, int ia, float b, int ib)
 }
 
 // One token by the whole wave.  Returns the lane's choice (lane k < K: the k-th id).
-__device__ __noinline__ int plain_token(const GateShape& s, const float* __restrict__ z, uint64_t kept)
+__device__ __noinline__ int plain_token(const GateShape& s, const float* __restrict__ z, uint64_t kept,
+                                        int shift)
 {
     const int lane = threadIdx.x & (kWave - 1);
     uint32_t out = 0;                                      // the lane's ids that are out of play
     if (s.groups > 1)
         for (int i = 0, id = lane; id < s.n; ++i, id += kWave)
-            if (!((kept >> s.group_of(id)) & 1)) out |= 1u << i;
+            if (!((kept >> (s.group_of(id) << shift)) & 1)) out |= 1u << i;
     int chosen = 0;
     for (int k = 0; k < s.K; ++k) {
         float best = 0.0f;
@@ -205,50 +206,43 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
     }
 
     bool again = false;                                    // the token needs the plain loop
-    uint64_t kept = ~0ull;
+    uint64_t kept = ~0ull;                                 // group g: bit g << shift
+    int shift = 0;
     const int size = s.n / s.groups;
     if (s.groups > 1) {
-        // A group's value is its largest logit (group_top 1); 64 / LANES groups per lane.  A
+        // A group's value is its largest logit (group_top 1); 2^shift lanes share a group.  A
         // group counts the groups ahead of it and the keep first ones stay.
         float* mine = mem + sub * s.n;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
             if (id_of(i) < s.n) mine[id_of(i)] = v[i];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        float value[kTokens];
-        int ahead[kTokens];
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            const int g = l + j * LANES;
-            value[j] = -INFINITY;                          // (fmaxf leaves NaN out)
-            ahead[j] = 0;
-            if (g < s.groups)
+        while ((s.groups << (shift + 1)) <= LANES) ++shift;
+        const int share = 1 << shift, group = l >> shift;
+        float value = -INFINITY;                           // (fmaxf leaves NaN out)
+        if (group < s.groups)
 #pragma unroll 8
-                for (int i = 0; i < size; ++i) value[j] = fmaxf(value[j], mine[g * size + i]);
-        }
+            for (int i = l & (share - 1); i < size; i += share)
+                value = fmaxf(value, mine[group * size + i]);
+        for (int off = 1; off < share; off <<= 1) value = fmaxf(value, __shfl_xor(value, off, kWave));
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (group < s.groups) mine[group] = value;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        int ahead = 0;
+#pragma unroll 8
         for (int g = 0; g < s.groups; ++g) {
-            float other = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kTokens; ++j)
-                if (g / LANES == j) other = __shfl(value[j], sub * LANES + g % LANES, kWave);
-#pragma unroll
-            for (int j = 0; j < kTokens; ++j)
-                if (other > value[j] || (other == value[j] && g < l + j * LANES)) ++ahead[j];
+            const float other = mine[g];
+            if (other > value || (other == value && g < group)) ++ahead;
         }
-        kept = 0;
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            const uint64_t in = __ballot(l + j * LANES < s.groups && ahead[j] < s.keep);
-            kept |= (LANES == kWave ? in : (in >> (sub * LANES)) & ((1ull << (LANES & 63)) - 1))
-                    << (j * (LANES & 63));
-        }
+        kept = __ballot(group < s.groups && ahead < s.keep);
+        if (LANES != kWave) kept = (kept >> (sub * LANES)) & ((1ull << (LANES & 63)) - 1);
     }
 
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int id = id_of(i);
         bool in = id < s.n;
-        if (s.groups > 1) in = in && ((kept >> s.group_of(id)) & 1);
+        if (s.groups > 1) in = in && ((kept >> (s.group_of(id) << shift)) & 1);
         again |= in && v[i] != v[i];
         // (a number's key has bit 31 or bits of 23-30 set, so clearing low bits leaves it in
         // play)
@@ -320,7 +314,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
             const uint64_t lanes = LANES == kWave ? ~0ull : ((1ull << (LANES & 63)) - 1) << (t * LANES);
             if (!(redo & lanes) || token0 + t >= s.tokens) continue;
             const int chosen = plain_token(s, logits + (size_t)(token0 + t) * s.n,
-                                           __shfl((unsigned long long)kept, t * LANES, kWave));
+                                           __shfl((unsigned long long)kept, t * LANES, kWave), shift);
             const int got = __shfl(chosen, l, kWave);
             if (sub == t) my_id = got;
         }
@@ -366,7 +360,8 @@ __device__ __forceinline__ double wave_sum(double v)
     return v;
 }
 
-// CH: ids per lane.  WIDE: choices are binary64 values (a bias was added); otherwise logits.
+// CH: ids per lane.  WIDE: choices are binary64 values (a bias was added); otherwise logits, and
+// groups are measured by the sum of their two best scores.
 template <int CH, bool WIDE>
 __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
     GateShape s, const float* __restrict__ logits, const float* __restrict__ bias,
@@ -381,7 +376,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
 
     float v[CH];
     uint32_t key[CH];
-    double c[CH];                                          // WIDE: the choices
+    double c[CH];                                          // scores; WIDE: the choices
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -397,19 +392,23 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
         peak = top;
         double part = 0.0;
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (lane + i * kWave < s.n && top > -INFINITY) part += exp_below((double)v[i] - peak);
+        for (int i = 0; i < CH; ++i) {
+            c[i] = 0.0;
+            if (lane + i * kWave < s.n && top > -INFINITY) c[i] = exp_below((double)v[i] - peak);
+            part += c[i];
+        }
         total = wave_sum(part);
+        const double inverse = top > -INFINITY ? 1.0 / total : 0.0;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) c[i] *= inverse;
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) c[i] = lane + i * kWave < s.n ? sigmoid((double)v[i]) : 0.0;
     }
-    const auto score = [&](float x) -> double {
-        if (s.sigmoid) return sigmoid((double)x);
-        return top > -INFINITY ? exp_below((double)x - peak) / total : 0.0;
-    };
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int id = lane + i * kWave;
-        c[i] = 0.0;
-        if (WIDE && id < s.n) c[i] = score(v[i]) + (double)bias[id];
+        if (WIDE && id < s.n) c[i] += (double)bias[id];
         key[i] = id < s.n ? choice_key(WIDE ? (float)c[i] : v[i]) : 0u;
     }
 
@@ -421,8 +420,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int id = lane + i * kWave;
-            const double w = WIDE ? c[i] : s.top == 2 ? score(v[i]) : (double)v[i];
-            if (id < s.n) mine[id] = w == w ? w : -INFINITY;
+            if (id < s.n) mine[id] = c[i] == c[i] ? c[i] : -INFINITY;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         int shift = 0;
@@ -514,7 +512,7 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
         }
     }
     // The K scores, one per lane.
-    double w = lane < s.K ? score(z[my_id]) : 0.0;
+    double w = lane < s.K ? fine_score(s, z[my_id], peak, total) : 0.0;
     if (s.renormalize) w = w / (wave_sum(w) + 1e-20);
     if (lane < s.K) {
         expert_ids[(size_t)token * s.K + lane] = my_id;
@@ -568,7 +566,7 @@ hipError_t launch_gate_topk(const GateShape& s, const float* logits, const float
         if (s.n <= 1024) return launch_scores<16>(s, logits, bias, expert_ids, expert_scales, stream);
         return launch_scores<32>(s, logits, bias, expert_ids, expert_scales, stream);
     }
-    if (s.tokens >= kGateQuarterTokens) {
+    if (s.tokens >= kGateQuarterTokens && s.groups <= 16) {      // (a lane or more per group)
         if (s.n <= 256) return launch_depth<16, 16>(s, logits, expert_ids, expert_scales, stream);
         if (s.n <= 576) return launch_depth<16, 36>(s, logits, expert_ids, expert_scales, stream);
     }
