@@ -6,12 +6,12 @@
 // gate_scores_kernel (a bias, or groups measured by sums of scores): one wave per token forms the
 // choices in binary64 and orders them through a 32-bit key of their binary32 rounding: rounding
 // never reverses an order, so a key that is alone at the top is the best choice, found by one
-// 32-bit wave maximum; only keys that tie are compared in binary64, then by id.  17 us for 8192
-// tokens x 256 ids, K = 8, 8 groups (8.9 MB), 6.8 us for 2 tokens: bound by its instructions and,
+// 32-bit wave maximum; only keys that tie are compared in binary64, then by id.  15.4 us for 8192
+// tokens x 256 ids, K = 8, 8 groups (8.9 MB), 6.5 us for 2 tokens: bound by its instructions and,
 // with few tokens, by one wave's latency.  (With the library's exponential, one lane to a group
-// and the winner's id by a lane shuffle it took 20.3 and 9.1 us; 16 lanes a token need half the
-// instructions but leave two waves a SIMD, which wait: 19.8 us, and 25.6 against 29.3 from 16384
-// tokens on.)
+// and the winner's id by a lane shuffle it took 18.3 and 8.3 us.  16 lanes a token need half the
+// instructions but leave two waves a SIMD, which wait: with 4096 tokens 15.9 us against 10.8, with
+// 8192 19.8 against 17.0 in one run, and only from 16384 on less, 25.6 against 29.3.)
 //
 // gate_logits_kernel (the logits themselves are compared, which is the order of the scores): the
 // scores are needed only for the K chosen.  LANES lanes per token; each lane first sorts its
