@@ -516,3 +516,16 @@ def test_router_infinite_biases():
         ids = ids.view(6, 4).cpu()
         assert torch.equal(ids.long(), z[:, 16:32].topk(4, 1).indices + 16)
         assert torch.isfinite(w).all()
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("W,BS", [(2, 1), (8, 275)])
+def test_router_scores_over_the_whole_range(W, BS, renorm):
+    """Sigmoids from 0 over subnormal binary32 values to 1; the biases alone decide the order."""
+    z = torch.tensor([-1e30, -800.0, -745.0, -103.5, -100.0, -90.0, -40.0, -16.0, -1.0, -1e-30, 0.0,
+                      1e-6, 1.0, 20.0, 90.0, 1e30])
+    g = torch.Generator().manual_seed(5)
+    logits = torch.stack([z[torch.randperm(16, generator=g)] for _ in range(W * BS)])
+    bias = torch.randperm(16, generator=g).float() * 4
+    _run_gate(W, BS, 16, 0, 16, logits, bias, True, 1, 1, 1, renorm, 1.0)
+    _run_gate(W, BS, 16, 0, 16, logits / 8, bias, False, 1, 1, 1, renorm, 1.0)
