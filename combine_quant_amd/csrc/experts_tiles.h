@@ -3,6 +3,7 @@
 #pragma once
 
 #include "experts_device.h"
+#include "experts_path.h"
 
 namespace moe_dc {
 namespace {
@@ -31,16 +32,6 @@ inline unsigned tile_grid(const MatmulShape& s, int height, int cols)
     const int64_t active = s.rows < s.E ? s.rows : s.E;
     const int64_t tiles = (s.rows / height + active) * ((half + cols - 1) / cols);
     return (unsigned)((tiles + 7) / 8 * 8);
-}
-
-// Whether there are at least `least` tiles of `height` rows and `cols` columns, in the mean over
-// the experts that can have rows.
-inline bool tiles_suffice(const MatmulShape& s, int height, int cols, int least)
-{
-    const int64_t half = s.swiglu ? s.out / 2 : s.out;
-    const int64_t active = s.rows < s.E ? s.rows : s.E;
-    if (active == 0) return false;
-    return active * ((s.rows / active + height - 1) / height) * ((half + cols - 1) / cols) >= least;
 }
 
 // The place of this workgroup among `total` tiles, or -1.  Workgroup b runs on XCD b % 8.  Each

@@ -20,12 +20,10 @@
 namespace moe_dc {
 namespace {
 
-constexpr int kTileN = 256;                     // weight rows of a workgroup
 constexpr int kTileRing = 3;                    // steps of x in LDS
 
-// Most rows of x of a workgroup: as many as the 160 KB of LDS take (MX keeps scales there too).
 template <int TYPE>
-constexpr int kTileM = Mm<TYPE>::kMx ? 192 : 256;
+constexpr int kTileM = tile_rows(TYPE);
 
 template <int TYPE>
 struct TileStages {

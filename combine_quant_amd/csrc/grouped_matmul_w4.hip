@@ -168,22 +168,11 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_kernel(MatmulShape s, Mat
     }
 }
 
-// Fewer tiles leave CUs idle, more the streaming kernel's narrow column blocks use.  int4, inner
-// size 4096, 8 experts: with 8 rows an expert 128 small tiles take 18.0 us against 16.3 by
-// streaming, 256 19.6 against 28.0; with 64 rows 64 tiles 58.7 against 51.4, 128 60.0 against
-// 93.1.
-constexpr int kSmallLeast = 144;
-constexpr int kW4TileLeast = 80;
-
 template <bool F16>
 hipError_t launch_token(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
-    // few rows per expert: the smaller tiles, where they are enough
-    const int64_t active = s.rows < s.E ? s.rows : s.E;
-    if (s.rows <= kW4SmallM * active && tiles_suffice(s, kW4SmallM, s.swiglu ? kW4SmallN / 2 : kW4SmallN, kSmallLeast))
-        return launch_w4_tiles<F16>(s, a, true, stream);
-    if (tiles_suffice(s, kW4TileM, s.swiglu ? kW4TileN / 2 : kW4TileN, kW4TileLeast))
-        return launch_w4_tiles<F16>(s, a, false, stream);
+    const ProductPath path = product_path(s);
+    if (path != kPathStream) return launch_w4_tiles<F16>(s, a, path == kPathSmallTiles, stream);
     const int half = s.swiglu ? s.out / 2 : s.out;
     const int per = s.swiglu ? 16 : 32;
     int64_t z = (s.rows / s.E + 63) / 64;

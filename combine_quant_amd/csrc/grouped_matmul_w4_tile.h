@@ -26,10 +26,6 @@
 namespace moe_dc {
 namespace {
 
-constexpr int kW4TileM = 128;                   // rows of x and weight rows of a workgroup
-constexpr int kW4TileN = 256;
-constexpr int kW4SmallM = 32;                   // and of the smaller one, two to a CU
-constexpr int kW4SmallN = 128;
 constexpr int kW4SmallWaves = 4;
 constexpr int kW4LdsBytes = 163840;
 

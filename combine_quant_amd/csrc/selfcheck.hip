@@ -10,7 +10,11 @@
 //   division: every binary32 b with the sign bit clear (zero, subnormals, infinity and NaNs
 //          included), div_rn<8>(448, b), div_rn<15>(57344, b) and div_rn<1>(1, b) compared bit
 //          for bit with the correctly rounded quotient
+//
+// It also answers, on the host, which kernel a product takes, so that a test can say which one
+// its sizes are meant to reach.
 #include "dc_convert.h"
+#include "experts_path.h"
 
 #include <hip/hip_runtime.h>
 
@@ -109,6 +113,20 @@ int moe_dc_selfcheck_conversions(unsigned long long* counts)
         e = hipMemcpy(counts, bad, kCounts * sizeof(unsigned long long), hipMemcpyDeviceToHost);
     const hipError_t f = hipFree(bad);
     return (int)(e != hipSuccess ? e : f);
+}
+
+// The moe_dc::ProductPath of a product: `type` is a moe_dc::MmType, `w4` 0 or a moe_w4_dtype,
+// `rows` W * BS * K.
+int moe_dc_selfcheck_product_path(int type, int w4, int E, long long rows, int out, int swiglu)
+{
+    MatmulShape s{};
+    s.type = type;
+    s.w4 = w4;
+    s.E = E;
+    s.rows = rows;
+    s.out = out;
+    s.swiglu = swiglu;
+    return product_path(s);
 }
 
 }  // extern "C"
