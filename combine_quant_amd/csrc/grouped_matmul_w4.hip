@@ -6,12 +6,9 @@
 // of dwords between the four lane groups then leaves in dword j the lane's eight elements of
 // 32-element step j, the operand layout of the 16x16x32 instructions.
 //
-// Codes become 16-bit floats exactly.  int4 for bf16 rows: the four bits under an exponent of 2^7
-// are 136 + code, and the surplus 136 * sum(x) leaves through the accumulator's start value, a
-// product with constant -136 shared by all weight tiles; for fp16 rows 1032 + code, minus
-// 1032 by a packed subtraction.  E2M1 by the conversion instruction.  x is the A operand
-// (rows of the result), the weights B (columns), so that one lane holds one weight row's results
-// and one scale: each group's sum is formed by itself in fp32, scaled and added in fp32.
+// Codes become 16-bit floats exactly (decode).  x is the A operand (rows of the result), the
+// weights B (columns), so that one lane holds one weight row's results and one scale: each
+// group's sum is formed by itself in fp32, scaled and added in fp32.
 #include "grouped_matmul_w4.h"
 #include "grouped_matmul_w4_tile.h"
 
@@ -49,9 +46,6 @@ __device__ __forceinline__ void w4_tile(const MatmulShape& s, const MatmulArgs& 
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[m][t] = v4f_t{0, 0, 0, 0};
-    const int neg136 = (int)0xC308C308u;                    // bf16 -136, twice
-    const v4i_t minus = {neg136, neg136, neg136, neg136};
-
     v4i_t wv[NT], xv[MT][4];
     float sc[NT][4 / STEPS];
     const auto fetch = [&](int c) {
@@ -95,16 +89,13 @@ __device__ __forceinline__ void w4_tile(const MatmulShape& s, const MatmulArgs& 
         for (int j = 0; j < 4 / STEPS; ++j) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                v4f_t start = {0, 0, 0, 0};
                 v4i_t xo[STEPS];
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    xo[i] = E2M1 ? xv[m][j * STEPS + i] : pair_order(xv[m][j * STEPS + i]);
-                    if (!E2M1 && !F16) start = mma16<F16>(xo[i], minus, start);
-                }
+                for (int i = 0; i < STEPS; ++i)
+                    xo[i] = F16 && !E2M1 ? pair_order(xv[m][j * STEPS + i]) : xv[m][j * STEPS + i];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    v4f_t p = start;
+                    v4f_t p = {0, 0, 0, 0};
 #pragma unroll
                     for (int i = 0; i < STEPS; ++i)
                         p = mma16<F16>(xo[i], decode<F16, E2M1>((uint32_t)wv[t][j * STEPS + i]), p);
@@ -132,7 +123,10 @@ __device__ __forceinline__ void w4_tile(const MatmulShape& s, const MatmulArgs& 
 #pragma unroll
             for (int w = 1; w < kW4Waves; ++w) u += part[((w * MT + m) * NT + t + nt) * kWave + lane];
         }
+        constexpr float unit = kCodeUnit<F16, E2M1>;
         const int n = t * 16 + l16;
+        r *= unit;
+        u *= unit;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int row = m * 16 + g * 4 + q;

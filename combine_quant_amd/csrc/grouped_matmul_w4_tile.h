@@ -11,9 +11,9 @@
 // decodes the codes of the next one to 16-bit floats in registers, a part with each part of its
 // own products, so that the conversions run beside the matrix instructions.
 //
-// Few rows are bound by the instructions that turn codes into operands, 230 a wave and step,
-// above the bytes: 16 rows on 16 of 64 experts x 7168 x 4096 int4 (227 MB) take 50 us, 32 experts
-// with 16 rows each (493 MB) 134 us, 3.7 TB/s.  With many rows the matrix units are the bound:
+// Few rows are bound by the instructions that turn codes into operands, above the bytes: 16 rows
+// on 16 of 64 experts x 7168 x 4096 int4 (227 MB) take 53 us, 32 experts with 16 rows each (493
+// MB) 141 us, 3.5 TB/s.  With many rows the matrix units are the bound:
 // 4096 rows on 32 experts x 2048 x 7168 E2M1 take 200 us, 600 Tflop/s, of which 10 us a tile are
 // its start and end, as inner size 2048 is only 16 steps; at 8192 it is 740 Tflop/s.
 //
@@ -55,49 +55,18 @@ union W4SmallLds {
 };
 static_assert(sizeof(W4Lds) <= kW4LdsBytes && 2 * sizeof(W4SmallLds) <= kW4LdsBytes, "LDS of a CU");
 
-// Four int4 codes as E4M3 bytes worth code * 2^-9 (subnormals, and 2^-6 for 8), from the codes'
-// low three bits and their sign bits moved to bit 0: negative codes become 0x88 - low3 = (low3 ^
-// 7) + 0x81.
-__device__ __forceinline__ uint32_t int4_bytes(uint32_t low3, uint32_t sign)
-{
-    const uint32_t seven = (sign << 2) | ((sign << 1) | sign);
-    return (low3 ^ seven) + ((sign << 7) | sign);
-}
-
-// Eight codes of a dword as 16-bit floats exactly, in their order.  SURPLUS (int4 for bf16):
-// instead 136 + code, in the order 0 4 1 5 2 6 3 7, which takes a third of the instructions.
-template <bool F16, bool E2M1, bool SURPLUS>
+// Eight codes of a dword as decode gives them, int4 for fp16 in their order too (a tile's x is
+// used by every column, so the weights are put in order instead).
+template <bool F16, bool E2M1>
 __device__ __forceinline__ v4i_t decode_tile(uint32_t w, float scale)
 {
-    v4i_t r;
-    if constexpr (E2M1 && F16) {
-        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
-        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
-        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
-        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
-    } else if constexpr (E2M1) {
-        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
-        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
-        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
-        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
-    } else if constexpr (SURPLUS) {
-        r = decode<false, false>(w);
-    } else if constexpr (F16) {
-        const v4i_t p = decode<true, false>(w);              // 0 4, 1 5, 2 6, 3 7
+    v4i_t r = decode<F16, E2M1>(w, scale);
+    if constexpr (F16 && !E2M1) {
+        const v4i_t p = r;                                   // 0 4, 1 5, 2 6, 3 7
         r.x = (int)__builtin_amdgcn_perm((uint32_t)p.y, (uint32_t)p.x, 0x05040100u);
         r.y = (int)__builtin_amdgcn_perm((uint32_t)p.w, (uint32_t)p.z, 0x05040100u);
         r.z = (int)__builtin_amdgcn_perm((uint32_t)p.y, (uint32_t)p.x, 0x07060302u);
         r.w = (int)__builtin_amdgcn_perm((uint32_t)p.w, (uint32_t)p.z, 0x07060302u);
-    } else {
-        const uint32_t v = w >> 4;
-        const uint32_t even = int4_bytes(w & 0x07070707u, (w >> 3) & 0x01010101u);   // 0 2 4 6
-        const uint32_t odd = int4_bytes(v & 0x07070707u, (v >> 3) & 0x01010101u);    // 1 3 5 7
-        const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u);           // 0 1 2 3
-        const uint32_t hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);           // 4 5 6 7
-        r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
-        r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
-        r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
-        r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
     }
     return r;
 }
@@ -132,13 +101,6 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
                   ((uint32_t)(sfirst & 3) + (uint32_t)(SWIGLU ? half + left : left) * srow + 3) & ~3u);
     // bf16 holds every E2M1 code times a power of two, so its scale enters with the conversion.
     constexpr bool kFolded = E2M1 && !F16;
-    // int4 for bf16: with few rows the conversions bound the tile, and the surplus 136 * sum(x)
-    // of the short decoding leaves through the sums' start value, a product with constant -136
-    // shared by both column tiles (half as many matrix instructions again, which are idle here;
-    // with many rows they are not).
-    constexpr bool kSurplus = !E2M1 && !F16 && MT <= 2;
-    const int neg136 = (int)0xC308C308u;                    // bf16 -136, twice
-    const v4i_t minus = {neg136, neg136, neg136, neg136};
 
     const int lr = lane >> 3;
     const uint32_t lk = (uint32_t)((lane & 7) ^ lr) * 16;
@@ -233,7 +195,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
     const auto decode_part = [&](int par, int j) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            w[par][t][j] = decode_tile<F16, E2M1, kSurplus>(raw[t][j], kFolded ? scale[par][t][j / STEPS] : 1.0f);
+            w[par][t][j] = decode_tile<F16, E2M1>(raw[t][j], kFolded ? scale[par][t][j / STEPS] : 1.0f);
     };
 
     v4f_t acc[MT][2];
@@ -298,9 +260,6 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j * MT / 4 == m) decode_part(par ^ 1, j);
-            if constexpr (kSurplus)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[m & 1][j] = pair_order(x[m & 1][j]);
             if constexpr (kFolded) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -310,12 +269,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
                 v4f_t sum[kParts][2];
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) {
-                    sum[p][0] = v4f_t{0, 0, 0, 0};
-                    if constexpr (kSurplus)
-#pragma unroll
-                        for (int j = 0; j < STEPS; ++j)
-                            sum[p][0] = mma16<F16>(x[m & 1][p * STEPS + j], minus, sum[p][0]);
-                    sum[p][1] = sum[p][0];
+                    sum[p][0] = sum[p][1] = v4f_t{0, 0, 0, 0};
 #pragma unroll
                     for (int j = 0; j < STEPS; ++j)
 #pragma unroll
@@ -355,7 +309,9 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = m * 16 + g * 4 + r;
-                const float y = SWIGLU ? silu(acc[m][0][r]) * acc[m][1][r] : acc[m][t][r];
+                constexpr float unit = kCodeUnit<F16, E2M1>;
+                const float y = SWIGLU ? silu(acc[m][0][r] * unit) * (acc[m][1][r] * unit)
+                                       : acc[m][t][r] * unit;
                 if (row < tile.rows && c < left)
                     static_cast<uint16_t*>(a.out)[(size_t)(tile.row0 + row) * half + tile.n0 + c] =
                         (uint16_t)pack_out2(y, 0.0f, F16);

@@ -432,9 +432,9 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
  *   weight         bytes [E][N][I/2], two codes per byte
  *   weight_scales  int4: token type [E][N][I/group_size]; E2M1: E8M0 bytes [E][N][I/32]
  * I must be a multiple of group_size.  The codes enter the matrix instructions exactly; each
- * group's sum is formed in fp32, multiplied by its scale and added in fp32.  (E2M1 codes may
- * enter as bf16 code * scale, which is exact for scale bytes up to 252; with 253 or 254 the
- * larger codes may turn infinite.)  x must be finite.
+ * group's sum (int4 with bf16 rows: a sixteenth of it) is formed in fp32, multiplied by its scale
+ * and added in fp32.  (E2M1 codes may enter as bf16 code * scale, which is exact for scale bytes
+ * up to 252; with 253 or 254 the larger codes may turn infinite.)
  * Everything else as for moe_grouped_matmul. */
 moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm, const void* x,
                                  const void* weight, const void* weight_scales,
