@@ -177,7 +177,8 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     // (Issued together at the step's start, the loads fill the address queue and hold up the
     // products: 1.09 ms instead of 0.86 at 16384 rows on 32 experts x 7168 x 4096 bf16.)  The
     // first half of the groups loads x(k + 2), the second the weights of k + 3, whose place is
-    // free once read_w has returned.
+    // free once read_w has returned: two groups after it, since LDS reads return in order and the
+    // products between have waited for rows read after it; with fewer groups by a wait.
     constexpr int kGroups = (MT + 1) / 2;
     constexpr int kXGroups = kGroups > 1 ? kGroups / 2 : 1;
     constexpr int kWFirst = kGroups > 1 ? kGroups / 2 : 0, kWGroups = kGroups - kWFirst;
@@ -204,7 +205,10 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         read_x(0, 0);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-            if (q == kReadW) read_w(par ^ 1, step + 1);
+            if (q == kReadW) {
+                read_w(par ^ 1, step + 1);
+                __builtin_amdgcn_sched_barrier(0);           // before read_x(q + 1), see kReadW
+            }
             if (q + 1 < kGroups) read_x((q + 1) & 1, q + 1);
             if (q == kWFirst && kWFirst < kReadW + 2)
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
