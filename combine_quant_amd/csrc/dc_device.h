@@ -152,8 +152,9 @@ __device__ __forceinline__ void store_stream(uint2* p, uint2 o)
 // through it are range-checked by the hardware: a load past the end returns 0 and a store
 // past it is dropped.  Code that covers a ragged row end this way needs no branch around the
 // access, so the compiler can count outstanding memory operations exactly and wait only for
-// the ones a value depends on.  Every access here is 16, 8 or 4 bytes at a multiple of its
-// size, so it lies either wholly inside or wholly past the end.
+// the ones a value depends on.  Every access is 16, 8 or 4 bytes at a multiple of its size (MX
+// scales: 16 bytes at a multiple of 4, within one row), so it lies either wholly inside or wholly
+// past the end.
 constexpr int32_t kRsrcWord3 = 0x00020000;       // gfx9 family: 32-bit data format, no swizzle
 constexpr uint32_t kRsrcPastEnd = 0x80000000u;    // an offset past the end of every resource
 constexpr int kRsrcNonTemporal = 2;              // aux bits: the nt cache policy
