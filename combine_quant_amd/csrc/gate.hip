@@ -23,6 +23,7 @@
 // kernel.
 #include "experts_internal.h"
 #include "dc_device.h"
+#include "gate_math.h"
 
 namespace moe_dc {
 namespace {
@@ -43,46 +44,6 @@ __device__ __forceinline__ uint32_t choice_key(float f)
 __device__ __forceinline__ float key_choice(uint32_t k)
 {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
-
-// 2^t for t <= 0, relative error below 2^-25: Taylor series of 2^f - 1 to the seventh power for
-// |f| <= 1/2 (remainder 5.2e-9) in binary32, the rest in binary64.
-__device__ __forceinline__ double exp2_fine(double t)
-{
-    const double r = __builtin_rint(t);
-    const float f = (float)(t - r);
-    float p = 1.525273380e-5f;                            // ln2^7 / 7!
-    p = __builtin_fmaf(p, f, 1.540353039e-4f);
-    p = __builtin_fmaf(p, f, 1.333355815e-3f);
-    p = __builtin_fmaf(p, f, 9.618129108e-3f);
-    p = __builtin_fmaf(p, f, 5.550410866e-2f);
-    p = __builtin_fmaf(p, f, 2.402265070e-1f);
-    p = __builtin_fmaf(p, f, 6.931471806e-1f);
-    return t < -1100.0 ? 0.0 : __builtin_ldexp(1.0 + (double)(p * f), (int)r);
-}
-
-// e^x for x <= 0 (or NaN) to about an ulp: x = k ln 2 + f, Taylor series of e^f to the 13th power
-// for |f| <= ln(2) / 2 (remainder 4.2e-18).
-__device__ __forceinline__ double exp_below(double x)
-{
-    const double k = __builtin_rint(x * 1.4426950408889634);
-    double f = __builtin_fma(-k, 0.6931471805599453, x);
-    f = __builtin_fma(-k, 2.3190468138462996e-17, f);     // ln 2 less its binary64 value
-    double p = 1.0 / 6227020800.0;
-    p = __builtin_fma(p, f, 1.0 / 479001600.0);
-    p = __builtin_fma(p, f, 1.0 / 39916800.0);
-    p = __builtin_fma(p, f, 1.0 / 3628800.0);
-    p = __builtin_fma(p, f, 1.0 / 362880.0);
-    p = __builtin_fma(p, f, 1.0 / 40320.0);
-    p = __builtin_fma(p, f, 1.0 / 5040.0);
-    p = __builtin_fma(p, f, 1.0 / 720.0);
-    p = __builtin_fma(p, f, 1.0 / 120.0);
-    p = __builtin_fma(p, f, 1.0 / 24.0);
-    p = __builtin_fma(p, f, 1.0 / 6.0);
-    p = __builtin_fma(p, f, 0.5);
-    p = __builtin_fma(p, f, 1.0);
-    p = __builtin_fma(p, f, 1.0);
-    return x < -760.0 ? 0.0 : __builtin_ldexp(p, (int)k);
 }
 
 // 1 / (1 + e^-z) as (1 or t) / (1 + t) with t = e^-|z|: the divisor lies in [1, 2], so its

@@ -12,9 +12,11 @@
 //          for bit with the correctly rounded quotient
 //
 // It also answers, on the host, which kernel a product takes, so that a test can say which one
-// its sizes are meant to reach.
+// its sizes are meant to reach, and evaluates the router's exponentials, so that a test can
+// measure their error.
 #include "dc_convert.h"
 #include "experts_path.h"
+#include "gate_math.h"
 
 #include <hip/hip_runtime.h>
 
@@ -127,6 +129,12 @@ int moe_dc_selfcheck_product_path(int type, int w4, int E, long long rows, int o
     s.out = out;
     s.swiglu = swiglu;
     return product_path(s);
+}
+
+// out[i] = 2^t[i] (which = 0, t <= 0) or e^t[i] (which = 1, t <= 0) as the router forms them.
+void moe_dc_selfcheck_exp(int which, const double* t, double* out, long long n)
+{
+    for (long long i = 0; i < n; ++i) out[i] = which ? exp_below(t[i]) : exp2_fine(t[i]);
 }
 
 }  // extern "C"
