@@ -171,8 +171,9 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
     int shift = 0;
     const int size = s.n / s.groups;
     if (s.groups > 1) {
-        // A group's value is its largest logit (group_top 1); 2^shift lanes share a group.  A
-        // group counts the groups ahead of it and the keep first ones stay.
+        // A group's value is its largest logit (group_top 1), NaN without one, as a key, since
+        // NaN ranks below -infinity; 2^shift lanes share a group.  A group counts the groups
+        // ahead of it and the keep first ones stay.
         float* mine = mem + sub * s.n;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -180,20 +181,21 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_logits_kernel(
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         while ((s.groups << (shift + 1)) <= LANES) ++shift;
         const int share = 1 << shift, group = l >> shift;
-        float value = -INFINITY;                           // (fmaxf leaves NaN out)
+        float value = NAN;                                 // (fmaxf leaves NaN out)
         if (group < s.groups)
 #pragma unroll 8
             for (int i = l & (share - 1); i < size; i += share)
                 value = fmaxf(value, mine[group * size + i]);
         for (int off = 1; off < share; off <<= 1) value = fmaxf(value, __shfl_xor(value, off, kWave));
+        const uint32_t rank = choice_key(value);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (group < s.groups) mine[group] = value;
+        if (group < s.groups) mine[group] = __uint_as_float(rank);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         int ahead = 0;
 #pragma unroll 8
         for (int g = 0; g < s.groups; ++g) {
-            const float other = mine[g];
-            if (other > value || (other == value && g < group)) ++ahead;
+            const uint32_t other = __float_as_uint(mine[g]);
+            if (other > rank || (other == rank && g < group)) ++ahead;
         }
         kept = __ballot(group < s.groups && ahead < s.keep);
         if (LANES != kWave) kept = (kept >> (sub * LANES)) & ((1ull << (LANES & 63)) - 1);
@@ -375,13 +377,16 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
 
     if (s.groups > 1) {
         // A group's value from its group_top best choices, 2^shift lanes sharing a group; then
-        // each group counts the groups ahead of it and the keep first ones stay.
+        // each group counts the groups ahead of it and the keep first ones stay.  NaN ranks below
+        // -infinity, as a choice and as a value: here -infinity is kLow, below every finite
+        // choice, and NaN -infinity.
+        constexpr double kLow = -1e300;
         const int size = s.n / s.groups;
         double* mine = group_lds + (size_t)wave * s.n;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int id = lane + i * kWave;
-            if (id < s.n) mine[id] = c[i] == c[i] ? c[i] : -INFINITY;
+            if (id < s.n) mine[id] = c[i] == c[i] ? fmax(c[i], kLow) : -INFINITY;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         int shift = 0;
@@ -400,8 +405,9 @@ __global__ __launch_bounds__(kGateWaves * kWave) void gate_scores_kernel(
             b = fmax(fmin(a, oa), fmax(b, ob));
             a = fmax(a, oa);
         }
+        const double last = s.top == 2 ? b : a;
         double value = s.top == 2 ? a + b : a;
-        if (value != value) value = -INFINITY;             // infinities of both signs
+        if (!(last > kLow)) value = last == kLow && a < INFINITY ? kLow : -INFINITY;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (group < s.groups) mine[group] = value;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
