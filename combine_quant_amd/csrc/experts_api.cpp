@@ -32,6 +32,26 @@ moe_status launched(hipError_t e, const char* what)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Whether two ranges of bytes share any (a NULL one shares none).
+bool overlap(const void* p, int64_t n, const void* q, int64_t m)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && (a < b ? b - a < (uintptr_t)n : a - b < (uintptr_t)m);
+}
+
+// The output of a product against everything that it reads, in bytes.
+moe_status check_overlap(const MatmulShape& s, const MatmulArgs& a, int64_t x, int64_t x_scales,
+                         int64_t w, int64_t w_scales)
+{
+    const int64_t out = s.cap * (s.swiglu ? s.out / 2 : s.out) * 2;
+    const int64_t counts = (int64_t)s.E * s.W * 4, offsets = (int64_t)(s.W + 1) * 8;
+    if (overlap(a.out, out, a.x, x) || overlap(a.out, out, a.x_scales, x_scales) ||
+        overlap(a.out, out, a.w, w) || overlap(a.out, out, a.w_scales, w_scales) ||
+        overlap(a.out, out, a.ep_recv_count, counts) || overlap(a.out, out, a.recv_offsets, offsets))
+        return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
+    return MOE_OK;
+}
+
 // The rules the two products share: the config, the sizes and the activation.
 moe_status check_matmul(const moe_dc_config* cfg, const moe_matmul* mm, MatmulShape* s)
 {
@@ -147,6 +167,11 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
         return fail(MOE_ERR_INVALID_ARG, "x_scales is required for MX rows");
     if (!aligned(x_scales, 4) || !aligned(weight_scales, 4))
         return fail(MOE_ERR_INVALID_ARG, "x_scales and weight_scales must be 4-byte aligned");
+    const int64_t xn = s.cap * s.in, wrows = (int64_t)s.E * s.out, wn = wrows * s.in;
+    const bool mx = mm->scaling == MOE_MM_SCALE_MX;
+    st = check_overlap(s, a, codes ? xn : xn * 2, mx ? xn / 32 : s.cap * 4, codes ? wn : wn * 2,
+                       mx ? wn / 32 : wrows * 4);
+    if (st != MOE_OK) return st;
     return launched(launch_grouped_matmul(s, a, static_cast<hipStream_t>(stream)),
                     "grouped matmul launch");
 }
@@ -179,6 +204,10 @@ moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm,
     if (!weight_scales) return fail(MOE_ERR_INVALID_ARG, "weight_scales is required");
     if (!aligned(weight_scales, 4))
         return fail(MOE_ERR_INVALID_ARG, "weight_scales must be 4-byte aligned");
+    const int64_t wn = (int64_t)s.E * s.out * s.in;
+    st = check_overlap(s, a, s.cap * s.in * 2, 0, wn / 2,
+                       wn / s.group * (mm->weight_dtype == MOE_W4_INT4 ? 2 : 1));
+    if (st != MOE_OK) return st;
     return launched(moe_dc::launch_grouped_matmul_w4(s, a, static_cast<hipStream_t>(stream)),
                     "4-bit grouped matmul launch");
 }
@@ -215,6 +244,11 @@ moe_status moe_gate_topk(const moe_dc_config* cfg, const moe_gate* gate, const f
         return fail(MOE_ERR_INVALID_ARG, "factor must be finite");
     if (!logits || !expert_ids || !expert_scales)
         return fail(MOE_ERR_INVALID_ARG, "a required tensor pointer is NULL");
+    const int64_t tokens = (int64_t)sh.W * sh.BS, outs = tokens * sh.K * 4;
+    if (overlap(expert_ids, outs, logits, tokens * n * 4) || overlap(expert_ids, outs, bias, n * 4) ||
+        overlap(expert_scales, outs, logits, tokens * n * 4) ||
+        overlap(expert_scales, outs, bias, n * 4) || overlap(expert_ids, outs, expert_scales, outs))
+        return fail(MOE_ERR_INVALID_ARG, "expert_ids or expert_scales overlaps another tensor");
     const moe_dc::GateShape s{sh.W * sh.BS, n, sh.K, gate->score == MOE_SCORE_SIGMOID ? 1 : 0,
                               g, gate->group_keep, gate->group_top, gate->renormalize,
                               gate->factor, (1u << 21) / (uint32_t)(n / g) + 1};

@@ -354,7 +354,8 @@ moe_status moe_combine_int8(const moe_dc_config* cfg, const int8_t* codes,
  * expert_scales that moe_dispatch and moe_combine take, and the products turn the packed rows
  * of expand_x into the rows of expert_out.  They follow the conventions at the top of this
  * header, except that x and weight must be 16-byte and their scales 4-byte aligned (there is
- * no element-wise fallback).  They need no workspace; each is one kernel. */
+ * no element-wise fallback), and that an output that overlaps another tensor of the same call is
+ * refused (MOE_ERR_INVALID_ARG).  They need no workspace; each is one kernel. */
 
 /* How the products' codes are scaled. */
 typedef enum {
