@@ -93,6 +93,17 @@ __device__ __forceinline__ uint32_t pack_out2(float lo, float hi, bool f16)
     return f16 ? __builtin_bit_cast(uint32_t, h) : __builtin_bit_cast(uint32_t, b);
 }
 
-__device__ __forceinline__ float silu(float t) { return t / (1.0f + __expf(-t)); }
+// silu(t) * u = t * u / (1 + exp(-t)).  Below t = -87 exp(-t) leaves the range of binary32, and the
+// quotient, that of its normal numbers, while times u it need not: numerator and denominator are
+// then both multiplied by 2^-126, and u by the numerator, which reaches to t = -176.
+__device__ __forceinline__ float silu_mul(float t, float u)
+{
+    const bool low = t < -87.0f;
+    const float shift = low ? -126.0f : 0.0f;
+    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(t, -1.44269504f, shift));
+    const float num = low ? t * 0x1p-126f * u : t;
+    const float q = num / (low ? e : 1.0f + e);
+    return low ? q : q * u;
+}
 
 }  // namespace moe_dc

@@ -134,7 +134,7 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int n = t * 16 + g * 4 + q;
-                const float y = s.swiglu ? silu(r[q]) * u[q] : r[q];
+                const float y = s.swiglu ? silu_mul(r[q], u[q]) : r[q];
                 if (n < left) o[n] = (uint16_t)f32_to_tok_rt(y, s.tok_f16);
             }
         }

@@ -285,7 +285,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                 if (SWIGLU) {
                     float u = (float)acc[m][1][q];
                     if (M::kRowScaled) u = u * ws_[1][q] * rs;
-                    r = silu(r) * u;
+                    r = silu_mul(r, u);
                 }
                 y[q] = r;
             }

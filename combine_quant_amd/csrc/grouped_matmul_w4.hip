@@ -130,7 +130,7 @@ __device__ __forceinline__ void w4_tile(const MatmulShape& s, const MatmulArgs& 
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int row = m * 16 + g * 4 + q;
-            const float y = s.swiglu ? silu(r[q]) * u[q] : r[q];
+            const float y = s.swiglu ? silu_mul(r[q], u[q]) : r[q];
             if (row < mrows && n < left)
                 static_cast<uint16_t*>(a.out)[(size_t)(row0 + row) * half + n0 + n] =
                     (uint16_t)f32_to_tok_rt(y, F16);

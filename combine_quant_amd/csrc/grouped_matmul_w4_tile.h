@@ -310,7 +310,7 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
             for (int r = 0; r < 4; ++r) {
                 const int row = m * 16 + g * 4 + r;
                 constexpr float unit = kCodeUnit<F16, E2M1>;
-                const float y = SWIGLU ? silu(acc[m][0][r] * unit) * (acc[m][1][r] * unit)
+                const float y = SWIGLU ? silu_mul(acc[m][0][r] * unit, acc[m][1][r] * unit)
                                        : acc[m][t][r] * unit;
                 if (row < tile.rows && c < left)
                     static_cast<uint16_t*>(a.out)[(size_t)(tile.row0 + row) * half + tile.n0 + c] =

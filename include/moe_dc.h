@@ -416,7 +416,8 @@ typedef struct {
  * I must be a multiple of 8 (tokens), 16 (ROW) or 128 (MX).
  * Numerics: products are exact; int8 sums are exact in 32 bits; the other sums are fp32 in an
  * order that depends on the sizes only (the same inputs give the same bytes); ROW scales
- * multiply the sum (weight's, then row's); out is rounded once, to nearest even.  The fp8
+ * multiply the sum (weight's, then row's); SwiGLU is within 2^-17 of its value for S[p][n] down
+ * to -176, below that 0; out is rounded once, to nearest even.  The fp8
  * matrix instructions add eight consecutive products at a time and drop, of each product, what
  * lies below 2^-13 of the largest one's power of two.  An infinity or NaN stays within its own
  * row (or weight row).
