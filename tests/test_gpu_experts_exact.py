@@ -500,3 +500,49 @@ def test_4bit_nonfinite_rows(token, bits, weight, group, counts, N, want):
     else:
         sign = torch.where(w[expert[bad], :, 20] & 8 > 0, -1.0, 1.0)
         assert torch.equal(out[bad].float(), sign * math.inf)
+
+
+# -- the least values of each type -----------------------------------------------------------------
+
+LEAST = {"bf16": 2.0 ** -133, "f16": 2.0 ** -24, "e4m3": 2.0 ** -9, "e5m2": 2.0 ** -16}
+
+
+@pytest.mark.parametrize("want", PATHS)
+@pytest.mark.parametrize("kind", [k for k in TYPES if k != "int8"] + ["int4", "e2m1", "int4_f16"])
+def test_subnormal_codes(kind, want):
+    """Rows of one to three times the type's least value, weights or scales that bring the sums
+    back into range: nothing is taken for 0, neither codes nor sums below binary32's normal range."""
+    E, BS, N = PATHS[want]
+    I, counts = 256, [20, 70, 0, 193] + [0] * (E - 4)
+    g = _gen(1)
+    w4 = {"int4": "int4", "e2m1": "e2m1", "int4_f16": "int4"}.get(kind)
+    rows_kind = kind if not w4 else "f16" if kind == "int4_f16" else "bf16"
+    elem = rows_kind.split("_")[-1]
+    cfg = cq.make_config(2, E, BS, 1024, 4, token_dtype=int(elem == "f16"))
+    assert path(rows_kind, cfg, N, False, w4) == want
+    erc, off, ranges = ref.pack_counts(counts, 2)
+    cap = cfg.expand_rows_capacity
+    x = (_whole((cap, I), -3, 3, g).double() * LEAST[elem]).to(CODES[elem])
+    xs, vx = None, x.double()
+    if w4:
+        w = torch.randint(0, 256, (E, N, I // 2), generator=g, device=DEV, dtype=torch.uint8)
+        ws = (torch.full((E, N, I // 32), 247, dtype=torch.uint8, device=DEV) if w4 == "e2m1" else
+              torch.full((E, N, I // 32), 2.0 ** (120 if elem == "bf16" else 14), device=DEV).to(x.dtype))
+        vw = ref.w4_to_f64(w, ws, w4, 32)
+        out = cq.grouped_matmul_w4(cfg, cq.make_matmul(I, N, weight_dtype=W4_DTYPE[w4], group_size=32), x, w, ws,
+                                   erc.to(DEV), off.to(DEV))
+    else:
+        wtype = "e4m3" if elem == "e5m2" else elem
+        least = {"bf16": 2.0 ** 120, "f16": 2.0 ** 10, "e4m3": 2.0 ** -9}[wtype]
+        w = (_whole((E, N, I), -3, 3, g).double() * least).to(CODES[wtype])
+        ws = None
+        if kind.startswith("mx"):
+            xs = torch.full((cap, I // 32), 137, dtype=torch.uint8, device=DEV)
+            ws = torch.full((E, N, I // 32), 137, dtype=torch.uint8, device=DEV)
+        elif elem in ("e4m3", "e5m2"):
+            xs, ws = torch.full((cap,), 1024.0, device=DEV), torch.full((E, N), 1024.0, device=DEV)
+        vx, vw = ref.codes_to_f64(x, xs), ref.codes_to_f64(w, ws)
+        out = cq.grouped_matmul(cfg, _desc(kind, I, N, False), x, w, erc.to(DEV), off.to(DEV), x_scales=xs,
+                                weight_scales=ws)
+    for e, (lo, hi) in enumerate(ranges):
+        assert torch.equal(out[lo:hi], (vx[lo:hi] @ vw[e].t()).float().to(out.dtype)), e
