@@ -131,11 +131,11 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
         }
         if (row < mrows) {
             uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)(row0 + row) * half + n0;
+            if (s.swiglu) silu_mul4(r, u, r);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int n = t * 16 + g * 4 + q;
-                const float y = s.swiglu ? silu_mul(r[q], u[q]) : r[q];
-                if (n < left) o[n] = (uint16_t)f32_to_tok_rt(y, s.tok_f16);
+                if (n < left) o[n] = (uint16_t)f32_to_tok_rt(r[q], s.tok_f16);
             }
         }
     }

@@ -277,18 +277,17 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
             const int c = c0 + t * 16;
-            float y[4];
+            float y[4], u[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float r = (float)acc[m][t][q];
-                if (M::kRowScaled) r = r * ws_[t][q] * rs;
+                y[q] = (float)acc[m][t][q];
+                if (M::kRowScaled) y[q] = y[q] * ws_[t][q] * rs;
                 if (SWIGLU) {
-                    float u = (float)acc[m][1][q];
-                    if (M::kRowScaled) u = u * ws_[1][q] * rs;
-                    r = silu_mul(r, u);
+                    u[q] = (float)acc[m][1][q];
+                    if (M::kRowScaled) u[q] = u[q] * ws_[1][q] * rs;
                 }
-                y[q] = r;
             }
+            if (SWIGLU) silu_mul4(y, u, y);
             const uint2 p = make_uint2(pack_out2(y[0], y[1], s.tok_f16), pack_out2(y[2], y[3], s.tok_f16));
             store_columns(o, c, left, p);
         }

@@ -127,13 +127,15 @@ __device__ __forceinline__ void w4_tile(const MatmulShape& s, const MatmulArgs& 
         const int n = t * 16 + l16;
         r *= unit;
         u *= unit;
+        float y[4] = {r[0], r[1], r[2], r[3]};
+        const float up[4] = {u[0], u[1], u[2], u[3]};
+        if (s.swiglu) silu_mul4(y, up, y);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int row = m * 16 + g * 4 + q;
-            const float y = s.swiglu ? silu_mul(r[q], u[q]) : r[q];
             if (row < mrows && n < left)
                 static_cast<uint16_t*>(a.out)[(size_t)(row0 + row) * half + n0 + n] =
-                    (uint16_t)f32_to_tok_rt(y, F16);
+                    (uint16_t)f32_to_tok_rt(y[q], F16);
         }
     }
     __syncthreads();

@@ -306,15 +306,20 @@ __device__ __forceinline__ void w4_tile_product(const MatmulShape& s, const Matm
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
             const int c = wave * (kT * 16) + t * 16 + l16;
+            constexpr float unit = kCodeUnit<F16, E2M1>;
+            float y[4], u[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                y[r] = acc[m][t][r] * unit;
+                u[r] = acc[m][1][r] * unit;
+            }
+            if (SWIGLU) silu_mul4(y, u, y);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = m * 16 + g * 4 + r;
-                constexpr float unit = kCodeUnit<F16, E2M1>;
-                const float y = SWIGLU ? silu_mul(acc[m][0][r] * unit, acc[m][1][r] * unit)
-                                       : acc[m][t][r] * unit;
                 if (row < tile.rows && c < left)
                     static_cast<uint16_t*>(a.out)[(size_t)(tile.row0 + row) * half + tile.n0 + c] =
-                        (uint16_t)pack_out2(y, 0.0f, F16);
+                        (uint16_t)pack_out2(y[r], 0.0f, F16);
             }
         }
 }

@@ -51,3 +51,22 @@ def test_gates_over_the_whole_range(E, BS, want, w4):
         assert torch.equal(row[over], y[over].sign() * math.inf)
         bad = (row - y).abs()[~over] > tol[~over]
         assert not bad.any(), [pairs[i] for i in (~over).nonzero().flatten()[bad].tolist()]
+
+
+@pytest.mark.parametrize("E,BS,want", [(4, 20, "stream"), (64, 20, "tiles")])
+def test_a_row_beside_rows_with_low_gates(E, BS, want):
+    cfg = cq.make_config(2, E, BS, 1024, 4)
+    N, I = 420, 128
+    assert path("bf16", cfg, N, True) == want
+    g = torch.Generator(device=DEV).manual_seed(2)
+    erc, off, _ = ref.pack_counts([17, 0, 2] + [0] * (E - 3), 2)
+    x = torch.randn((cfg.expand_rows_capacity, I), generator=g, device=DEV).bfloat16()
+    x[:, 0] = 0
+    w = torch.randn((E, N, I), generator=g, device=DEV).bfloat16()
+    w[:, :, 0] = -100.0
+    mm = cq.make_matmul(I, N, activation=cq.MOE_ACT_SWIGLU)
+    plain = cq.grouped_matmul(cfg, mm, x, w, erc.to(DEV), off.to(DEV)).clone()
+    x[3, 0] = 1.0
+    out = cq.grouped_matmul(cfg, mm, x, w, erc.to(DEV), off.to(DEV))
+    keep = [r for r in range(19) if r != 3]
+    assert torch.equal(out[keep], plain[keep]) and not torch.equal(out[3], plain[3])
