@@ -39,11 +39,14 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m)
     return p && q && (a < b ? b - a < (uintptr_t)n : a - b < (uintptr_t)m);
 }
 
+// The rows that a product may touch.
+int64_t touched(const MatmulShape& s) { return s.rows < s.cap ? s.rows : s.cap; }
+
 // The output of a product against everything that it reads, in bytes.
 moe_status check_overlap(const MatmulShape& s, const MatmulArgs& a, int64_t x, int64_t x_scales,
                          int64_t w, int64_t w_scales)
 {
-    const int64_t out = s.cap * (s.swiglu ? s.out / 2 : s.out) * 2;
+    const int64_t out = touched(s) * (s.swiglu ? s.out / 2 : s.out) * 2;
     const int64_t counts = (int64_t)s.E * s.W * 4, offsets = (int64_t)(s.W + 1) * 8;
     if (overlap(a.out, out, a.x, x) || overlap(a.out, out, a.x_scales, x_scales) ||
         overlap(a.out, out, a.w, w) || overlap(a.out, out, a.w_scales, w_scales) ||
@@ -167,9 +170,9 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
         return fail(MOE_ERR_INVALID_ARG, "x_scales is required for MX rows");
     if (!aligned(x_scales, 4) || !aligned(weight_scales, 4))
         return fail(MOE_ERR_INVALID_ARG, "x_scales and weight_scales must be 4-byte aligned");
-    const int64_t xn = s.cap * s.in, wrows = (int64_t)s.E * s.out, wn = wrows * s.in;
+    const int64_t rows = touched(s), xn = rows * s.in, wrows = (int64_t)s.E * s.out, wn = wrows * s.in;
     const bool mx = mm->scaling == MOE_MM_SCALE_MX;
-    st = check_overlap(s, a, codes ? xn : xn * 2, mx ? xn / 32 : s.cap * 4, codes ? wn : wn * 2,
+    st = check_overlap(s, a, codes ? xn : xn * 2, mx ? xn / 32 : rows * 4, codes ? wn : wn * 2,
                        mx ? wn / 32 : wrows * 4);
     if (st != MOE_OK) return st;
     return launched(launch_grouped_matmul(s, a, static_cast<hipStream_t>(stream)),
@@ -205,7 +208,7 @@ moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm,
     if (!aligned(weight_scales, 4))
         return fail(MOE_ERR_INVALID_ARG, "weight_scales must be 4-byte aligned");
     const int64_t wn = (int64_t)s.E * s.out * s.in;
-    st = check_overlap(s, a, s.cap * s.in * 2, 0, wn / 2,
+    st = check_overlap(s, a, touched(s) * s.in * 2, 0, wn / 2,
                        wn / s.group * (mm->weight_dtype == MOE_W4_INT4 ? 2 : 1));
     if (st != MOE_OK) return st;
     return launched(moe_dc::launch_grouped_matmul_w4(s, a, static_cast<hipStream_t>(stream)),

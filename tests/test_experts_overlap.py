@@ -50,6 +50,17 @@ def test_product_in_place():
     _refused(_product(_cfg(), cq.make_matmul(128, 128), p))
 
 
+def test_rows_beyond_any_batch_do_not_count():
+    """A capacity above W * BS * K does not make buffers that hold the batch's rows overlap: the call
+    gets past the checks (and, without a GPU, no further)."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("host rule; the pointers are not a GPU's")
+    cfg = _cfg()
+    cfg.expand_rows_capacity = (1 << 31) - 1
+    assert _product(cfg, cq.make_matmul(128, 96), _apart(TOKENS)) == cq.MOE_ERR_DEVICE
+
+
 @pytest.mark.parametrize("which", ["xs", "ws"])
 @pytest.mark.parametrize("kind", ["row", "mx"])
 def test_product_output_and_scales(which, kind):
