@@ -31,8 +31,7 @@ struct TileStages {
     char w[kTileWaves][2][32 * 128];            // each wave's own 32 weight rows, swizzled
     // MX: the E8M0 bytes of four steps, 16 of each row of x, then of each weight row (with the
     // four bytes of one step at a time the requests for them outnumbered the rows': 3.45 ms
-    // instead of 2.63 at 65536 skewed rows on 256 experts x 7168 x 4096).  A row's last window
-    // may hold fewer steps: then [64 rows' block][step][row][4 bytes]
+    // instead of 2.63 at 65536 skewed rows on 256 experts x 7168 x 4096)
     char scales[2][Mm<TYPE>::kMx ? (kTileM<TYPE> + kTileN) * 16 : 0];
 };
 
@@ -113,25 +112,35 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         sx ? static_cast<const char*>(a.x_scales) + (size_t)row0 * ns : wsb,
         !M::kMx ? 0 : (uint32_t)(sx ? rows : SWIGLU ? half + left : left) * ns);
     const int sto = (sx ? 0 : kTileM<TYPE> * 16) + sblk * 1024;
-    const auto fetch_scales = [&](int window) {
+    // The 16 bytes of a row's last window end where the row does (from the window's own start they
+    // would run into the next row and, of the last row, past the tensor), so that its steps lie
+    // scale_shift bytes further; a row of fewer than 16 bytes comes a step's dword at a time, as
+    // [64 rows' block][step][row][4 bytes].
+    const auto scale_shift = [&](int window) {
         const uint32_t k = (uint32_t)window * 16;
+        return k < ns && k + 16 > ns ? (int)(k + 16 - ns) : 0;
+    };
+    const auto fetch_scales = [&](int window) {
+        const uint32_t k = (uint32_t)(window * 16 - scale_shift(window));
         char* to = lds.scales[window & 1] + sto;
-        if (k < ns && k + 16 > ns) {
-            // the rest of the row a step's dword at a time: 16 bytes would reach into the next
-            // row and, of the last row, past the tensor
-#pragma unroll
-            for (uint32_t j = 0; j < 3; ++j)
-                load_lds4(sr, to + j * 256, sok && k + j * 4 < ns ? soff + k + j * 4 : kRsrcPastEnd);
-        } else {
+        if (ns >= 16) {
             load_lds16(sr, to, sok && k < ns ? soff + k : kRsrcPastEnd);
+        } else if (window == 0) {
+#pragma unroll
+            for (uint32_t d = 0; d < 12; d += 4)
+                load_lds4(sr, to + d * 64, sok && d < ns ? soff + d : kRsrcPastEnd);
         }
     };
-    // Byte of the scales of a step (0..3 in its window) of row r + l16, in a full window or a
-    // row's last part (r a multiple of 16, known at compile time but for the wave's rows).
-    const int sfull = l16 * 16 + g, spart = l16 * 4 + g;
-    const auto scale_byte = [&](bool part, int in_window, int r) {
-        return part ? spart + (r >> 6) * 1024 + in_window * 256 + (r & 63) * 4
-                    : sfull + r * 16 + in_window * 4;
+    // The scale of a step for row r + l16 (r a multiple of 16).  Steps of windows known to be
+    // full need no shift; only those after the unrolled loop may be of rows below 16 bytes.
+    enum Where { kFull, kPerhapsLast, kAfterLoop };
+    const auto scale_of = [&](Where where, int step, int r) {
+        const char* to = lds.scales[step >> 2 & 1];
+        const int k = step & 3;
+        if (where == kAfterLoop && ns < 16)
+            return (int)*reinterpret_cast<const uint8_t*>(to + (r >> 6) * 1024 + k * 256 + ((r & 63) + l16) * 4 + g);
+        if (where != kFull) to += scale_shift(step >> 2);
+        return (int)*reinterpret_cast<const uint8_t*>(to + (r + l16) * 16 + k * 4 + g);
     };
     // Load i of a step's x, and of its weights.
     const auto fetch_x = [&](int step, int i) {
@@ -151,15 +160,13 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     const int f1 = l16 * 128 + (((4 + g) ^ (l16 & 7)) << 4);
     v8i_t w[2][2];
     int wsc[2][2] = {{0, 0}, {0, 0}};
-    const auto read_w = [&](int par, int step, bool part) {
+    const auto read_w = [&](int par, int step, Where where) {
         const char* wl = lds.w[wave][par];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             w[par][t] = join(*reinterpret_cast<const v4i_t*>(wl + t * 2048 + f0),
                              *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f1));
-            if (M::kMx)
-                wsc[par][t] = *reinterpret_cast<const uint8_t*>(
-                    lds.scales[step >> 2 & 1] + scale_byte(part, step & 3, kTileM<TYPE> + wave * 32 + t * 16));
+            if (M::kMx) wsc[par][t] = scale_of(where, step, kTileM<TYPE> + wave * 32 + t * 16);
         }
     };
     Acc acc[MT][2];
@@ -183,7 +190,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     all_x(1);
     wait_loads<kAhead>();
     if (M::kMx) meet();                         // the scales come from other waves
-    read_w(0, 0, steps < 4);
+    read_w(0, 0, kAfterLoop);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     all_w(2);
     // A step's products go in groups of 32 rows (the last one perhaps 16): a group reads the next
@@ -197,13 +204,12 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     constexpr int kXGroups = kGroups > 1 ? kGroups / 2 : 1;
     constexpr int kWFirst = kGroups > 1 ? kGroups / 2 : 0, kWGroups = kGroups - kWFirst;
     constexpr int kReadW = kWFirst >= 2 ? kWFirst - 2 : 0;
-    // phase: step modulo the unrolling; part: the steps after the last full window
-    const auto one = [&](int phase, int step, bool part) {
+    // phase: step modulo the unrolling
+    const auto one = [&](int phase, int step, Where where) {
         const int par = phase & 1;
         wait_loads<kAhead>();
         meet();
         const char* xl = lds.x[step % kTileRing];
-        const char* xsl = lds.scales[step >> 2 & 1];
         if (M::kMx && phase == 0) fetch_scales((step >> 2) + 1);
         v8i_t x[2][2];
         int xsv[2][2] = {{0, 0}, {0, 0}};
@@ -214,15 +220,15 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                 if (m >= MT) break;
                 x[set][i] = join(*reinterpret_cast<const v4i_t*>(xl + m * 2048 + f0),
                                  *reinterpret_cast<const v4i_t*>(xl + m * 2048 + f1));
-                if (M::kMx) xsv[set][i] = *reinterpret_cast<const uint8_t*>(xsl + scale_byte(part, phase, m * 16));
+                if (M::kMx) xsv[set][i] = scale_of(where, step, m * 16);
             }
         };
         read_x(0, 0);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
             if (q == kReadW) {
-                read_w(par ^ 1, step + 1, part || (phase == 3 && step + 5 > steps));
-                __builtin_amdgcn_sched_barrier(0);           // before read_x(q + 1), see kReadW
+                read_w(par ^ 1, step + 1, where == kFull && phase == 3 ? kPerhapsLast : where);
+                __builtin_amdgcn_sched_barrier(0x7F);        // LDS reads stay before read_x(q + 1)
             }
             if (q + 1 < kGroups) read_x((q + 1) & 1, q + 1);
             if (q == kWFirst && kWFirst < kReadW + 2)
@@ -247,11 +253,11 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     int step = 0;
     for (; step + kUnroll <= steps; step += kUnroll) {
 #pragma unroll
-        for (int r = 0; r < kUnroll; ++r) one(r, step + r, false);
+        for (int r = 0; r < kUnroll; ++r) one(r, step + r, kFull);
     }
 #pragma unroll
     for (int r = 0; r < kUnroll - 1; ++r)
-        if (step + r < steps) one(r, step + r, true);
+        if (step + r < steps) one(r, step + r, kAfterLoop);
     wait_loads<0>();                            // nothing may land in LDS after the tile
 
     constexpr int kT = SWIGLU ? 1 : 2;
