@@ -30,9 +30,10 @@ namespace {
 
 constexpr int kGateWaves = 4;
 constexpr int kGateMaxIds = 2048;
-// Tokens from which a wave serves four (16384 x 516, K = 16: 33 us, against 52 with a wave each;
-// below, waves would be too few for the CUs).
-constexpr int kGateQuarterTokens = 2048;
+// Tokens from which a wave serves four; below, the waves are too few for the CUs.  With a wave
+// each and with four to a wave: 2048 x 256, K = 8, 8.4 and 9.4 us, 4096 x 256 11.5 and 9.8; 2048 x
+// 516, K = 16, 13.5 and 16.6, 4096 x 516 19.8 and 18.6, 16384 x 516 50 and 31.
+constexpr int kGateQuarterTokens = 4096;
 // Order-preserving keys: 0 is kept for ids out of play, 1 for NaN.
 __device__ __forceinline__ uint32_t choice_key(float f)
 {
@@ -527,6 +528,10 @@ hipError_t launch_gate_topk(const GateShape& s, const float* logits, const float
                             int32_t* expert_ids, float* expert_scales, hipStream_t stream)
 {
     static_assert(kGateWaves * kGateMaxIds * sizeof(double) <= 65536, "LDS of a workgroup");
+    // An id more than a kernel holds takes the next one, of more ids per lane: 8192 tokens with a
+    // bias, K = 8, 256 ids 12.1 us, 257 17.1, 640 21.6, 641 26.4, 1024 30.9, 1025 45.2; without,
+    // K = 16, 576 20.8 (16 lanes a token), 577 29.8 (64); 128 tokens 256 6.8, 257 8.4, 1025 11.4.
+    // 640 and 576 leave room for special ids beside 512 experts.
     if (bias || (s.groups > 1 && s.top == 2)) {
         if (s.n <= 256) return launch_scores<4>(s, logits, bias, expert_ids, expert_scales, stream);
         if (s.n <= 640) return launch_scores<10>(s, logits, bias, expert_ids, expert_scales, stream);

@@ -46,7 +46,7 @@ def _rows(groups, size):
 
 
 @pytest.mark.parametrize("groups,size", [(4, 16), (8, 32), (6, 10), (3, 128)])
-@pytest.mark.parametrize("repeat", [1, 130])                         # a wave a token, and four
+@pytest.mark.parametrize("repeat", [1, 130, 260])                    # a wave a token, and four
 @pytest.mark.parametrize("keep", [1, 2])
 def test_by_the_best_logit(groups, size, repeat, keep):
     z = _rows(groups, size)
