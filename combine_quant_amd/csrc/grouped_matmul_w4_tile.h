@@ -11,11 +11,12 @@
 // decodes the codes of the next one to 16-bit floats in registers, a part with each part of its
 // own products, so that the conversions run beside the matrix instructions.
 //
-// Few rows are bound by the instructions that turn codes into operands, above the bytes: 16 rows
-// on 16 of 64 experts x 7168 x 4096 int4 (227 MB) take 53 us, 32 experts with 16 rows each (493
-// MB) 141 us, 3.5 TB/s.  With many rows the matrix units are the bound:
-// 4096 rows on 32 experts x 2048 x 7168 E2M1 take 200 us, 600 Tflop/s, of which 10 us a tile are
-// its start and end, as inner size 2048 is only 16 steps; at 8192 it is 740 Tflop/s.
+// Few rows are bound by the instructions that turn codes into operands (155 a wave and step),
+// above the bytes: 16 rows on 16 of 64 experts x 7168 x 4096 int4 (227 MB) take 53 us with the same
+// weights again, 62 with others between, 32 experts with 16 rows each (493 MB) 131 us, 3.8 TB/s.
+// With many rows the matrix units are the bound, but with 128 rows a weight's decoding serves few
+// products, and a tile's start and end take 10 us: 4096 rows on 32 experts x 2048 x 7168 E2M1 take
+// 186-192 us, 640 Tflop/s (16 steps a tile); at inner size 8192 it is 760, int4 at 4096 670.
 //
 // x is the A operand (rows of the result) and the weights B (columns): lane l holds column l % 16
 // and rows (l / 16) * 4 + 0..3, hence one scale per lane and column tile.
