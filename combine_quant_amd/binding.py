@@ -21,7 +21,7 @@ MOE_SCALES_NONE, MOE_SCALES_SCALAR, MOE_SCALES_SHARED, MOE_SCALES_PER_EXPERT = 0
 MOE_SCALE_FP32, MOE_SCALE_E8M0, MOE_SCALE_FP32_RECIPROCAL = 0, 1, 2
 MOE_DC_FLAG_SEPARATE_ROUTE, MOE_DC_FLAG_CHECK_IDS = 1, 2
 MOE_TOKEN_BF16, MOE_TOKEN_F16 = 0, 1
-MOE_MM_SCALE_NONE, MOE_MM_SCALE_ROW, MOE_MM_SCALE_MX = 0, 1, 2
+MOE_MM_SCALE_NONE, MOE_MM_SCALE_ROW, MOE_MM_SCALE_MX, MOE_MM_SCALE_BLOCK = 0, 1, 2, 3
 MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 MOE_W4_INT4, MOE_W4_E2M1 = 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
@@ -32,7 +32,8 @@ EXPORTS = ("moe_dc_validate", "moe_dc_scales_per_row", "moe_dc_dispatch_workspac
            "moe_dc_combine_scatter_workspace_bytes", "moe_dispatch",
            "moe_dispatch_no_workspace", "moe_combine",
            "moe_combine_scatter", "moe_combine_quantize", "moe_combine_int8",
-           "moe_gate_topk", "moe_grouped_matmul", "moe_grouped_matmul_w4",
+           "moe_gate_topk", "moe_grouped_matmul", "moe_grouped_matmul_quantize",
+           "moe_grouped_matmul_w4",
            "moe_dc_last_error", "moe_dc_version")
 
 
@@ -138,6 +139,8 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     mmp, gatep = ctypes.POINTER(MoeMatmul), ctypes.POINTER(MoeGate)
     lib.moe_grouped_matmul.restype = ctypes.c_int
     lib.moe_grouped_matmul.argtypes = [cfgp, mmp] + [P] * 7 + [P]
+    lib.moe_grouped_matmul_quantize.restype = ctypes.c_int
+    lib.moe_grouped_matmul_quantize.argtypes = [cfgp, mmp, ctypes.c_int32] + [P] * 8 + [P]
     lib.moe_grouped_matmul_w4.restype = ctypes.c_int
     lib.moe_grouped_matmul_w4.argtypes = [cfgp, mmp] + [P] * 6 + [P]
     lib.moe_gate_topk.restype = ctypes.c_int
@@ -476,23 +479,39 @@ def _routed_rows(cfg, ep_recv_count, recv_offsets, dev):
             _ptr(recv_offsets, torch.int64, (cfg.ep_world_size + 1,), "recv_offsets", dev)]
 
 
-def _grouped_matmul_call(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales,
-                         weight_scales, out):
+def _groups(n):
+    """Scales of n elements in groups of 128."""
+    return (n + 127) // 128
+
+
+def _product_inputs(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales, weight_scales, dev):
     E, cap, I, N = cfg.moe_expert_num, cfg.expand_rows_capacity, mm.in_features, mm.out_features
-    dev, token = out.device, token_torch_dtype(cfg)
+    token = token_torch_dtype(cfg)
     tokens = mm.x_dtype == MOE_DTYPE_DEFAULT
     wtype = token if tokens else _ROW_DTYPES.get(
         MOE_DTYPE_E4M3 if mm.x_dtype == MOE_DTYPE_E5M2 else mm.x_dtype)
     sdt, xshape, wshape = torch.float32, (cap,), (E, N)
     if mm.scaling == MOE_MM_SCALE_MX:
         sdt, xshape, wshape = torch.uint8, (cap, I // 32), (E, N, I // 32)
-    args = [
+    elif mm.scaling == MOE_MM_SCALE_BLOCK:
+        parts = 2 if mm.activation == MOE_ACT_SWIGLU else 1
+        xshape, wshape = (cap, _groups(I)), (E, parts * _groups(N // parts), _groups(I))
+    return [
         _ptr(x, token if tokens else _ROW_DTYPES.get(mm.x_dtype), (cap, I), "x", dev),
         _ptr(x_scales, sdt, xshape, "x_scales", dev),
         _ptr(weight, wtype, (E, N, I), "weight", dev),
         _ptr(weight_scales, sdt, wshape, "weight_scales", dev),
         *_routed_rows(cfg, ep_recv_count, recv_offsets, dev),
-        _ptr(out, token, (cap, _out_columns(mm)), "out", dev),
+    ]
+
+
+def _grouped_matmul_call(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales,
+                         weight_scales, out):
+    dev = out.device
+    args = [
+        *_product_inputs(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales, weight_scales,
+                         dev),
+        _ptr(out, token_torch_dtype(cfg), (cfg.expand_rows_capacity, _out_columns(mm)), "out", dev),
     ]
     return load_library().moe_grouped_matmul, (ctypes.byref(cfg), ctypes.byref(mm), *args), dev
 
@@ -502,6 +521,27 @@ def moe_grouped_matmul(cfg, mm, x, x_scales, weight, weight_scales, ep_recv_coun
     """Enqueue one product of the packed rows with their experts' weights on `stream`."""
     _launch(*_grouped_matmul_call(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales,
                                   weight_scales, out), stream)
+
+
+def _grouped_matmul_quantize_call(cfg, mm, out_dtype, x, x_scales, weight, weight_scales,
+                                  ep_recv_count, recv_offsets, codes, out_scales):
+    cap, M, dev = cfg.expand_rows_capacity, _out_columns(mm), codes.device
+    args = [
+        *_product_inputs(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales, weight_scales,
+                         dev),
+        _ptr(codes, _ROW_DTYPES.get(out_dtype), (cap, M), "codes", dev),
+        _ptr(out_scales, torch.float32, (cap, _groups(M)), "out_scales", dev),
+    ]
+    return (load_library().moe_grouped_matmul_quantize,
+            (ctypes.byref(cfg), ctypes.byref(mm), ctypes.c_int32(out_dtype), *args), dev)
+
+
+def moe_grouped_matmul_quantize(cfg, mm, out_dtype, x, x_scales, weight, weight_scales,
+                                ep_recv_count, recv_offsets, codes, out_scales, stream=None):
+    """Enqueue one product of block-scaled rows on `stream`, its results coded with one scale per
+    row and 128 columns."""
+    _launch(*_grouped_matmul_quantize_call(cfg, mm, out_dtype, x, x_scales, weight, weight_scales,
+                                           ep_recv_count, recv_offsets, codes, out_scales), stream)
 
 
 def _grouped_matmul_w4_call(cfg, mm, x, weight, weight_scales, ep_recv_count, recv_offsets, out):
@@ -711,6 +751,29 @@ def grouped_matmul(cfg, mm, x, weight, ep_recv_count, recv_offsets, x_scales=Non
     [cap][N/2] with SwiGLU; rows at or past recv_offsets[W] are not written)."""
     launch, out = prepare_grouped_matmul(cfg, mm, x, weight, ep_recv_count, recv_offsets,
                                          x_scales, weight_scales, out)
+    launch(stream)
+    return out
+
+
+def prepare_grouped_matmul_quantize(cfg, mm, out_dtype, x, x_scales, weight, weight_scales,
+                                    ep_recv_count, recv_offsets, out=None):
+    """Plan for moe_grouped_matmul_quantize: (launch, (codes, out_scales))."""
+    if out is None:
+        cap, M = cfg.expand_rows_capacity, _out_columns(mm)
+        out = (torch.empty((cap, M), dtype=torch.uint8, device=x.device),
+               torch.empty((cap, _groups(M)), dtype=torch.float32, device=x.device))
+    fn, args, dev = _grouped_matmul_quantize_call(cfg, mm, out_dtype, x, x_scales, weight,
+                                                  weight_scales, ep_recv_count, recv_offsets, *out)
+    keep = (cfg, mm, x, x_scales, weight, weight_scales, ep_recv_count, recv_offsets, out)
+    return Launch(fn, args, dev, keep), out
+
+
+def grouped_matmul_quantize(cfg, mm, out_dtype, x, x_scales, weight, weight_scales, ep_recv_count,
+                            recv_offsets, out=None, stream=None):
+    """Allocate (or reuse `out` = (codes, out_scales)) and enqueue moe_grouped_matmul_quantize;
+    returns out, as a block-scaled product takes it (x and x_scales)."""
+    launch, out = prepare_grouped_matmul_quantize(cfg, mm, out_dtype, x, x_scales, weight,
+                                                  weight_scales, ep_recv_count, recv_offsets, out)
     launch(stream)
     return out
 

@@ -42,16 +42,25 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m)
 // The rows that a product may touch.
 int64_t touched(const MatmulShape& s) { return s.rows < s.cap ? s.rows : s.cap; }
 
-// The output of a product against everything that it reads, in bytes.
+// Scales of `n` elements in groups of 128.
+int64_t groups_of(int64_t n) { return (n + moe_dc::kBlock - 1) / moe_dc::kBlock; }
+
+// The outputs of a product against each other and everything that it reads, in bytes.
 moe_status check_overlap(const MatmulShape& s, const MatmulArgs& a, int64_t x, int64_t x_scales,
                          int64_t w, int64_t w_scales)
 {
-    const int64_t out = touched(s) * (s.swiglu ? s.out / 2 : s.out) * 2;
+    const int64_t cols = s.swiglu ? s.out / 2 : s.out;
+    const int64_t out = touched(s) * cols * (s.out_code ? 1 : 2);
+    const int64_t scales = touched(s) * groups_of(cols) * 4;
     const int64_t counts = (int64_t)s.E * s.W * 4, offsets = (int64_t)(s.W + 1) * 8;
-    if (overlap(a.out, out, a.x, x) || overlap(a.out, out, a.x_scales, x_scales) ||
-        overlap(a.out, out, a.w, w) || overlap(a.out, out, a.w_scales, w_scales) ||
-        overlap(a.out, out, a.ep_recv_count, counts) || overlap(a.out, out, a.recv_offsets, offsets))
-        return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
+    const struct { const void* p; int64_t n; } outs[2] = {{a.out, out}, {a.out_scales, scales}};
+    for (const auto& o : outs)
+        if (overlap(o.p, o.n, a.x, x) || overlap(o.p, o.n, a.x_scales, x_scales) ||
+            overlap(o.p, o.n, a.w, w) || overlap(o.p, o.n, a.w_scales, w_scales) ||
+            overlap(o.p, o.n, a.ep_recv_count, counts) || overlap(o.p, o.n, a.recv_offsets, offsets))
+            return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
+    if (overlap(a.out, out, a.out_scales, scales))
+        return fail(MOE_ERR_INVALID_ARG, "codes and out_scales overlap");
     return MOE_OK;
 }
 
@@ -83,6 +92,7 @@ moe_status check_matmul(const moe_dc_config* cfg, const moe_matmul* mm, MatmulSh
     s->type = sh.tok_f16 ? moe_dc::kMmF16 : moe_dc::kMmBf16;
     s->w4 = 0;
     s->group = 0;
+    s->out_code = 0;
     s->rows = (int64_t)sh.W * sh.BS * sh.K;
     s->cap = sh.cap;
     return MOE_OK;
@@ -97,7 +107,9 @@ hipError_t launch_grouped_matmul(const MatmulShape& s, const MatmulArgs& a, hipS
     case moe_dc::kMmE4m3: return moe_dc::launch_grouped_e4m3(s, a, stream);
     case moe_dc::kMmE5m2: return moe_dc::launch_grouped_e5m2(s, a, stream);
     case moe_dc::kMmMxE4m3: return moe_dc::launch_grouped_mxe4m3(s, a, stream);
-    default: return moe_dc::launch_grouped_mxe5m2(s, a, stream);
+    case moe_dc::kMmMxE5m2: return moe_dc::launch_grouped_mxe5m2(s, a, stream);
+    case moe_dc::kMmBlockE4m3: return moe_dc::launch_grouped_block_e4m3(s, a, stream);
+    default: return moe_dc::launch_grouped_block_e5m2(s, a, stream);
     }
 }
 
@@ -110,22 +122,20 @@ moe_status check_pointers(const MatmulArgs& a)
     return MOE_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, const void* x,
-                              const void* x_scales, const void* weight,
-                              const void* weight_scales, const int32_t* ep_recv_count,
-                              const int64_t* recv_offsets, void* out, void* stream)
+// moe_grouped_matmul, with tokens in `out`, or moe_grouped_matmul_quantize, with codes of out_code
+// and out_scales.
+moe_status grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, const void* x, const void* x_scales,
+                          const void* weight, const void* weight_scales, const int32_t* ep_recv_count,
+                          const int64_t* recv_offsets, int32_t out_code, void* out, float* out_scales,
+                          void* stream)
 {
     MatmulShape s;
     moe_status st = check_matmul(cfg, mm, &s);
     if (st != MOE_OK) return st;
     if (mm->weight_dtype != 0 || mm->group_size != 0)
         return fail(MOE_ERR_INVALID_ARG, "weight_dtype and group_size belong to the 4-bit product");
-    if (mm->scaling < MOE_MM_SCALE_NONE || mm->scaling > MOE_MM_SCALE_MX)
-        return fail(MOE_ERR_INVALID_ARG, "scaling %d is not one of 0..2", mm->scaling);
+    if (mm->scaling < MOE_MM_SCALE_NONE || mm->scaling > MOE_MM_SCALE_BLOCK)
+        return fail(MOE_ERR_INVALID_ARG, "scaling %d is not one of 0..3", mm->scaling);
     const bool codes = mm->x_dtype != MOE_DTYPE_DEFAULT;
     int32_t step = 8;
     switch (mm->x_dtype) {
@@ -142,9 +152,12 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
     case MOE_DTYPE_E4M3:
     case MOE_DTYPE_E5M2:
         if (mm->scaling == MOE_MM_SCALE_NONE)
-            return fail(MOE_ERR_INVALID_ARG, "fp8 rows need scaling MOE_MM_SCALE_ROW or _MX");
+            return fail(MOE_ERR_INVALID_ARG, "fp8 rows need scaling MOE_MM_SCALE_ROW, _MX or _BLOCK");
         if (mm->scaling == MOE_MM_SCALE_ROW) {
             s.type = mm->x_dtype == MOE_DTYPE_E4M3 ? moe_dc::kMmE4m3 : moe_dc::kMmE5m2;
+            step = 16;
+        } else if (mm->scaling == MOE_MM_SCALE_BLOCK) {
+            s.type = mm->x_dtype == MOE_DTYPE_E4M3 ? moe_dc::kMmBlockE4m3 : moe_dc::kMmBlockE5m2;
             step = 16;
         } else {
             s.type = mm->x_dtype == MOE_DTYPE_E4M3 ? moe_dc::kMmMxE4m3 : moe_dc::kMmMxE5m2;
@@ -159,24 +172,57 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
     if (s.in % step != 0)
         return fail(MOE_ERR_INVALID_ARG, "in_features %d must be a multiple of %d for these rows",
                     s.in, step);
-    const MatmulArgs a{x, x_scales, weight, weight_scales, ep_recv_count, recv_offsets, out};
+    s.out_code = out_code;
+    const MatmulArgs a{x, x_scales, weight, weight_scales, ep_recv_count, recv_offsets, out, out_scales};
     st = check_pointers(a);
     if (st != MOE_OK) return st;
     if (!codes && (x_scales || weight_scales))
         return fail(MOE_ERR_INVALID_ARG, "token rows take no x_scales or weight_scales");
     if (codes && !weight_scales)
         return fail(MOE_ERR_INVALID_ARG, "weight_scales is required for scaling %d", mm->scaling);
-    if (mm->scaling == MOE_MM_SCALE_MX && !x_scales)
-        return fail(MOE_ERR_INVALID_ARG, "x_scales is required for MX rows");
+    const bool mx = mm->scaling == MOE_MM_SCALE_MX, block = mm->scaling == MOE_MM_SCALE_BLOCK;
+    if ((mx || block) && !x_scales)
+        return fail(MOE_ERR_INVALID_ARG, "x_scales is required for %s rows", mx ? "MX" : "block-scaled");
     if (!aligned(x_scales, 4) || !aligned(weight_scales, 4))
         return fail(MOE_ERR_INVALID_ARG, "x_scales and weight_scales must be 4-byte aligned");
     const int64_t rows = touched(s), xn = rows * s.in, wrows = (int64_t)s.E * s.out, wn = wrows * s.in;
-    const bool mx = mm->scaling == MOE_MM_SCALE_MX;
-    st = check_overlap(s, a, codes ? xn : xn * 2, mx ? xn / 32 : rows * 4, codes ? wn : wn * 2,
-                       mx ? wn / 32 : wrows * 4);
+    const int64_t parts = s.swiglu ? 2 : 1;
+    st = check_overlap(s, a, codes ? xn : xn * 2,
+                       mx ? xn / 32 : block ? rows * groups_of(s.in) * 4 : rows * 4, codes ? wn : wn * 2,
+                       mx ? wn / 32 : block ? s.E * parts * groups_of(s.out / parts) * groups_of(s.in) * 4
+                                            : wrows * 4);
     if (st != MOE_OK) return st;
     return launched(launch_grouped_matmul(s, a, static_cast<hipStream_t>(stream)),
                     "grouped matmul launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, const void* x,
+                              const void* x_scales, const void* weight,
+                              const void* weight_scales, const int32_t* ep_recv_count,
+                              const int64_t* recv_offsets, void* out, void* stream)
+{
+    return grouped_matmul(cfg, mm, x, x_scales, weight, weight_scales, ep_recv_count, recv_offsets, 0,
+                          out, nullptr, stream);
+}
+
+moe_status moe_grouped_matmul_quantize(const moe_dc_config* cfg, const moe_matmul* mm, int32_t out_dtype,
+                                       const void* x, const float* x_scales, const void* weight,
+                                       const float* weight_scales, const int32_t* ep_recv_count,
+                                       const int64_t* recv_offsets, void* codes, float* out_scales,
+                                       void* stream)
+{
+    if (mm && mm->scaling != MOE_MM_SCALE_BLOCK)
+        return fail(MOE_ERR_INVALID_ARG, "coded results need scaling MOE_MM_SCALE_BLOCK, got %d", mm->scaling);
+    if (out_dtype != MOE_DTYPE_E4M3 && out_dtype != MOE_DTYPE_E5M2)
+        return fail(MOE_ERR_INVALID_ARG, "out_dtype %d is not one of 2 (E4M3), 3 (E5M2)", out_dtype);
+    if (!out_scales) return fail(MOE_ERR_INVALID_ARG, "out_scales is NULL");
+    if (!aligned(out_scales, 4)) return fail(MOE_ERR_INVALID_ARG, "out_scales must be 4-byte aligned");
+    return grouped_matmul(cfg, mm, x, x_scales, weight, weight_scales, ep_recv_count, recv_offsets,
+                          out_dtype, codes, out_scales, stream);
 }
 
 moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm, const void* x,
@@ -201,7 +247,7 @@ moe_status moe_grouped_matmul_w4(const moe_dc_config* cfg, const moe_matmul* mm,
                     mm->group_size);
     s.w4 = mm->weight_dtype;
     s.group = mm->group_size;
-    const MatmulArgs a{x, nullptr, weight, weight_scales, ep_recv_count, recv_offsets, out};
+    const MatmulArgs a{x, nullptr, weight, weight_scales, ep_recv_count, recv_offsets, out, nullptr};
     st = check_pointers(a);
     if (st != MOE_OK) return st;
     if (!weight_scales) return fail(MOE_ERR_INVALID_ARG, "weight_scales is required");

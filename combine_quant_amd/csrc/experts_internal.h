@@ -10,10 +10,13 @@
 namespace moe_dc {
 
 // Row and weight types of the products.  Row kinds (Int8, E4m3, E5m2) carry one fp32 scale per
-// row and one per weight row; the MX kinds one E8M0 byte per 32 elements of each.
+// row and one per weight row; the MX kinds one E8M0 byte per 32 elements of each; the block kinds
+// one fp32 scale per 128 elements of a row and per 128 x 128 block of the weights.
 enum MmType : int32_t {
-    kMmBf16 = 0, kMmF16 = 1, kMmInt8 = 2, kMmE4m3 = 3, kMmE5m2 = 4, kMmMxE4m3 = 5, kMmMxE5m2 = 6
+    kMmBf16 = 0, kMmF16 = 1, kMmInt8 = 2, kMmE4m3 = 3, kMmE5m2 = 4, kMmMxE4m3 = 5, kMmMxE5m2 = 6,
+    kMmBlockE4m3 = 7, kMmBlockE5m2 = 8
 };
+constexpr int kBlock = 128;  // elements per scale of the block kinds, in either dimension
 
 // One validated product (see moe_matmul in include/moe_dc.h).
 struct MatmulShape {
@@ -25,6 +28,7 @@ struct MatmulShape {
     int32_t w4;              // 0, or moe_w4_dtype
     int32_t group;           // w4: elements per scale
     int32_t tok_f16;
+    int32_t out_code;        // 0: out holds tokens; else the CodeType of out, with out_scales
     int64_t rows;            // W*BS*K, the most rows there can be
     int64_t cap;
 };
@@ -37,6 +41,7 @@ struct MatmulArgs {
     const int32_t* ep_recv_count;
     const int64_t* recv_offsets;
     void* out;
+    float* out_scales;       // out_code: one per row and 128 columns
 };
 
 // One per MmType.
@@ -47,6 +52,8 @@ hipError_t launch_grouped_e4m3(const MatmulShape& s, const MatmulArgs& a, hipStr
 hipError_t launch_grouped_e5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_mxe4m3(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_mxe5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_block_e4m3(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_block_e5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_matmul_w4(const MatmulShape& s, const MatmulArgs& a,
                                     hipStream_t stream);
 

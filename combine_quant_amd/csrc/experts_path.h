@@ -13,8 +13,9 @@ enum ProductPath : int32_t {
 };
 
 constexpr int kTileN = 256;                     // weight rows of a workgroup
-// Most rows of x of a workgroup: as many as the 160 KB of LDS take (MX keeps scales there too).
-constexpr int tile_rows(int type) { return type == kMmMxE4m3 || type == kMmMxE5m2 ? 192 : 256; }
+// Most rows of x of a workgroup: as many as the 160 KB of LDS take (MX and block kinds keep scales
+// there too).
+constexpr int tile_rows(int type) { return type >= kMmMxE4m3 ? 192 : 256; }
 
 constexpr int kW4TileM = 128;                   // rows of x and weight rows of a workgroup
 constexpr int kW4TileN = 256;

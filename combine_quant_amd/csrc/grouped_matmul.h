@@ -10,6 +10,8 @@ namespace {
 template <int TYPE>
 hipError_t launch_type(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
+    // coded results need whole groups of 128 columns in one workgroup
+    if (Mm<TYPE>::kBlk && s.out_code) return launch_tiles<TYPE>(s, a, stream);
     return product_path(s) == kPathTiles ? launch_tiles<TYPE>(s, a, stream) : launch_stream<TYPE>(s, a, stream);
 }
 

@@ -42,9 +42,15 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
     const int mrows = rows < MT * 16 ? rows : MT * 16;
     const __amdgpu_buffer_rsrc_t xr =
         make_rsrc(static_cast<const char*>(a.x) + (size_t)row0 * row_bytes, (uint32_t)mrows * row_bytes);
-    const int ns = s.in / 32;
+    // MX: bytes of 32 elements.  Block: floats, one a chunk, for the weights in rows of 128 weight
+    // rows, those of the gate and of the up rows begun anew (n0 + 0..31 lies within one block).
+    const int ns = M::kBlk ? chunks : s.in / 32;
     const uint8_t* wsc = static_cast<const uint8_t*>(a.w_scales) + ((size_t)e * s.out + n0) * ns;
     const uint8_t* xsc = static_cast<const uint8_t*>(a.x_scales) + (size_t)row0 * ns;
+    const int blocks = (half + kBlock - 1) / kBlock;
+    const float* wblock = static_cast<const float*>(a.w_scales) +
+        ((size_t)e * blocks * (s.swiglu ? 2 : 1) + n0 / kBlock) * ns;
+    const float* xblock = static_cast<const float*>(a.x_scales) + (size_t)row0 * ns;
 
     Acc acc[MT][NT];
 #pragma unroll
@@ -70,6 +76,9 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
                 const int rr = rt * 16 + l16 < left ? rt * 16 + l16 : left - 1;
                 const int cc = c < chunks ? c : chunks - 1;
                 wsv[d][t] = wsc[((size_t)part * half + rr) * ns + cc * 4 + g];
+            } else if (M::kBlk) {
+                const int cc = c < chunks ? c : chunks - 1;
+                wsv[d][t] = __float_as_int(wblock[(size_t)part * blocks * ns + cc]);
             }
         }
 #pragma unroll
@@ -81,6 +90,10 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
                 const int rr = m * 16 + l16 < mrows ? m * 16 + l16 : mrows - 1;
                 const int cc = c < chunks ? c : chunks - 1;
                 xsv[d][m] = xsc[(size_t)rr * ns + cc * 4 + g];
+            } else if (M::kBlk) {
+                const int rr = m * 16 + l16 < mrows ? m * 16 + l16 : mrows - 1;
+                const int cc = c < chunks ? c : chunks - 1;
+                xsv[d][m] = __float_as_int(xblock[(size_t)rr * ns + cc]);
             }
         }
     };
@@ -92,9 +105,17 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    acc[m][t] = M::mma(join(wv[d][t][0], wv[d][t][1]), join(xv[d][m][0], xv[d][m][1]), acc[m][t],
-                                       wsv[d][t], xsv[d][m]);
+                for (int t = 0; t < NT; ++t) {
+                    const v8i_t wc = join(wv[d][t][0], wv[d][t][1]), xc = join(xv[d][m][0], xv[d][m][1]);
+                    if constexpr (M::kBlk) {
+                        // past the last chunk the operands are 0, and an infinite scale must not be met
+                        const Acc sum = M::mma(wc, xc, Acc{0, 0, 0, 0}, 0, 0);
+                        if (c + d * kStreamWaves < chunks)
+                            add_scaled(acc[m][t], sum, __int_as_float(wsv[d][t]) * __int_as_float(xsv[d][m]));
+                    } else {
+                        acc[m][t] = M::mma(wc, xc, acc[m][t], wsv[d][t], xsv[d][m]);
+                    }
+                }
             fetch(d, c + (d + D) * kStreamWaves);
         }
     }

@@ -32,15 +32,116 @@ struct TileStages {
     // MX: the E8M0 bytes of four steps, 16 of each row of x, then of each weight row (with the
     // four bytes of one step at a time the requests for them outnumbered the rows': 3.45 ms
     // instead of 2.63 at 65536 skewed rows on 256 experts x 7168 x 4096)
-    char scales[2][Mm<TYPE>::kMx ? (kTileM<TYPE> + kTileN) * 16 : 0];
+    // Block: the floats of four steps, likewise 16 bytes of each row of x, then of the tile's two
+    // rows of weight blocks
+    char scales[2][Mm<TYPE>::kMx ? (kTileM<TYPE> + kTileN) * 16 : Mm<TYPE>::kBlk ? (kTileM<TYPE> + 64) * 16 : 0];
 };
 
-// The table is done with before the first stage is filled.
+// The table is done with before the first stage is filled, and the stages before the largest
+// values of a coded output meet: of each row, per wave (Mm<TYPE>::kBlk).
 template <int TYPE>
 union TileLds {
     TileStages<TYPE> st;
     TileTable table;
+    uint32_t amax[Mm<TYPE>::kBlk ? kTileM<TYPE> * kTileWaves : 1];
 };
+
+// Four values as codes, the first in the lowest byte.  None is NaN.
+__device__ __forceinline__ uint32_t code4(const float (&v)[4], int code)
+{
+    const float top = code == kCodeE4m3 ? 448.0f : 57344.0f;
+    float c[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[q] = __builtin_amdgcn_fmed3f(v[q], -top, top);
+    int w;
+    if (code == kCodeE4m3) {
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    } else {
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c[0], c[1], 0, false);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c[2], c[3], w, true);
+    }
+    return (uint32_t)w;
+}
+
+// A tile's sums as codes with one scale per row and 128 columns, as dispatch codes a token in mode
+// 3.  A tile holds one group of columns with SwiGLU, else two, so the largest values of 8 or 4
+// waves meet in LDS and nothing but the codes leaves the workgroup.  In a group with an infinity or a
+// NaN (whose bits are the largest) the scale is NaN and the codes are 0.
+template <int TYPE, int MT, bool SWIGLU>
+__device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs& a, const Tile& tile,
+                                          int half, int left, v4f_t (&acc)[MT][2], uint32_t* amax)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, g = lane >> 4;
+    constexpr int kT = SWIGLU ? 1 : 2;
+    constexpr int kMeet = SWIGLU ? kTileWaves : kTileWaves / 2;      // waves of a group
+    const int c0 = wave * (kT * 16) + g * 4;
+    __syncthreads();                            // the last step's rows have been read
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            if (SWIGLU) {
+                float y[4], u[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    y[q] = acc[m][0][q];
+                    u[q] = acc[m][1][q];
+                }
+                silu_mul4(y, u, y);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[m][0][q] = y[q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t bits = __float_as_uint(acc[m][t][q]) & 0x7FFFFFFFu;
+                if (c0 + t * 16 + q < left && bits > most) most = bits;
+            }
+        }
+        most = dpp_max(most, __shfl_xor(most, 16, kWave));
+        most = dpp_max(most, __shfl_xor(most, 32, kWave));
+        if (g == 0) amax[(m * 16 + l16) * kTileWaves + wave] = most;
+    }
+    __syncthreads();
+    const int first = wave / kMeet * kMeet;
+    const int groups = (half + kBlock - 1) / kBlock;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int row = m * 16 + l16;
+        if (row >= tile.rows) continue;
+        uint32_t most = 0;
+#pragma unroll
+        for (int w = 0; w < kMeet; ++w) most = dpp_max(most, amax[row * kTileWaves + first + w]);
+        const bool finite = most < 0x7F800000u;
+        float dyn = (s.out_code == kCodeE4m3 ? 448.0f : 57344.0f) / __uint_as_float(most);
+        const float scale = finite ? 1.0f / dyn : NAN;
+        uint8_t* o = static_cast<uint8_t*>(a.out) + (size_t)(tile.row0 + row) * half + tile.n0;
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            const int c = c0 + t * 16;
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float p = acc[m][t][q] * dyn;
+                v[q] = finite && p == p ? p : 0.0f;
+            }
+            const uint32_t p = code4(v, s.out_code);
+            if (c + 3 < left && (reinterpret_cast<uintptr_t>(o + c) & 3) == 0) {
+                *reinterpret_cast<uint32_t*>(o + c) = p;
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < left) o[c + q] = (uint8_t)(p >> (8 * q));
+            }
+        }
+        // the group's first columns' lanes write its scale
+        if (wave == first && g == 0 && first * kT * 16 < left)
+            a.out_scales[(size_t)(tile.row0 + row) * groups + (tile.n0 + first * kT * 16) / kBlock] = scale;
+    }
+}
 
 // One tile: 16 * MT rows of x from row0 (of which `rows` exist), 256 weight rows from column n0.
 // Wave w owns weight rows 32 * w + 0..31 of the tile (with SwiGLU 16 gate rows and the 16 up rows
@@ -57,8 +158,9 @@ union TileLds {
 // issues the same number.
 template <int TYPE, int MT, bool SWIGLU>
 __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulArgs& a,
-                                             const Tile& tile, TileStages<TYPE>& lds)
+                                             const Tile& tile, TileLds<TYPE>& shared)
 {
+    TileStages<TYPE>& lds = shared.st;
     const int e = tile.e, n0 = tile.n0, row0 = tile.row0, rows = tile.rows;
     typedef Mm<TYPE> M;
     typedef typename M::Acc Acc;
@@ -76,8 +178,11 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         make_rsrc(wbase + (size_t)half * row_bytes, (uint32_t)left * row_bytes);
     const __amdgpu_buffer_rsrc_t xr =
         make_rsrc(static_cast<const char*>(a.x) + (size_t)row0 * row_bytes, (uint32_t)rows * row_bytes);
-    const uint32_t ns = (uint32_t)s.in / 32;
-    const char* wsb = static_cast<const char*>(a.w_scales) + ((size_t)e * s.out + n0) * ns;
+    // bytes of scales of a row of x, and of a weight row (MX) or of 128 of them (block)
+    const uint32_t ns = M::kBlk ? (uint32_t)steps * 4 : (uint32_t)s.in / 32;
+    const int blocks = (half + kBlock - 1) / kBlock;         // rows of weight blocks, of gate or up
+    const char* wsb = static_cast<const char*>(a.w_scales) +
+        (M::kBlk ? ((size_t)e * blocks * (SWIGLU ? 2 : 1) + n0 / kBlock) * ns : ((size_t)e * s.out + n0) * ns);
 
     // One load moves 8 rows of 128 bytes; lane i brings row i / 8 the 16 bytes that belong at
     // position i % 8, which holds chunk (i % 8) ^ (row & 7).
@@ -102,15 +207,20 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     }
     // MX: every fourth step a wave brings 16 bytes of scales of 64 rows: waves 0-2 rows of x,
     // waves 3-6 weight rows (wave 7 the same as wave 6).  Rows are ns bytes, ns a multiple of 4.
+    // Block: waves 3-7 the same two rows of weight blocks, of columns n0 and n0 + 128 or of gate
+    // and up.
+    constexpr bool kLdsScales = M::kMx || M::kBlk;
     const bool sx = wave * 64 < kTileM<TYPE>;
-    const int sblk = sx ? wave : (wave < 6 ? wave : 6) - kTileM<TYPE> / 64;
+    const int sblk = sx ? wave : M::kBlk ? 0 : (wave < 6 ? wave : 6) - kTileM<TYPE> / 64;
     const int srow = sblk * 64 + lane;
     const int scol = SWIGLU ? srow / 32 * 16 + (srow & 15) : srow;      // of the weight row
-    const bool sok = sx ? srow < rows : scol < left;
-    const uint32_t soff = (uint32_t)(sx ? srow : SWIGLU && (srow & 16) ? half + scol : scol) * ns;
+    const bool sok = sx ? srow < rows : M::kBlk ? srow < 2 && (SWIGLU || srow * kBlock < left) : scol < left;
+    const uint32_t soff = (uint32_t)(sx ? srow : M::kBlk ? (SWIGLU ? srow * blocks : srow)
+                                                 : SWIGLU && (srow & 16) ? half + scol : scol) * ns;
     const __amdgpu_buffer_rsrc_t sr = make_rsrc(
         sx ? static_cast<const char*>(a.x_scales) + (size_t)row0 * ns : wsb,
-        !M::kMx ? 0 : (uint32_t)(sx ? rows : SWIGLU ? half + left : left) * ns);
+        !kLdsScales ? 0 : (uint32_t)(sx ? rows : M::kBlk ? (SWIGLU ? blocks + 1 : left > kBlock ? 2 : 1)
+                                                  : SWIGLU ? half + left : left) * ns);
     const int sto = (sx ? 0 : kTileM<TYPE> * 16) + sblk * 1024;
     // The 16 bytes of a row's last window end where the row does (from the window's own start they
     // would run into the next row and, of the last row, past the tensor), so that its steps lie
@@ -131,17 +241,19 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                 load_lds4(sr, to + d * 64, sok && d < ns ? soff + d : kRsrcPastEnd);
         }
     };
-    // The scale of a step for row r + l16 (r a multiple of 16).  Steps of windows known to be
+    // The scale of a step for row r + i (r a multiple of 16 or 64).  Steps of windows known to be
     // full need no shift; only those after the unrolled loop may be of rows below 16 bytes.
     enum Where { kFull, kPerhapsLast, kAfterLoop };
-    const auto scale_of = [&](Where where, int step, int r) {
+    const auto scale_at = [&](Where where, int step, int r, int i) {
         const char* to = lds.scales[step >> 2 & 1];
         const int k = step & 3;
         if (where == kAfterLoop && ns < 16)
-            return (int)*reinterpret_cast<const uint8_t*>(to + (r >> 6) * 1024 + k * 256 + ((r & 63) + l16) * 4 + g);
-        if (where != kFull) to += scale_shift(step >> 2);
-        return (int)*reinterpret_cast<const uint8_t*>(to + (r + l16) * 16 + k * 4 + g);
+            to += (r >> 6) * 1024 + k * 256 + ((r & 63) + i) * 4;
+        else
+            to += (where != kFull ? scale_shift(step >> 2) : 0) + (r + i) * 16 + k * 4;
+        return M::kBlk ? *reinterpret_cast<const int*>(to) : (int)*reinterpret_cast<const uint8_t*>(to + g);
     };
+    const auto scale_of = [&](Where where, int step, int r) { return scale_at(where, step, r, l16); };
     // Load i of a step's x, and of its weights.
     const auto fetch_x = [&](int step, int i) {
         const uint32_t k = (uint32_t)step * 128;
@@ -167,6 +279,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
             w[par][t] = join(*reinterpret_cast<const v4i_t*>(wl + t * 2048 + f0),
                              *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f1));
             if (M::kMx) wsc[par][t] = scale_of(where, step, kTileM<TYPE> + wave * 32 + t * 16);
+            if (M::kBlk) wsc[par][t] = scale_at(where, step, kTileM<TYPE>, SWIGLU ? t : wave >> 2);
         }
     };
     Acc acc[MT][2];
@@ -183,13 +296,13 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 #pragma unroll
         for (int i = 0; i < 4; ++i) fetch_w(step, i);
     };
-    if (M::kMx) fetch_scales(0);
+    if (kLdsScales) fetch_scales(0);
     all_x(0);
     all_w(0);
     all_w(1);
     all_x(1);
     wait_loads<kAhead>();
-    if (M::kMx) meet();                         // the scales come from other waves
+    if (kLdsScales) meet();                     // the scales come from other waves
     read_w(0, 0, kAfterLoop);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     all_w(2);
@@ -210,7 +323,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         wait_loads<kAhead>();
         meet();
         const char* xl = lds.x[step % kTileRing];
-        if (M::kMx && phase == 0) fetch_scales((step >> 2) + 1);
+        if (kLdsScales && phase == 0) fetch_scales((step >> 2) + 1);
         v8i_t x[2][2];
         int xsv[2][2] = {{0, 0}, {0, 0}};
         const auto read_x = [&](int set, int group) {
@@ -220,7 +333,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                 if (m >= MT) break;
                 x[set][i] = join(*reinterpret_cast<const v4i_t*>(xl + m * 2048 + f0),
                                  *reinterpret_cast<const v4i_t*>(xl + m * 2048 + f1));
-                if (M::kMx) xsv[set][i] = scale_of(where, step, m * 16);
+                if (kLdsScales) xsv[set][i] = scale_of(where, step, m * 16);
             }
         };
         read_x(0, 0);
@@ -243,13 +356,18 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 #pragma unroll
             for (int i = 0; i < 2 && q * 2 + i < MT; ++i)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    acc[q * 2 + i][t] = M::mma(w[par][t], x[q & 1][i], acc[q * 2 + i][t], wsc[par][t],
-                                               xsv[q & 1][i]);
+                for (int t = 0; t < 2; ++t) {
+                    if constexpr (M::kBlk)
+                        add_scaled(acc[q * 2 + i][t], M::mma(w[par][t], x[q & 1][i], Acc{0, 0, 0, 0}, 0, 0),
+                                   __int_as_float(wsc[par][t]) * __int_as_float(xsv[q & 1][i]));
+                    else
+                        acc[q * 2 + i][t] = M::mma(w[par][t], x[q & 1][i], acc[q * 2 + i][t], wsc[par][t],
+                                                   xsv[q & 1][i]);
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    constexpr int kUnroll = M::kMx ? 4 : 2;
+    constexpr int kUnroll = kLdsScales ? 4 : 2;
     int step = 0;
     for (; step + kUnroll <= steps; step += kUnroll) {
 #pragma unroll
@@ -262,6 +380,12 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 
     constexpr int kT = SWIGLU ? 1 : 2;
     const int c0 = wave * (kT * 16) + g * 4;    // the lane's first column
+    if constexpr (M::kBlk) {
+        if (s.out_code != 0) {
+            code_tile<TYPE, MT, SWIGLU>(s, a, tile, half, left, acc, shared.amax);
+            return;
+        }
+    }
     float ws_[2][4];
     if (M::kRowScaled) {
 #pragma unroll
@@ -309,24 +433,24 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
     if (!find_tile<kRows, SWIGLU ? kTileN / 2 : kTileN>(s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t))
         return;
     switch ((t.rows + 15) / 16) {
-    case 1: tile_product<TYPE, 1, SWIGLU>(s, a, t, lds.st); break;
-    case 2: tile_product<TYPE, 2, SWIGLU>(s, a, t, lds.st); break;
-    case 3: tile_product<TYPE, 3, SWIGLU>(s, a, t, lds.st); break;
-    case 4: tile_product<TYPE, 4, SWIGLU>(s, a, t, lds.st); break;
-    case 5: tile_product<TYPE, 5, SWIGLU>(s, a, t, lds.st); break;
-    case 6: tile_product<TYPE, 6, SWIGLU>(s, a, t, lds.st); break;
-    case 7: tile_product<TYPE, 7, SWIGLU>(s, a, t, lds.st); break;
-    case 8: tile_product<TYPE, 8, SWIGLU>(s, a, t, lds.st); break;
-    case 9: tile_product<TYPE, 9, SWIGLU>(s, a, t, lds.st); break;
-    case 10: tile_product<TYPE, 10, SWIGLU>(s, a, t, lds.st); break;
-    case 11: tile_product<TYPE, 11, SWIGLU>(s, a, t, lds.st); break;
-    case 12: tile_product<TYPE, 12, SWIGLU>(s, a, t, lds.st); break;
+    case 1: tile_product<TYPE, 1, SWIGLU>(s, a, t, lds); break;
+    case 2: tile_product<TYPE, 2, SWIGLU>(s, a, t, lds); break;
+    case 3: tile_product<TYPE, 3, SWIGLU>(s, a, t, lds); break;
+    case 4: tile_product<TYPE, 4, SWIGLU>(s, a, t, lds); break;
+    case 5: tile_product<TYPE, 5, SWIGLU>(s, a, t, lds); break;
+    case 6: tile_product<TYPE, 6, SWIGLU>(s, a, t, lds); break;
+    case 7: tile_product<TYPE, 7, SWIGLU>(s, a, t, lds); break;
+    case 8: tile_product<TYPE, 8, SWIGLU>(s, a, t, lds); break;
+    case 9: tile_product<TYPE, 9, SWIGLU>(s, a, t, lds); break;
+    case 10: tile_product<TYPE, 10, SWIGLU>(s, a, t, lds); break;
+    case 11: tile_product<TYPE, 11, SWIGLU>(s, a, t, lds); break;
+    case 12: tile_product<TYPE, 12, SWIGLU>(s, a, t, lds); break;
     default:
         if constexpr (kRows > 192) switch ((t.rows + 15) / 16) {
-            case 13: tile_product<TYPE, 13, SWIGLU>(s, a, t, lds.st); break;
-            case 14: tile_product<TYPE, 14, SWIGLU>(s, a, t, lds.st); break;
-            case 15: tile_product<TYPE, 15, SWIGLU>(s, a, t, lds.st); break;
-            default: tile_product<TYPE, 16, SWIGLU>(s, a, t, lds.st); break;
+            case 13: tile_product<TYPE, 13, SWIGLU>(s, a, t, lds); break;
+            case 14: tile_product<TYPE, 14, SWIGLU>(s, a, t, lds); break;
+            case 15: tile_product<TYPE, 15, SWIGLU>(s, a, t, lds); break;
+            default: tile_product<TYPE, 16, SWIGLU>(s, a, t, lds); break;
             }
         break;
     }

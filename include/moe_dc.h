@@ -361,7 +361,9 @@ moe_status moe_combine_int8(const moe_dc_config* cfg, const int8_t* codes,
 typedef enum {
     MOE_MM_SCALE_NONE = 0,      /* token rows and weights                                  */
     MOE_MM_SCALE_ROW = 1,       /* one fp32 per row of x and one per weight row            */
-    MOE_MM_SCALE_MX = 2         /* one E8M0 byte per 32 elements of x and of the weights   */
+    MOE_MM_SCALE_MX = 2,        /* one E8M0 byte per 32 elements of x and of the weights   */
+    MOE_MM_SCALE_BLOCK = 3      /* one fp32 per 128 elements of a row of x and per block of 128
+                                   x 128 elements of the weights                            */
 } moe_mm_scaling;
 
 typedef enum {
@@ -381,8 +383,8 @@ typedef struct {
     int32_t out_features;       /* N, in [1, 65536]: weight rows per expert                 */
     int32_t x_dtype;            /* moe_dtype of the rows: DEFAULT = the token type, INT8,
                                    E4M3 or E5M2 (moe_grouped_matmul only)                   */
-    int32_t scaling;            /* moe_mm_scaling: NONE for tokens, ROW for INT8, ROW or MX for
-                                   E4M3 and E5M2                                            */
+    int32_t scaling;            /* moe_mm_scaling: NONE for tokens, ROW for INT8, ROW, MX or
+                                   BLOCK for E4M3 and E5M2                                  */
     int32_t activation;         /* moe_activation                                           */
     int32_t weight_dtype;       /* moe_w4_dtype for moe_grouped_matmul_w4, else 0            */
     int32_t group_size;         /* moe_grouped_matmul_w4: 32, 64 or 128 elements per scale
@@ -399,24 +401,29 @@ typedef struct {
  *   out[p][n] = S[p][n]                                        MOE_ACT_NONE,   n < N
  *   out[p][n] = silu(S[p][n]) * S[p][N/2 + n], silu(t) = t / (1 + exp(-t))
  *                                                              MOE_ACT_SWIGLU, n < N/2
- * X and V are the tokens themselves, code * scale of the row (ROW), or code * 2^(byte - 127) of
- * the block (MX).
+ * X and V are the tokens themselves, code * scale of the row (ROW), code * 2^(byte - 127) of
+ * the block (MX), or code * scale of the group or block (BLOCK).
  *
  * Inputs:
  *   x              [cap][I] in x_dtype (mode-0 expand_x, or its codes)
  *   x_scales       ROW: fp32 [cap] (mode 2's dynamic_scales), or NULL for all 1 (mode 1, whose
  *                  static scale belongs into weight_scales); MX: bytes [cap][I/32] (the
- *                  dynamic_scales of MOE_SCALE_E8M0); NULL for tokens
+ *                  dynamic_scales of MOE_SCALE_E8M0); BLOCK: fp32 [cap][Ceil(I, 128)] (mode 3's
+ *                  dynamic_scales); NULL for tokens
  *   weight         [E][N][I]: tokens for token rows, int8 for INT8, E4M3 for E4M3 and E5M2
- *   weight_scales  ROW: fp32 [E][N]; MX: bytes [E][N][I/32]; NULL for tokens
+ *   weight_scales  ROW: fp32 [E][N]; MX: bytes [E][N][I/32]; BLOCK: fp32
+ *                  [E][Ceil(N, 128)][Ceil(I, 128)], with SwiGLU [E][2 Ceil(N/2, 128)][Ceil(I, 128)]:
+ *                  the blocks of the gate rows, then those of the up rows, which begin anew at row
+ *                  N/2; NULL for tokens
  *   ep_recv_count, recv_offsets: as produced by moe_dispatch for this config
  * Output:
  *   out            token type [cap][N], or [cap][N/2] with SwiGLU.  Rows at or past
  *                  recv_offsets[W] are not written
- * I must be a multiple of 8 (tokens), 16 (ROW) or 128 (MX).
+ * I must be a multiple of 8 (tokens), 16 (ROW, BLOCK) or 128 (MX).
  * Numerics: products are exact; int8 sums are exact in 32 bits; the other sums are fp32 in an
  * order that depends on the sizes only (the same inputs give the same bytes); ROW scales
- * multiply the sum (weight's, then row's); SwiGLU is within 2^-17 of its value for S[p][n] down
+ * multiply the sum (weight's, then row's); BLOCK sums 128 products, multiplies them by the
+ * product of their two scales and adds, each in fp32; SwiGLU is within 2^-17 of its value for S[p][n] down
  * to -176, below that 0; out is rounded once, to nearest even.  The fp8
  * matrix instructions add eight consecutive products at a time and drop, of each product, what
  * lies below 2^-13 of the largest one's power of two.  An infinity or NaN stays within its own
@@ -426,6 +433,28 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
                               const void* x_scales, const void* weight,
                               const void* weight_scales, const int32_t* ep_recv_count,
                               const int64_t* recv_offsets, void* out, void* stream);
+
+/* moe_grouped_matmul_quantize -- moe_grouped_matmul of block-scaled rows, its results coded for
+ * another such product.
+ *
+ * With M = N, or N/2 with SwiGLU, and out[p][n] as moe_grouped_matmul defines it, before its last
+ * rounding: each row's columns in groups of 128 (the last may be short) are coded as moe_dispatch
+ * codes a token in mode 3: dyn = type_max / max|out| over the group, codes = type(out * dyn), scale =
+ * 1/dyn; a group of zeros has codes 0 and scale 0.  A group that holds an infinity or a NaN has scale
+ * NaN and codes 0.
+ *
+ * Inputs as for moe_grouped_matmul with scaling MOE_MM_SCALE_BLOCK (no other is taken).
+ *   out_dtype      MOE_DTYPE_E4M3 or MOE_DTYPE_E5M2 (moe_dtype), whatever the rows of x hold
+ * Outputs:
+ *   codes          bytes [cap][M]
+ *   out_scales     fp32 [cap][Ceil(M, 128)]
+ * Rows at or past recv_offsets[W] are not written.  Numerics and errors as for
+ * moe_grouped_matmul. */
+moe_status moe_grouped_matmul_quantize(const moe_dc_config* cfg, const moe_matmul* mm,
+                                       int32_t out_dtype, const void* x, const float* x_scales,
+                                       const void* weight, const float* weight_scales,
+                                       const int32_t* ep_recv_count, const int64_t* recv_offsets,
+                                       void* codes, float* out_scales, void* stream);
 
 /* moe_grouped_matmul_w4 -- moe_grouped_matmul of token rows with 4-bit weights.
  *
