@@ -33,7 +33,7 @@ EXPORTS = ("moe_dc_validate", "moe_dc_scales_per_row", "moe_dc_dispatch_workspac
            "moe_dispatch_no_workspace", "moe_combine",
            "moe_combine_scatter", "moe_combine_quantize", "moe_combine_int8",
            "moe_gate_topk", "moe_grouped_matmul", "moe_grouped_matmul_quantize",
-           "moe_grouped_matmul_w4",
+           "moe_grouped_matmul_w4", "moe_rms_norm",
            "moe_dc_last_error", "moe_dc_version")
 
 
@@ -98,6 +98,14 @@ class MoeGate(ctypes.Structure):
     ]
 
 
+class MoeNorm(ctypes.Structure):
+    """Mirror of moe_norm."""
+    _fields_ = [
+        ("epsilon", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class MoeDcError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{_STATUS.get(status, status)}: {message}")
@@ -145,6 +153,8 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     lib.moe_grouped_matmul_w4.argtypes = [cfgp, mmp] + [P] * 6 + [P]
     lib.moe_gate_topk.restype = ctypes.c_int
     lib.moe_gate_topk.argtypes = [cfgp, gatep] + [P] * 4 + [P]
+    lib.moe_rms_norm.restype = ctypes.c_int
+    lib.moe_rms_norm.argtypes = [cfgp, ctypes.POINTER(MoeNorm)] + [P] * 7 + [P]
     lib.moe_dc_last_error.restype = ctypes.c_char_p
     lib.moe_dc_last_error.argtypes = []
     lib.moe_dc_version.restype = ctypes.c_char_p
@@ -173,6 +183,10 @@ def make_matmul(in_features, out_features, x_dtype=MOE_DTYPE_DEFAULT,
 def make_gate(score=MOE_SCORE_SOFTMAX, group_count=1, group_keep=1, group_top=1,
               renormalize=False, factor=1.0):
     return MoeGate(score, group_count, group_keep, group_top, int(renormalize), factor)
+
+
+def make_norm(epsilon=1e-6):
+    return MoeNorm(epsilon, 0)
 
 
 def token_torch_dtype(cfg):
@@ -584,6 +598,40 @@ def moe_gate_topk(cfg, gate, logits, bias, expert_ids, expert_scales, stream=Non
     _launch(*_gate_topk_call(cfg, gate, logits, bias, expert_ids, expert_scales), stream)
 
 
+# -- the norm before the router ----------------------------------------------------------------
+
+def _norm_scales_spec(cfg):
+    """(dtype, shape) of the norm's dynamic_scales, or None in mode 0."""
+    ns = moe_dc_scales_per_row(cfg)
+    if ns <= 0:
+        return None
+    dt = torch.uint8 if cfg.scale_format == MOE_SCALE_E8M0 else torch.float32
+    return dt, (cfg.ep_world_size, cfg.bs) + ((ns,) if ns > 1 else ())
+
+
+def _rms_norm_call(cfg, norm, x, residual, gamma, residual_out, y, codes, dynamic_scales):
+    shape, token, dev = (cfg.ep_world_size, cfg.bs, cfg.hidden), token_torch_dtype(cfg), x.device
+    spec = _norm_scales_spec(cfg)
+    args = [
+        _ptr(x, token, shape, "x", dev),
+        _ptr(residual, token, shape, "residual", dev),
+        _ptr(gamma, token, shape[2:], "gamma", dev),
+        _ptr(residual_out, token, shape, "residual_out", dev),
+        _ptr(y, token, shape, "y", dev),
+        _ptr(codes, _CODE_DTYPES.get(code_type(cfg)), shape, "codes", dev),
+        _ptr(dynamic_scales, None if spec is None else spec[0], None if spec is None else spec[1],
+             "dynamic_scales", dev),
+    ]
+    return load_library().moe_rms_norm, (ctypes.byref(cfg), ctypes.byref(norm), *args), dev
+
+
+def moe_rms_norm(cfg, norm, x, residual, gamma, residual_out, y, codes, dynamic_scales,
+                 stream=None):
+    """Enqueue one RMS norm of the tokens on `stream`."""
+    _launch(*_rms_norm_call(cfg, norm, x, residual, gamma, residual_out, y, codes,
+                            dynamic_scales), stream)
+
+
 # -- allocation helpers (torch owns the memory; the library never allocates) ----------------
 
 def alloc_dispatch_outputs(cfg, device="cuda"):
@@ -813,5 +861,30 @@ def gate_topk(cfg, gate, logits, bias=None, out=None, stream=None):
     """Allocate (or reuse `out`) and enqueue moe_gate_topk; returns (expert_ids, expert_scales)
     as dispatch and combine take them."""
     launch, out = prepare_gate_topk(cfg, gate, logits, bias, out)
+    launch(stream)
+    return out
+
+
+def prepare_rms_norm(cfg, norm, x, gamma, residual=None, out=None):
+    """Plan for moe_rms_norm: (launch, dict of "residual_out", "y", "codes" and
+    "dynamic_scales"; None where there is none).  `out` is such a dict; what it lacks is not
+    written."""
+    if out is None:
+        _check(moe_dc_validate(cfg))
+        spec = _norm_scales_spec(cfg)
+        out = dict(
+            residual_out=None if residual is None else torch.empty_like(x), y=torch.empty_like(x),
+            codes=None if cfg.quant_mode == 0 else
+            torch.empty(x.shape, dtype=_ALLOC_DTYPES[code_type(cfg)], device=x.device),
+            dynamic_scales=None if spec is None else
+            torch.empty(spec[1], dtype=spec[0], device=x.device))
+    fn, args, dev = _rms_norm_call(cfg, norm, x, residual, gamma, out.get("residual_out"),
+                                   out.get("y"), out.get("codes"), out.get("dynamic_scales"))
+    return Launch(fn, args, dev, (cfg, norm, x, gamma, residual, dict(out))), out
+
+
+def rms_norm(cfg, norm, x, gamma, residual=None, out=None, stream=None):
+    """Allocate (or reuse `out`) and enqueue moe_rms_norm; returns the dict of outputs."""
+    launch, out = prepare_rms_norm(cfg, norm, x, gamma, residual, out)
     launch(stream)
     return out

@@ -1,9 +1,11 @@
-// experts_api.cpp -- C ABI of the router and the experts' products: host validation and launch.
+// experts_api.cpp -- C ABI of the norm, the router and the experts' products: host validation and
+// launch.
 //
 // As in api.cpp, nothing here allocates device memory or synchronises the host; each call is
 // one kernel on the caller's stream.
 #include "moe_dc.h"
 #include "experts_internal.h"
+#include "norm_internal.h"
 
 #include <cmath>
 #include <cstdarg>
@@ -304,6 +306,54 @@ moe_status moe_gate_topk(const moe_dc_config* cfg, const moe_gate* gate, const f
     return launched(moe_dc::launch_gate_topk(s, logits, bias, expert_ids, expert_scales,
                                              static_cast<hipStream_t>(stream)),
                     "router kernel launch");
+}
+
+moe_status moe_rms_norm(const moe_dc_config* cfg, const moe_norm* norm, const void* x,
+                        const void* residual, const void* gamma, void* residual_out, void* y,
+                        void* codes, void* dynamic_scales, void* stream)
+{
+    moe_dc::Shape sh;
+    moe_status st = moe_dc::check_config(cfg, &sh);
+    if (st != MOE_OK) return st;
+    if (!norm) return fail(MOE_ERR_INVALID_ARG, "norm description is NULL");
+    if (!std::isfinite(norm->epsilon) || norm->epsilon <= 0.0f)
+        return fail(MOE_ERR_INVALID_ARG, "epsilon must be finite and above 0");
+    if (norm->reserved != 0) return fail(MOE_ERR_INVALID_ARG, "reserved must be 0");
+    if (sh.quant_mode == 1 || sh.scales_kind != MOE_SCALES_NONE)
+        return fail(MOE_ERR_UNSUPPORTED, "the norm's codes take no scales tensor");
+    if (sh.code_type == moe_dc::kCodeE2m1) return fail(MOE_ERR_UNSUPPORTED, "E2M1 codes are not supported");
+    if (!x || !gamma) return fail(MOE_ERR_INVALID_ARG, "a required tensor pointer is NULL");
+    if (residual_out && !residual)
+        return fail(MOE_ERR_INVALID_ARG, "residual_out is the sum with a residual, which is NULL");
+    const bool coded = sh.quant_mode != 0;
+    if (coded != (codes != nullptr) || coded != (dynamic_scales != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "codes and dynamic_scales must be given iff quant_mode is not 0");
+    if (!coded && !y) return fail(MOE_ERR_INVALID_ARG, "y is required for quant_mode 0");
+    if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(gamma, 2) || !aligned(residual_out, 2) ||
+        !aligned(y, 2) || (sh.scale_format != MOE_SCALE_E8M0 && !aligned(dynamic_scales, 4)))
+        return fail(MOE_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+    const int64_t tokens = (int64_t)sh.W * sh.BS, rows = tokens * sh.H * 2;
+    const int64_t scales = tokens * sh.scales_per_row * (sh.scale_format == MOE_SCALE_E8M0 ? 1 : 4);
+    const struct { const void* p; int64_t n; } outs[4] = {
+        {residual_out, rows}, {y, rows}, {codes, rows / 2}, {dynamic_scales, scales}};
+    for (int i = 0; i < 4; ++i) {
+        // a token is read whole before any of it is written: the sum may take its addends' place
+        // and y that of x
+        if ((overlap(outs[i].p, outs[i].n, x, rows) && !(i < 2 && outs[i].p == x)) ||
+            (overlap(outs[i].p, outs[i].n, residual, rows) && !(i < 2 && outs[i].p == residual)) ||
+            overlap(outs[i].p, outs[i].n, gamma, sh.H * 2))
+            return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input without being in its place");
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return fail(MOE_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    const bool vectorized = sh.H % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(gamma, 16) &&
+                            aligned(residual_out, 16) && aligned(y, 16) && aligned(codes, 8);
+    const moe_dc::NormShape s{(int32_t)tokens, sh.H, sh.tok_f16, sh.quant_mode, sh.code_type,
+                              sh.scale_format, sh.scales_per_row, norm->epsilon};
+    const moe_dc::NormArgs a{x, residual, gamma, residual_out, y, codes, dynamic_scales};
+    return launched(moe_dc::launch_rms_norm(s, a, vectorized, static_cast<hipStream_t>(stream)),
+                    "norm kernel launch");
 }
 
 }  // extern "C"

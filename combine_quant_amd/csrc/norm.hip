@@ -1,0 +1,292 @@
+// norm.hip -- RMS norm of the tokens, with the residual's addition before and codes behind.
+//
+//   s = x + residual (fp32), y = s / sqrt(mean(s^2) + epsilon) * gamma, codes of y
+//
+// The kernel reads every token once and holds it in registers: one workgroup per token, SLOTS
+// vectors of eight elements a thread, so that a group of 128 is 16 adjacent lanes and an MX block 4.
+// The sum of squares (and in mode 2 the largest value) meets in LDS.  Codes are formed from y before
+// its rounding to the token type, by the functions dispatch uses.
+#include "dc_quantize.h"
+#include "norm_internal.h"
+
+namespace moe_dc {
+namespace {
+
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint4 o)
+{
+    const u32x4_t v = {o.x, o.y, o.z, o.w};
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 0);
+}
+
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, uint2 o)
+{
+    const u32x2_t v = {o.x, o.y};
+    __builtin_amdgcn_raw_buffer_store_b64(v, r, (int)off, 0, 0);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8], bool f16)
+{
+    return f16 ? make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                            pack_f16x2(f[6], f[7]))
+               : make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                            pack_bf16x2(f[6], f[7]));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+    return v;
+}
+
+// Sum over the workgroup; `scratch` holds one float per wave.
+__device__ __forceinline__ float block_sum(float v, float* scratch)
+{
+    v = wave_sum(v);
+    if ((threadIdx.x & (kWave - 1)) == 0) scratch[threadIdx.x / kWave] = v;
+    __syncthreads();
+    float r = 0.0f;
+    for (int w = 0; w < (int)(blockDim.x / kWave); ++w) r += scratch[w];
+    return r;
+}
+
+__device__ __forceinline__ float reciprocal_rms(const NormShape& s, float squares)
+{
+    return 1.0f / __builtin_sqrtf(squares / (float)s.H + s.epsilon);
+}
+
+// Shared exponent of an MX block, 0 where it holds an infinity or NaN.
+template <int MODE, int CT>
+__device__ __forceinline__ int shared_exp(uint32_t peak)
+{
+    return peak < 0x7F800000u ? mx_shared_exp<MODE, CT>(peak) : 0;
+}
+
+__device__ __forceinline__ float inverse_power(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
+
+// The scale of an MX block as the config stores it; `bad`: the block holds an infinity or NaN.
+__device__ __forceinline__ void store_mx_scale(const NormShape& s, void* scales, size_t at, int e, bool bad)
+{
+    if (s.scale_format == MOE_SCALE_E8M0)
+        static_cast<uint8_t*>(scales)[at] = bad ? 0xFFu : (uint8_t)(e + 127);
+    else
+        static_cast<float*>(scales)[at] = bad ? NAN : s.scale_format == MOE_SCALE_FP32 ? pow2f(e)
+                                                                                             : inverse_power(e);
+}
+
+template <int MODE, int CT, int SLOTS>
+__global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
+{
+    __shared__ float sums[16];
+    __shared__ uint32_t peaks[16];
+    const size_t token = blockIdx.x;
+    const uint32_t row = (uint32_t)s.H * 2;
+    const bool f16 = s.tok_f16;
+    const auto rsrc = [&](const void* p, uint32_t bytes) {
+        return make_rsrc(static_cast<const char*>(p) + token * bytes, bytes);
+    };
+    const __amdgpu_buffer_rsrc_t xr = rsrc(a.x, row), gr = make_rsrc(a.gamma, row);
+    // (an absent residual is a resource of no bytes: zeros)
+    const __amdgpu_buffer_rsrc_t rr = a.residual ? rsrc(a.residual, row) : make_rsrc(a.x, 0);
+    uint4 xv[SLOTS], rv[SLOTS], gv[SLOTS];
+    uint32_t at[SLOTS];
+#pragma unroll
+    for (int n = 0; n < SLOTS; ++n) {
+        at[n] = (threadIdx.x + n * blockDim.x) * 16;
+        xv[n] = load16(xr, at[n]);
+        rv[n] = load16(rr, at[n]);
+        gv[n] = load16(gr, at[n]);
+    }
+    float f[SLOTS][8];
+    float squares = 0.0f;
+#pragma unroll
+    for (int n = 0; n < SLOTS; ++n) {
+        float r[8];
+        unpack8(xv[n], f[n], f16);
+        unpack8(rv[n], r, f16);
+        float part = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (a.residual) f[n][q] = f[n][q] + r[q];
+            part += f[n][q] * f[n][q];
+        }
+        squares += part;
+    }
+    squares = block_sum(squares, sums);
+    if (a.residual_out) {
+        const __amdgpu_buffer_rsrc_t so = rsrc(a.residual_out, row);
+#pragma unroll
+        for (int n = 0; n < SLOTS; ++n) store16(so, at[n], pack8(f[n], f16));
+    }
+    const float rms = reciprocal_rms(s, squares);
+#pragma unroll
+    for (int n = 0; n < SLOTS; ++n) {
+        float g[8];
+        unpack8(gv[n], g, f16);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[n][q] = f[n][q] * rms * g[q];
+    }
+    if (a.y) {
+        const __amdgpu_buffer_rsrc_t yo = rsrc(a.y, row);
+#pragma unroll
+        for (int n = 0; n < SLOTS; ++n) store16(yo, at[n], pack8(f[n], f16));
+    }
+    if (MODE == 0) return;
+
+    // vectors past the row's end hold zeros (gamma is read as 0 there), or NaN where the row's
+    // reciprocal is infinite or NaN; they are left out of the largest values
+    const __amdgpu_buffer_rsrc_t co = rsrc(a.codes, (uint32_t)s.H);
+    uint32_t most[SLOTS];
+#pragma unroll
+    for (int n = 0; n < SLOTS; ++n) most[n] = at[n] < row ? absmax8(f[n], 0u) : 0u;
+    if (MODE == 2) {
+        uint32_t peak = most[0];
+#pragma unroll
+        for (int n = 1; n < SLOTS; ++n) peak = dpp_max(peak, most[n]);
+        peak = block_max_u32(peak, peaks);
+        float dyn, scale;
+        group_dyn<CT>(peak, dyn, scale);
+#pragma unroll
+        for (int n = 0; n < SLOTS; ++n) store8(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
+        if (threadIdx.x == 0) static_cast<float*>(a.scales)[token] = scale;
+    } else if (MODE == 3) {
+#pragma unroll
+        for (int n = 0; n < SLOTS; ++n) {
+            const uint32_t peak = group_max_u32<kGroup / 8>(most[n]);
+            float dyn, scale;
+            group_dyn<CT>(peak, dyn, scale);
+            store8(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
+            if ((threadIdx.x & (kGroup / 8 - 1)) == 0 && at[n] < row)
+                static_cast<float*>(a.scales)[token * s.scales_per_row + at[n] / (2 * kGroup)] = scale;
+        }
+    } else if (MODE >= 4) {
+#pragma unroll
+        for (int n = 0; n < SLOTS; ++n) {
+            const uint32_t peak = group_max_u32<kMxBlock / 8>(most[n]);
+            const int e = shared_exp<MODE, CT>(peak);
+            store8(co, at[n] / 2, dynamic_codes8<CT>(f[n], inverse_power(e)));
+            if ((threadIdx.x & (kMxBlock / 8 - 1)) == 0 && at[n] < row)
+                store_mx_scale(s, a.scales, token * s.scales_per_row + at[n] / (2 * kMxBlock), e,
+                               peak >= 0x7F800000u);
+        }
+        // the pad entry of an odd number of blocks
+        if (threadIdx.x == 0 && (s.H + kMxBlock - 1) / kMxBlock < s.scales_per_row) {
+            const size_t pad = token * s.scales_per_row + s.scales_per_row - 1;
+            if (s.scale_format == MOE_SCALE_E8M0) static_cast<uint8_t*>(a.scales)[pad] = 0;
+            else static_cast<float*>(a.scales)[pad] = 0.0f;
+        }
+    }
+}
+
+// Any H and any alignment: y of the token in LDS, a thread per group of codes.
+constexpr int kAnyThreads = 256;
+
+template <int MODE, int CT>
+__global__ __launch_bounds__(kAnyThreads) void norm_any_kernel(NormShape s, NormArgs a)
+{
+    __shared__ float y[8192];
+    __shared__ float sums[kAnyThreads / kWave];
+    __shared__ uint32_t peaks[kAnyThreads / kWave];
+    const size_t token = blockIdx.x, base = token * s.H;
+    const bool f16 = s.tok_f16;
+    const auto value = [&](const void* p, size_t i) { return tok_lo_rt(static_cast<const uint16_t*>(p)[i], f16); };
+    float squares = 0.0f;
+    for (int i = threadIdx.x; i < s.H; i += kAnyThreads) {
+        float v = value(a.x, base + i);
+        if (a.residual) v = v + value(a.residual, base + i);
+        y[i] = v;
+        squares += v * v;
+    }
+    squares = block_sum(squares, sums);
+    const float rms = reciprocal_rms(s, squares);
+    uint32_t peak = 0;
+    for (int i = threadIdx.x; i < s.H; i += kAnyThreads) {
+        if (a.residual_out) static_cast<uint16_t*>(a.residual_out)[base + i] = (uint16_t)f32_to_tok_rt(y[i], f16);
+        const float v = y[i] * rms * value(a.gamma, i);
+        y[i] = v;
+        peak = dpp_max(peak, __float_as_uint(v) & 0x7FFFFFFFu);
+        if (a.y) static_cast<uint16_t*>(a.y)[base + i] = (uint16_t)f32_to_tok_rt(v, f16);
+    }
+    if (MODE == 0) return;
+    __syncthreads();
+    uint8_t* codes = static_cast<uint8_t*>(a.codes) + base;
+    const auto code = [&](int i, float by) {
+        const float p = y[i] * by;
+        codes[i] = CT == kCodeInt8 ? (uint8_t)int8_code(p) : p != p ? (uint8_t)0 : (uint8_t)fp8_code<CT>(p);
+    };
+    if (MODE == 2) {
+        peak = block_max_u32(peak, peaks);
+        float dyn, scale;
+        group_dyn<CT>(peak, dyn, scale);
+        for (int i = threadIdx.x; i < s.H; i += kAnyThreads) code(i, dyn);
+        if (threadIdx.x == 0) static_cast<float*>(a.scales)[token] = scale;
+        return;
+    }
+    constexpr int kSpan = MODE == 3 ? kGroup : kMxBlock;
+    for (int b = threadIdx.x; b < s.scales_per_row; b += kAnyThreads) {
+        const int lo = b * kSpan, hi = lo + kSpan < s.H ? lo + kSpan : s.H;
+        const size_t at = token * s.scales_per_row + b;
+        uint32_t most = 0;
+        for (int i = lo; i < hi; ++i) most = dpp_max(most, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+        if (MODE == 3) {
+            float dyn, scale;
+            group_dyn<CT>(most, dyn, scale);
+            for (int i = lo; i < hi; ++i) code(i, dyn);
+            static_cast<float*>(a.scales)[at] = scale;
+        } else if (lo >= s.H) {
+            if (s.scale_format == MOE_SCALE_E8M0) static_cast<uint8_t*>(a.scales)[at] = 0;
+            else static_cast<float*>(a.scales)[at] = 0.0f;
+        } else {
+            const int e = shared_exp<MODE, CT>(most);
+            for (int i = lo; i < hi; ++i) code(i, inverse_power(e));
+            store_mx_scale(s, a.scales, at, e, most >= 0x7F800000u);
+        }
+    }
+}
+
+// Few tokens: as many threads as vectors; many: four vectors a thread.
+constexpr int kSlotsMany = 2;
+
+template <int MODE, int CT>
+hipError_t launch(const NormShape& s, const NormArgs& a, bool vectorized, hipStream_t stream)
+{
+    const dim3 grid((unsigned)s.tokens);
+    if (!vectorized) {
+        norm_any_kernel<MODE, CT><<<grid, kAnyThreads, 0, stream>>>(s, a);
+        return hipGetLastError();
+    }
+    const int vectors = s.H / 8;
+    if (s.tokens < 1024) {
+        norm_kernel<MODE, CT, 1><<<grid, (vectors + kWave - 1) / kWave * kWave, 0, stream>>>(s, a);
+    } else {
+        const int threads = (vectors + kSlotsMany - 1) / kSlotsMany;
+        norm_kernel<MODE, CT, kSlotsMany><<<grid, (threads + kWave - 1) / kWave * kWave, 0, stream>>>(s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormShape& s, const NormArgs& a, bool vectorized, hipStream_t stream)
+{
+    switch (s.quant_mode * 8 + (s.quant_mode ? s.code_type : 0)) {
+    case 0: return launch<0, kCodeBf16>(s, a, vectorized, stream);
+    case 2 * 8 + kCodeInt8: return launch<2, kCodeInt8>(s, a, vectorized, stream);
+    case 2 * 8 + kCodeE4m3: return launch<2, kCodeE4m3>(s, a, vectorized, stream);
+    case 2 * 8 + kCodeE5m2: return launch<2, kCodeE5m2>(s, a, vectorized, stream);
+    case 3 * 8 + kCodeE4m3: return launch<3, kCodeE4m3>(s, a, vectorized, stream);
+    case 3 * 8 + kCodeE5m2: return launch<3, kCodeE5m2>(s, a, vectorized, stream);
+    case 4 * 8 + kCodeE4m3: return launch<4, kCodeE4m3>(s, a, vectorized, stream);
+    case 4 * 8 + kCodeE5m2: return launch<4, kCodeE5m2>(s, a, vectorized, stream);
+    case 5 * 8 + kCodeE4m3: return launch<5, kCodeE4m3>(s, a, vectorized, stream);
+    default: return launch<5, kCodeE5m2>(s, a, vectorized, stream);
+    }
+}
+
+}  // namespace moe_dc

@@ -511,6 +511,45 @@ moe_status moe_gate_topk(const moe_dc_config* cfg, const moe_gate* gate, const f
                          const float* bias, int32_t* expert_ids, float* expert_scales,
                          void* stream);
 
+/* ---- the norm before the router ------------------------------------------------------------ */
+
+/* Attributes of the norm.  One float and one int32, 8 bytes. */
+typedef struct {
+    float epsilon;              /* finite, > 0                                              */
+    int32_t reserved;           /* 0                                                        */
+} moe_norm;
+
+/* moe_rms_norm -- the tokens that router and dispatch take: RMS norm, with the residual's addition
+ * before it and 8-bit codes behind it.
+ *
+ * For every token, over its H elements, in fp32:
+ *   s = x + residual                      (x alone without a residual)
+ *   y = s / sqrt(mean(s^2) + epsilon) * gamma
+ *   residual_out = s, y = y, rounded to the token type (nearest even)
+ *   codes, dynamic_scales = y (before that rounding) coded as moe_dispatch codes a token with
+ *                  cfg->quant_mode 2, 3, 4 or 5, cfg->out_dtype and cfg->scale_format
+ * They follow the conventions at the top of this header; H not a multiple of 8 or tensors that are
+ * not 16-byte aligned (codes: 8) select a slower kernel.
+ *   x              token type [W][BS][H]
+ *   residual       token type [W][BS][H] or NULL
+ *   gamma          token type [H]
+ *   residual_out   token type [W][BS][H], or NULL; may be residual or x itself (in place)
+ *   y              token type [W][BS][H], NULL allowed with codes; may be x or residual itself
+ *   codes          bytes [W][BS][H]; NULL iff quant_mode is 0
+ *   dynamic_scales [W][BS][moe_dc_scales_per_row(cfg)] in cfg->scale_format; NULL iff quant_mode
+ *                  is 0
+ * The codes are rows for moe_grouped_matmul: mode 2 ROW, mode 3 BLOCK, modes 4/5 with E8M0 MX.
+ * Numerics: the mean is a sum in fp32, in an order that depends on H and on the number of tokens;
+ * s^2 must not leave the range of fp32.  A token with an infinity or NaN, or whose sum of squares
+ * is infinite, has NaN or zeros in y; a scale whose token, group or block holds one is NaN (E8M0:
+ * 255) and the code of a NaN is 0.
+ * Errors: MOE_ERR_UNSUPPORTED for quant_mode 1, a scales tensor and E2M1; MOE_ERR_INVALID_ARG for
+ * outputs that overlap each other or an input other than in its place; otherwise as for
+ * moe_dispatch.  Needs no workspace; one kernel. */
+moe_status moe_rms_norm(const moe_dc_config* cfg, const moe_norm* norm, const void* x,
+                        const void* residual, const void* gamma, void* residual_out, void* y,
+                        void* codes, void* dynamic_scales, void* stream);
+
 /* Text of the last non-OK status on this thread ("" if none). */
 const char* moe_dc_last_error(void);
 
