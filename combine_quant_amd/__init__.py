@@ -11,7 +11,7 @@ from .binding import (  # noqa: F401
     MOE_SCALE_FP32, MOE_SCALE_FP32_RECIPROCAL, MOE_SCALES_NONE, MOE_SCALES_PER_EXPERT,
     MOE_SCALES_SCALAR, MOE_SCALES_SHARED, MOE_TOKEN_BF16, MOE_TOKEN_F16, Launch, MoeDcConfig, MoeDcError,
     MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_MM_SCALE_BLOCK, MOE_MM_SCALE_MX, MOE_MM_SCALE_NONE, MOE_MM_SCALE_ROW,
-    MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W4_E2M1, MOE_W4_INT4, MoeGate, MoeMatmul, MoeNorm,
+    MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W4_E2M1, MOE_W4_INT4, MoeExperts, MoeGate, MoeMatmul, MoeNorm,
     alloc_dispatch_outputs, gate_topk, grouped_matmul, grouped_matmul_quantize, grouped_matmul_w4, make_gate, make_matmul, make_norm,
     moe_gate_topk, moe_grouped_matmul, moe_grouped_matmul_quantize, moe_grouped_matmul_w4, prepare_gate_topk,
     prepare_grouped_matmul, prepare_grouped_matmul_quantize, prepare_grouped_matmul_w4, token_torch_dtype,
@@ -21,4 +21,5 @@ from .binding import (  # noqa: F401
     moe_dc_dispatch_workspace_bytes, moe_dc_last_error, moe_dc_scales_per_row,
     moe_dc_validate, moe_dc_version, moe_dispatch, moe_dispatch_no_workspace, prepare_combine, prepare_combine_int8,
     prepare_combine_quantize, prepare_combine_scatter, prepare_dispatch, moe_rms_norm,
-    prepare_rms_norm, rms_norm)
+    prepare_rms_norm, rms_norm, experts_layer, make_experts,
+    moe_dc_experts_layer_workspace_bytes, moe_experts_layer, prepare_experts_layer)

@@ -34,6 +34,7 @@ EXPORTS = ("moe_dc_validate", "moe_dc_scales_per_row", "moe_dc_dispatch_workspac
            "moe_combine_scatter", "moe_combine_quantize", "moe_combine_int8",
            "moe_gate_topk", "moe_grouped_matmul", "moe_grouped_matmul_quantize",
            "moe_grouped_matmul_w4", "moe_rms_norm",
+           "moe_dc_experts_layer_workspace_bytes", "moe_experts_layer",
            "moe_dc_last_error", "moe_dc_version")
 
 
@@ -106,6 +107,14 @@ class MoeNorm(ctypes.Structure):
     ]
 
 
+class MoeExperts(ctypes.Structure):
+    """Mirror of moe_experts."""
+    _fields_ = [
+        ("intermediate", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+    ]
+
+
 class MoeDcError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{_STATUS.get(status, status)}: {message}")
@@ -155,6 +164,11 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     lib.moe_gate_topk.argtypes = [cfgp, gatep] + [P] * 4 + [P]
     lib.moe_rms_norm.restype = ctypes.c_int
     lib.moe_rms_norm.argtypes = [cfgp, ctypes.POINTER(MoeNorm)] + [P] * 7 + [P]
+    expp = ctypes.POINTER(MoeExperts)
+    lib.moe_dc_experts_layer_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_dc_experts_layer_workspace_bytes.argtypes = [cfgp, expp]
+    lib.moe_experts_layer.restype = ctypes.c_int
+    lib.moe_experts_layer.argtypes = [cfgp, expp] + [P] * 11 + [ctypes.c_size_t, P]
     lib.moe_dc_last_error.restype = ctypes.c_char_p
     lib.moe_dc_last_error.argtypes = []
     lib.moe_dc_version.restype = ctypes.c_char_p
@@ -187,6 +201,10 @@ def make_gate(score=MOE_SCORE_SOFTMAX, group_count=1, group_keep=1, group_top=1,
 
 def make_norm(epsilon=1e-6):
     return MoeNorm(epsilon, 0)
+
+
+def make_experts(intermediate, scaling=MOE_MM_SCALE_NONE):
+    return MoeExperts(intermediate, scaling)
 
 
 def token_torch_dtype(cfg):
@@ -632,6 +650,45 @@ def moe_rms_norm(cfg, norm, x, residual, gamma, residual_out, y, codes, dynamic_
                             dynamic_scales), stream)
 
 
+# -- the whole layer for few tokens ------------------------------------------------------------
+
+def moe_dc_experts_layer_workspace_bytes(cfg, experts) -> int:
+    return load_library().moe_dc_experts_layer_workspace_bytes(ctypes.byref(cfg),
+                                                               ctypes.byref(experts))
+
+
+def _experts_layer_call(cfg, experts, x, expert_ids, expert_scales, x_active_mask, up, up_scales,
+                        down, down_scales, shared_x, y, workspace):
+    W, BS, H, K, E, F = (cfg.ep_world_size, cfg.bs, cfg.hidden, cfg.topk, cfg.moe_expert_num,
+                         experts.intermediate)
+    dev, token = y.device, token_torch_dtype(cfg)
+    wtype = _ROW_DTYPES[MOE_DTYPE_E4M3] if experts.scaling == MOE_MM_SCALE_BLOCK else token
+    mshape = {1: (W, BS), 2: (W, BS, K)}.get(cfg.mask_kind)
+    args = [
+        _ptr(x, token, (W, BS, H), "x", dev),
+        _ptr(expert_ids, torch.int32, (W, BS, K), "expert_ids", dev),
+        _ptr(expert_scales, torch.float32, (W, BS, K), "expert_scales", dev),
+        _ptr(x_active_mask, (torch.uint8, torch.bool), mshape, "x_active_mask", dev),
+        _ptr(up, wtype, (E, 2 * F, H), "up", dev),
+        _ptr(up_scales, torch.float32, (E, 2 * _groups(F), _groups(H)), "up_scales", dev),
+        _ptr(down, wtype, (E, H, F), "down", dev),
+        _ptr(down_scales, torch.float32, (E, _groups(H), _groups(F)), "down_scales", dev),
+        _ptr(shared_x, token, (W, BS, H), "shared_x", dev),
+        _ptr(y, token, (W, BS, H), "y", dev),
+        _ptr(workspace, torch.uint8, None, "workspace", dev),
+    ]
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    return (load_library().moe_experts_layer,
+            (ctypes.byref(cfg), ctypes.byref(experts), *args, ctypes.c_size_t(ws_bytes)), dev)
+
+
+def moe_experts_layer(cfg, experts, x, expert_ids, expert_scales, x_active_mask, up, up_scales,
+                      down, down_scales, shared_x, y, workspace, stream=None):
+    """Enqueue the experts' layer of up to 64 tokens on `stream`."""
+    _launch(*_experts_layer_call(cfg, experts, x, expert_ids, expert_scales, x_active_mask, up,
+                                 up_scales, down, down_scales, shared_x, y, workspace), stream)
+
+
 # -- allocation helpers (torch owns the memory; the library never allocates) ----------------
 
 def alloc_dispatch_outputs(cfg, device="cuda"):
@@ -888,3 +945,29 @@ def rms_norm(cfg, norm, x, gamma, residual=None, out=None, stream=None):
     launch, out = prepare_rms_norm(cfg, norm, x, gamma, residual, out)
     launch(stream)
     return out
+
+
+def prepare_experts_layer(cfg, experts, x, expert_ids, expert_scales, up, down, up_scales=None,
+                          down_scales=None, x_active_mask=None, shared_x=None, y=None,
+                          workspace=None):
+    """Plan for moe_experts_layer: (launch, y)."""
+    y = _new_y(cfg, x) if y is None else y
+    if workspace is None:
+        workspace = torch.empty((moe_dc_experts_layer_workspace_bytes(cfg, experts),),
+                                dtype=torch.uint8, device=x.device)
+    fn, args, dev = _experts_layer_call(cfg, experts, x, expert_ids, expert_scales, x_active_mask,
+                                        up, up_scales, down, down_scales, shared_x, y, workspace)
+    keep = (cfg, experts, x, expert_ids, expert_scales, up, down, up_scales, down_scales,
+            x_active_mask, shared_x, y, workspace)
+    return Launch(fn, args, dev, keep), y
+
+
+def experts_layer(cfg, experts, x, expert_ids, expert_scales, up, down, up_scales=None,
+                  down_scales=None, x_active_mask=None, shared_x=None, y=None, workspace=None,
+                  stream=None):
+    """Allocate (or reuse `y` / `workspace`) and enqueue moe_experts_layer; returns y."""
+    launch, y = prepare_experts_layer(cfg, experts, x, expert_ids, expert_scales, up, down,
+                                      up_scales, down_scales, x_active_mask, shared_x, y,
+                                      workspace)
+    launch(stream)
+    return y

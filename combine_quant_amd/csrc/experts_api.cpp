@@ -1,10 +1,11 @@
-// experts_api.cpp -- C ABI of the norm, the router and the experts' products: host validation and
-// launch.
+// experts_api.cpp -- C ABI of the norm, the router, the experts' products and the layer of a few
+// tokens: host validation and launch.
 //
 // As in api.cpp, nothing here allocates device memory or synchronises the host; each call is
-// one kernel on the caller's stream.
+// one kernel on the caller's stream (the layer two).
 #include "moe_dc.h"
 #include "experts_internal.h"
+#include "layer_internal.h"
 #include "norm_internal.h"
 
 #include <cmath>
@@ -63,6 +64,32 @@ moe_status check_overlap(const MatmulShape& s, const MatmulArgs& a, int64_t x, i
             return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
     if (overlap(a.out, out, a.out_scales, scales))
         return fail(MOE_ERR_INVALID_ARG, "codes and out_scales overlap");
+    return MOE_OK;
+}
+
+// The rules of the layer's attributes; fills *s.
+moe_status check_layer(const moe_dc_config* cfg, const moe_experts* experts, moe_dc::LayerShape* s)
+{
+    moe_dc::Shape sh;
+    moe_status st = moe_dc::check_config(cfg, &sh);
+    if (st != MOE_OK) return st;
+    if (!experts) return fail(MOE_ERR_INVALID_ARG, "experts description is NULL");
+    if (experts->scaling != MOE_MM_SCALE_NONE && experts->scaling != MOE_MM_SCALE_BLOCK)
+        return fail(MOE_ERR_INVALID_ARG, "scaling %d is not one of 0 (token weights), 3 (block)",
+                    experts->scaling);
+    const int32_t step = experts->scaling == MOE_MM_SCALE_BLOCK ? 16 : 8;
+    if (experts->intermediate < 1 || experts->intermediate > 32768)
+        return fail(MOE_ERR_INVALID_ARG, "intermediate %d outside [1, 32768]", experts->intermediate);
+    if (sh.H % step != 0 || experts->intermediate % step != 0)
+        return fail(MOE_ERR_INVALID_ARG, "hidden %d and intermediate %d must be multiples of %d", sh.H,
+                    experts->intermediate, step);
+    if ((int64_t)sh.W * sh.BS > moe_dc::kLayerTokens)
+        return fail(MOE_ERR_UNSUPPORTED, "%lld tokens: the layer takes up to %d", (long long)sh.W * sh.BS,
+                    moe_dc::kLayerTokens);
+    const int32_t T = sh.W * sh.BS, picks = T * sh.K;
+    *s = moe_dc::LayerShape{T, sh.K, sh.E, sh.zero_end, sh.id_end, sh.H, experts->intermediate,
+                            experts->scaling == MOE_MM_SCALE_BLOCK ? 1 : 0, sh.tok_f16, sh.mask_kind,
+                            sh.E < picks ? sh.E : picks};
     return MOE_OK;
 }
 
@@ -354,6 +381,55 @@ moe_status moe_rms_norm(const moe_dc_config* cfg, const moe_norm* norm, const vo
     const moe_dc::NormArgs a{x, residual, gamma, residual_out, y, codes, dynamic_scales};
     return launched(moe_dc::launch_rms_norm(s, a, vectorized, static_cast<hipStream_t>(stream)),
                     "norm kernel launch");
+}
+
+size_t moe_dc_experts_layer_workspace_bytes(const moe_dc_config* cfg, const moe_experts* experts)
+{
+    moe_dc::LayerShape s;
+    return check_layer(cfg, experts, &s) == MOE_OK ? moe_dc::layer_workspace_bytes(s) : 0;
+}
+
+moe_status moe_experts_layer(const moe_dc_config* cfg, const moe_experts* experts, const void* x,
+                             const int32_t* expert_ids, const float* expert_scales,
+                             const uint8_t* x_active_mask, const void* up, const float* up_scales,
+                             const void* down, const float* down_scales, const void* shared_x, void* y,
+                             void* workspace, size_t workspace_bytes, void* stream)
+{
+    moe_dc::LayerShape s;
+    moe_status st = check_layer(cfg, experts, &s);
+    if (st != MOE_OK) return st;
+    if (!x || !expert_ids || !expert_scales || !up || !down || !y)
+        return fail(MOE_ERR_INVALID_ARG, "a required tensor pointer is NULL");
+    if ((s.mask_kind != 0) != (x_active_mask != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "x_active_mask must be given iff mask_kind != 0");
+    if ((s.block != 0) != (up_scales != nullptr) || (s.block != 0) != (down_scales != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "up_scales and down_scales must be given iff scaling is _BLOCK");
+    const size_t need = moe_dc::layer_workspace_bytes(s);
+    if (!workspace || workspace_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    if (!aligned(x, 16) || !aligned(up, 16) || !aligned(down, 16) || !aligned(workspace, 16))
+        return fail(MOE_ERR_INVALID_ARG, "x, up, down and workspace must be 16-byte aligned");
+    if (!aligned(expert_ids, 4) || !aligned(expert_scales, 4) || !aligned(up_scales, 4) ||
+        !aligned(down_scales, 4) || !aligned(shared_x, 2) || !aligned(y, 2))
+        return fail(MOE_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+    const int64_t rows = (int64_t)s.T * s.H * 2, picks = (int64_t)s.T * s.K, each = s.block ? 1 : 2;
+    const int64_t weights = (int64_t)s.E * s.F * s.H * each, gf = groups_of(s.F), gh = groups_of(s.H);
+    const struct { const void* p; int64_t n; } ins[9] = {
+        {x, rows}, {expert_ids, picks * 4}, {expert_scales, picks * 4},
+        {x_active_mask, s.mask_kind == 1 ? s.T : picks}, {up, 2 * weights}, {down, weights},
+        {up_scales, s.E * 2 * gf * gh * 4}, {down_scales, s.E * gf * gh * 4}, {shared_x, rows}};
+    for (const auto& in : ins)
+        if (overlap(y, rows, in.p, in.n) || overlap(workspace, (int64_t)need, in.p, in.n))
+            return fail(MOE_ERR_INVALID_ARG, "y or workspace overlaps an input");
+    if (overlap(y, rows, workspace, (int64_t)need))
+        return fail(MOE_ERR_INVALID_ARG, "y and workspace overlap");
+    char* ws = static_cast<char*>(workspace);
+    const moe_dc::LayerArgs a{x, expert_ids, expert_scales, x_active_mask, up, up_scales, down, down_scales,
+                              shared_x, y, reinterpret_cast<moe_dc::Slot*>(ws),
+                              reinterpret_cast<int32_t*>(ws + moe_dc::layer_tokens_offset(s)),
+                              ws + moe_dc::layer_h_offset(s)};
+    return launched(moe_dc::launch_experts_layer(s, a, static_cast<hipStream_t>(stream)),
+                    "experts' layer launch");
 }
 
 }  // extern "C"

@@ -550,6 +550,54 @@ moe_status moe_rms_norm(const moe_dc_config* cfg, const moe_norm* norm, const vo
                         const void* residual, const void* gamma, void* residual_out, void* y,
                         void* codes, void* dynamic_scales, void* stream);
 
+/* ---- the whole layer for few tokens -------------------------------------------------------- */
+
+/* The experts of a layer.  Two int32, 8 bytes. */
+typedef struct {
+    int32_t intermediate;       /* F, in [1, 32768]: gate rows (and up rows) of an expert    */
+    int32_t scaling;            /* MOE_MM_SCALE_NONE: weights of the token type; _BLOCK: E4M3
+                                   with one fp32 per block of 128 x 128 elements             */
+} moe_experts;
+
+/* Workspace bytes moe_experts_layer needs (the picks' rows of F tokens,
+ * and up to 20 KiB).  0 for an invalid config or description.  Scratch, as for dispatch; one workspace must
+ * not be used by two calls that may run concurrently. */
+size_t moe_dc_experts_layer_workspace_bytes(const moe_dc_config* cfg, const moe_experts* experts);
+
+/* moe_experts_layer -- everything between the router and the residual for up to 64 tokens (W * BS),
+ * in two kernels: what moe_dispatch, two products and moe_combine do for many.
+ *
+ * For every token t, over its active picks k of expert e with weight w:
+ *   h = silu(x . gate_e) * (x . up_e), y = sum over k of w * (h . down_e)
+ * with up = gate rows [0, F), then up rows [F, 2F).  A zero expert adds nothing, a copy expert
+ * w * x; shared_x (the shared expert's output) is added at the end.
+ *   x              token type [W][BS][H]
+ *   expert_ids     int32 [W][BS][K], expert_scales fp32 [W][BS][K]: as moe_gate_topk gives them
+ *   x_active_mask  as for moe_dispatch (an inactive pick contributes nothing)
+ *   up             [E][2F][H], down [E][H][F]: tokens, or E4M3 codes
+ *   up_scales      fp32 [E][2 Ceil(F, 128)][Ceil(H, 128)] (the gate rows' blocks, then those of the
+ *                  up rows, as moe_grouped_matmul takes them), down_scales fp32
+ *                  [E][Ceil(H, 128)][Ceil(F, 128)]; NULL without _BLOCK
+ *   shared_x       token type [W][BS][H] or NULL
+ *   y              token type [W][BS][H]; a token without active picks gets shared_x or +0
+ *   workspace      moe_dc_experts_layer_workspace_bytes bytes
+ * H and F must be multiples of 8 (tokens) or 16 (_BLOCK); x, up, down and workspace 16-byte aligned.
+ * cfg's quantization attributes are not used.
+ * Numerics: products of token values and codes are exact (the tokens are not quantized); sums are
+ * fp32 in an order that depends on the sizes and ids only; _BLOCK sums the products of a block,
+ * multiplies by its scale and adds; SwiGLU as for moe_grouped_matmul.  w * h is rounded to the token
+ * type between the two products (w is the sum of the weights where a token picked an expert more
+ * than once) and y once at the end.  An infinity or NaN in a weight reaches only the tokens that
+ * picked its expert.
+ * Errors: MOE_ERR_UNSUPPORTED for more than 64 tokens; y or the workspace overlapping an input is
+ * MOE_ERR_INVALID_ARG; otherwise as for moe_dispatch.  Picks with ids out of range count as
+ * inactive. */
+moe_status moe_experts_layer(const moe_dc_config* cfg, const moe_experts* experts, const void* x,
+                             const int32_t* expert_ids, const float* expert_scales,
+                             const uint8_t* x_active_mask, const void* up, const float* up_scales,
+                             const void* down, const float* down_scales, const void* shared_x,
+                             void* y, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Text of the last non-OK status on this thread ("" if none). */
 const char* moe_dc_last_error(void);
 
