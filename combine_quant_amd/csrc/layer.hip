@@ -1,35 +1,51 @@
 // layer.hip -- the experts' layer of a few tokens: y[t] = sum over k of w[t][k] * down(swiglu(up(x[t])))
 // of the pick's expert, in two kernels.
 //
-// With few tokens the layer is the reading of the weights of the experts that have any, once.  Both
-// kernels walk weight rows in chunks of 128 bytes from memory to matrix registers, as the streaming
-// products do; nothing is packed or sent, a row of the matrix operand is a token where it lies.
+// With few tokens the layer is the reading of the weights of the experts that have any, once; nothing is
+// packed or sent, a row of the matrix operand is a token where it lies.  Both kernels walk weight rows
+// in chunks of 128 bytes.  Every wave has a ring of stages in LDS, which its own loads fill directly,
+// several chunks ahead (whole 128-byte rows, and no registers for what is on its way), so that no
+// barrier holds the stream up.
 //
-//   up:   one workgroup per (expert with tokens, 16 columns): four waves take chunks of the inner
+//   up:   one workgroup per (expert with tokens, 16 columns): the waves take chunks of the inner
 //         dimension in turn; gate and up rows, SwiGLU and the pick's weight, h in the token type.
-//         Every workgroup finds its expert and its tokens in the ids by itself, one lane a token.
-//   down: one workgroup per 16 columns of y: eight waves take the chunks of all experts in turn;
+//         Every wave finds its expert and its tokens in the ids by itself, one lane a token.
+//   down: one workgroup per 16 or 32 columns of y: the waves take the chunks of all experts in turn;
 //         an expert's sums are added to its tokens' in LDS, and the waves' in the end, in an order
 //         that depends on the ids only.
 #include "dc_device.h"
 #include "experts_device.h"
+#include "experts_tiles.h"
 #include "layer_internal.h"
 
 namespace moe_dc {
 namespace {
 
-constexpr int kUpWaves = 4;
-constexpr int kDownWaves = 8;
-constexpr int kCols = 16;                       // columns of a workgroup (SwiGLU: of gate and of up)
+constexpr int kRing = 2;                        // stages of a wave
+// Many small workgroups hide each other's start and end.  Two waves with two stages against four
+// with two and four with three, us: 1 token on 8 experts of 7168 x 2048 bf16 127, 131, 133; 32 tokens
+// on 256 experts E4M3 1214, 1224, 1276, on 64 experts 471, 545, 621.
+constexpr int kUpWaves = 2;
+// Columns of y and waves of a workgroup: many columns share the rows of h, but few workgroups leave
+// CUs idle.  32 columns and four waves against 16 and eight, us: H = 7168, 32 tokens on 64 experts
+// E4M3 471 and 501, 64 tokens 492 and 529; H = 2048, 16 tokens on 32 experts x 1408 bf16 132 and 108,
+// H = 4096, 8 tokens on 8 experts x 1024 48.9 and 45.2.
+constexpr int kWideDown = 32 * 192;             // H from which it takes 32
 constexpr int kMaxIds = 1024;                   // experts
+constexpr int kMaxChunks = 64;                  // of an up row with scales (H <= 8192)
 
-// Operands.  A chunk is 128 bytes of a weight row: 64 tokens or 128 E4M3 codes.  Lane l holds, of
-// weight row l % 16, the 16 bytes at (l / 16) * 16 and at 64 + (l / 16) * 16, and of x (or h) the
-// elements that meet them.
-template <bool F16, bool BLOCK>
-struct Chunk {
-    static constexpr int kElements = BLOCK ? 128 : 64;
-    static constexpr int kXLoads = BLOCK ? 4 : 2;           // of 16 bytes, per row of x and chunk
+// A chunk is 128 bytes of a weight row: 64 tokens or 128 E4M3 codes, which meet 128 or 256 bytes of a
+// row of x (or h), one or two halves of 128.  NT tiles of 16 weight rows and RP rows of x make a
+// stage; a load fills 1 KB of it.
+template <bool F16, bool BLOCK, int NT, int RP>
+struct Stage {
+    static constexpr int kHalves = BLOCK ? 2 : 1;
+    static constexpr int kTiles = (RP + 15) / 16;            // of rows of x
+    static constexpr int kW = NT * 2048;
+    static constexpr int kX = RP * 128 * kHalves < 1024 ? 1024 : RP * 128 * kHalves;
+    static constexpr int kBytes = kW + kX;
+    static constexpr int kXLoads = kX / 1024;
+    static constexpr int kLoads = NT * 2 + kXLoads;
 
     // Two codes of a dword as a pair of 16-bit floats, exactly.
     template <bool HI>
@@ -47,8 +63,35 @@ struct Chunk {
             return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_t, a),
                                                            __builtin_bit_cast(v8bf_t, b), acc, 0, 0, 0);
     }
-    // acc + weights (two loads) times x (kXLoads loads)
-    static __device__ __forceinline__ v4f_t mma(const v4i_t (&w)[2], const v4i_t (&x)[kXLoads], v4f_t acc)
+
+    // What a lane reads of a stage: of weight row l % 16 the pieces (16 bytes) l / 16 and 4 + l / 16,
+    // and of row l % 16 of x those that meet them.  Piece p of row r lies at place p ^ (r & 7).
+    struct Regs {
+        v4i_t w[NT][2];
+        v4i_t x[kTiles][2 * kHalves];
+    };
+    static __device__ __forceinline__ void read(const char* st, Regs& r)
+    {
+        const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                r.w[t][p] = *reinterpret_cast<const v4i_t*>(st + t * 2048 + l16 * 128 +
+                                                            (((p * 4 + g) ^ (l16 & 7)) << 4));
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+            const int row = m * 16 + (RP < 16 ? l16 % RP : l16);
+            const char* xs = st + kW + row * 128;
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const int half = BLOCK ? i >> 1 : 0, piece = BLOCK ? 2 * g + (i & 1) : i * 4 + g;
+                r.x[m][i] = *reinterpret_cast<const v4i_t*>(xs + half * RP * 128 + ((piece ^ (row & 7)) << 4));
+            }
+        }
+    }
+    // acc + a weight tile times a tile of rows
+    static __device__ __forceinline__ v4f_t mma(const v4i_t (&w)[2], const v4i_t (&x)[2 * kHalves], v4f_t acc)
     {
         if constexpr (BLOCK) {
 #pragma unroll
@@ -63,65 +106,97 @@ struct Chunk {
             return mma16(w[1], x[1], mma16(w[0], x[0], acc));
         }
     }
-    // Byte offsets of the lane's pieces of chunk c; past the row's end they are past every resource.
-    static __device__ __forceinline__ void offsets(int c, int g, uint32_t row_bytes, uint32_t (&wo)[2],
-                                                   uint32_t (&xo)[kXLoads])
+
+    // Byte offsets of the lane's pieces within a chunk, for the loads: weights (of a tile's first 8
+    // rows) and, of load i, the row of x, its half and piece.
+    static __device__ __forceinline__ uint32_t wpiece()
     {
+        const int lane = threadIdx.x & (kWave - 1);
+        return (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+    }
+    static __device__ __forceinline__ int xrow(int i)
+    {
+        const int at = (i * kWave + (int)(threadIdx.x & (kWave - 1))) / 8;
+        return at / RP < kHalves ? at % RP : RP;             // RP: none
+    }
+    static __device__ __forceinline__ uint32_t xpiece(int i)
+    {
+        const int lane = threadIdx.x & (kWave - 1), at = (i * kWave + lane) / 8;
+        return (uint32_t)(at / RP * 128 + (((lane & 7) ^ (at % RP & 7)) << 4));
+    }
+    // Loads chunk c into a stage.  wr: NT tiles' resources; row_bytes of a weight row; xoff: offset of
+    // the row of x (kRsrcPastEnd: none) for load i.
+    static __device__ __forceinline__ void fill(char* st, const __amdgpu_buffer_rsrc_t (&wr)[NT],
+                                                __amdgpu_buffer_rsrc_t xr, uint32_t row_bytes,
+                                                const uint32_t (&xoff)[kXLoads], int c)
+    {
+        const uint32_t k = (uint32_t)c * 128 + wpiece();
+        const uint32_t w0 = k < row_bytes ? ((threadIdx.x & (kWave - 1)) >> 3) * row_bytes + k : kRsrcPastEnd;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const uint32_t k = (uint32_t)c * 128 + p * 64 + g * 16;
-            wo[p] = k < row_bytes ? k : kRsrcPastEnd;
-            if constexpr (BLOCK) {
-                xo[2 * p] = k < row_bytes ? 2 * k : kRsrcPastEnd;
-                xo[2 * p + 1] = k < row_bytes ? 2 * k + 16 : kRsrcPastEnd;
-            } else {
-                xo[p] = wo[p];
-            }
+        for (int t = 0; t < NT; ++t) {
+            load_lds16(wr[t], st + t * 2048, w0);
+            load_lds16(wr[t], st + t * 2048 + 1024, w0 == kRsrcPastEnd ? w0 : w0 + 8 * row_bytes);
+        }
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) {
+            const uint32_t q = (uint32_t)c * (128 * kHalves) + xpiece(i);
+            load_lds16(xr, st + kW + i * 1024,
+                       xoff[i] != kRsrcPastEnd && q < row_bytes * kHalves ? xoff[i] + q : kRsrcPastEnd);
         }
     }
 };
 
-__device__ __forceinline__ uint32_t beyond(uint32_t base, uint32_t off)
-{
-    return off == kRsrcPastEnd ? off : base + off;
-}
+// Until what the wave's LDS reads and loads so far asked for is there.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ bool active(const LayerShape& s, const LayerArgs& a, int t, int k)
 {
     return s.mask_kind == 0 || a.mask[s.mask_kind == 1 ? t : t * s.K + k] != 0;
 }
 
-struct UpLds {
-    float part[kUpWaves * 4 * 2 * kWave * 4];   // sums of [wave][row tile][gate, up][lane]
+// A wave's own notes.
+struct UpNotes {
     uint32_t present[kMaxIds / 32];
     int token[kLayerTokens];
     float weight[kLayerTokens];
+    float scales[2][kMaxChunks];                // of the gate's and the up rows' block
 };
 
 // The expert of slot j (the j-th of those that have tokens, by id), its tokens in ascending order and
 // the sum of the weights with which each chose it.  Lane t holds the ids of token t.
-__device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& a, int j, UpLds& lds)
+__device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& a, int j, UpNotes& notes)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    const int wave = threadIdx.x / kWave;
-    int id[kMaxK];
+    const uint32_t picks = (uint32_t)(s.T * s.K);
+    // all loads at once
+    const __amdgpu_buffer_rsrc_t ir = make_rsrc(a.ids, picks * 4), fr = make_rsrc(a.weights, picks * 4);
+    const __amdgpu_buffer_rsrc_t mr =
+        make_rsrc(a.mask, s.mask_kind == 0 ? 0 : s.mask_kind == 1 ? (uint32_t)s.T : picks);
+    int id[kMaxK], on[kMaxK];
+    float weight[kMaxK];
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
         id[k] = -1;
-        if (k < s.K && lane < s.T) {
-            const int v = a.ids[lane * s.K + k];
-            if (v >= 0 && v < s.E && active(s, a, lane, k)) id[k] = v;
+        on[k] = 1;
+        weight[k] = 0.0f;
+        if (k < s.K) {
+            const uint32_t at = (uint32_t)(lane * s.K + k);     // past the end for lanes without a token
+            id[k] = (int)__builtin_amdgcn_raw_buffer_load_b32(ir, (int)(at * 4), 0, 0);
+            weight[k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(fr, (int)(at * 4), 0, 0));
+            if (s.mask_kind != 0)
+                on[k] = (int)__builtin_amdgcn_raw_buffer_load_b8(
+                    mr, (int)(s.mask_kind == 1 ? (uint32_t)lane : at), 0, 0);
         }
     }
-    if (threadIdx.x < kMaxIds / 32) lds.present[threadIdx.x] = 0;
-    __syncthreads();
-    if (wave == 0) {
+    if (lane < kMaxIds / 32) notes.present[lane] = 0;
 #pragma unroll
-        for (int k = 0; k < kMaxK; ++k)
-            if (id[k] >= 0) atomicOr(&lds.present[id[k] >> 5], 1u << (id[k] & 31));
-    }
-    __syncthreads();
-    const uint32_t word = lane < kMaxIds / 32 ? lds.present[lane] : 0;
+    for (int k = 0; k < kMaxK; ++k)
+        if (k < s.K) {
+            if (lane >= s.T || on[k] == 0 || id[k] < 0 || id[k] >= s.E) id[k] = -1;
+            else atomicOr(&notes.present[id[k] >> 5], 1u << (id[k] & 31));
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const uint32_t word = lane < kMaxIds / 32 ? notes.present[lane] : 0;
     int upto = __popc(word);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -136,161 +211,191 @@ __device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& 
     const int skip = j - (__builtin_amdgcn_readlane(upto, src) - __popc(bits));
     for (int i = 0; i < skip; ++i) bits &= bits - 1;
     slot.expert = src * 32 + __ffs((int)bits) - 1;
-    int before = 0;
     bool has = false;
-    float weight = 0.0f;
+    float total = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kMaxK; ++k) {
-        if (id[k] >= 0 && id[k] < slot.expert) ++before;
-        if (id[k] == slot.expert) {
-            has = true;
-            weight += a.weights[lane * s.K + k];
+    for (int k = 0; k < kMaxK; ++k)
+        if (k < s.K) {
+            slot.first += __popcll((unsigned long long)__ballot(id[k] >= 0 && id[k] < slot.expert));
+            if (id[k] == slot.expert) {
+                has = true;
+                total += weight[k];
+            }
         }
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) before += __shfl_xor(before, off, kWave);
     const uint64_t who = __ballot(has);
-    slot.first = __builtin_amdgcn_readfirstlane(before);
     slot.rows = __popcll((unsigned long long)who);
-    if (has && wave == 0) {
+    if (has) {
         const int at = __popcll((unsigned long long)(who & ((1ull << lane) - 1)));
-        lds.token[at] = lane;
-        lds.weight[at] = weight;
+        notes.token[at] = lane;
+        notes.weight[at] = total;
     }
-    __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     return slot;
 }
 
-template <bool F16, bool BLOCK, int MT, int D>
-__device__ __forceinline__ void up_tile(const LayerShape& s, const LayerArgs& a, const Slot& slot, int n0,
-                                        UpLds& lds)
+// RP: rows of an expert that share a sweep over its weights.
+template <bool F16, bool BLOCK, int RP>
+__global__ __launch_bounds__(kUpWaves * kWave) void up_kernel(LayerShape s, LayerArgs a)
 {
-    typedef Chunk<F16, BLOCK> C;
+    typedef Stage<F16, BLOCK, 2, RP> S;
+    constexpr int kRows = S::kTiles;
+    __shared__ __align__(1024) char ring[kUpWaves][kRing][S::kBytes];
+    __shared__ UpNotes all_notes[kUpWaves];
+    static_assert(kRing * S::kBytes >= kRows * 2 * kWave * 16, "a wave's sums take its ring's place");
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, g = lane >> 4;
+    UpNotes& notes = all_notes[wave];
+    const int j = blockIdx.y;
+    const Slot slot = find_slot(s, a, j, notes);
+    if (blockIdx.x == 0 && wave == 0) {
+        if (lane == 0) a.slots[j] = slot;
+        if (lane < slot.rows) a.tokens[slot.first + lane] = notes.token[lane];
+    }
+    if (slot.expert < 0) return;
+    const int n0 = blockIdx.x * 16;
     const uint32_t row_bytes = (uint32_t)s.H * (BLOCK ? 1 : 2);
     const int chunks = (int)((row_bytes + 127) / 128);
-    const int left = s.F - n0 < kCols ? s.F - n0 : kCols;
+    const int left = s.F - n0 < 16 ? s.F - n0 : 16;
     const char* base = static_cast<const char*>(a.up) + ((size_t)slot.expert * 2 * s.F + n0) * row_bytes;
     const __amdgpu_buffer_rsrc_t wr[2] = {make_rsrc(base, (uint32_t)left * row_bytes),
                                           make_rsrc(base + (size_t)s.F * row_bytes, (uint32_t)left * row_bytes)};
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)s.T * s.H * 2);
-    const int blocks = (s.F + 127) / 128;
-    const float* scales = a.up_scales + ((size_t)slot.expert * 2 * blocks + n0 / 128) * chunks;
-    const uint32_t wrow = (uint32_t)l16 * row_bytes;
-    uint32_t xrow[MT];
+    if (BLOCK) {
+        const int blocks = (s.F + 127) / 128;
+        const float* scales = a.up_scales + ((size_t)slot.expert * 2 * blocks + n0 / 128) * chunks;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = m * 16 + l16;
-        xrow[m] = r < slot.rows ? (uint32_t)lds.token[r] * s.H * 2 : kRsrcPastEnd;
+        for (int t = 0; t < 2; ++t)
+            load_lds4(make_rsrc(scales + (size_t)t * blocks * chunks, (uint32_t)chunks * 4),
+                      reinterpret_cast<char*>(notes.scales[t]), (uint32_t)lane * 4);
     }
-    v4i_t w[D][2][2], x[D][MT][C::kXLoads];
-    float sc[D][2];
-    const auto fetch = [&](int d, int c) {
-        uint32_t wo[2], xo[C::kXLoads];
-        C::offsets(c, g, row_bytes, wo, xo);
+    for (int r0 = 0; r0 < slot.rows; r0 += RP) {
+        uint32_t xoff[S::kXLoads];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) w[d][t][p] = load_chunk(wr[t], beyond(wrow, wo[p]));
-            if (BLOCK) sc[d][t] = scales[(size_t)t * blocks * chunks + (c < chunks ? c : chunks - 1)];
+        for (int i = 0; i < S::kXLoads; ++i) {
+            const int r = r0 + S::xrow(i);
+            xoff[i] = S::xrow(i) < RP && r < slot.rows ? (uint32_t)notes.token[r] * s.H * 2 : kRsrcPastEnd;
         }
+        v4f_t acc[kRows][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < kRows; ++m) acc[m][0] = acc[m][1] = v4f_t{0, 0, 0, 0};
 #pragma unroll
-            for (int p = 0; p < C::kXLoads; ++p)
-                x[d][m][p] = load_chunk(xr, xrow[m] == kRsrcPastEnd ? kRsrcPastEnd : beyond(xrow[m], xo[p]));
-    };
-    v4f_t acc[MT][2];
+        for (int d = 0; d < kRing; ++d) S::fill(ring[wave][d], wr, xr, row_bytes, xoff, wave + d * kUpWaves);
+        for (int c = wave; c < chunks; c += kRing * kUpWaves) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = v4f_t{0, 0, 0, 0};
-#pragma unroll
-    for (int d = 0; d < D; ++d) fetch(d, wave + d * kUpWaves);
-    for (int c = wave; c < chunks; c += D * kUpWaves) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if constexpr (BLOCK) {
-                        const v4f_t sum = C::mma(w[d][t], x[d][m], v4f_t{0, 0, 0, 0});
-                        if (c + d * kUpWaves < chunks) add_scaled(acc[m][t], sum, sc[d][t]);
-                    } else {
-                        acc[m][t] = C::mma(w[d][t], x[d][m], acc[m][t]);
-                    }
+            for (int d = 0; d < kRing; ++d) {
+                const int now = c + d * kUpWaves;
+                typename S::Regs r;
+                wait_loads<(kRing - 1) * S::kLoads>();
+                S::read(ring[wave][d], r);
+                float sc[2];
+                if (BLOCK) {
+                    sc[0] = notes.scales[0][now & (kMaxChunks - 1)];
+                    sc[1] = notes.scales[1][now & (kMaxChunks - 1)];
                 }
-            fetch(d, c + (d + D) * kUpWaves);
+                wait_lds();
+                S::fill(ring[wave][d], wr, xr, row_bytes, xoff, now + kRing * kUpWaves);
+#pragma unroll
+                for (int m = 0; m < kRows; ++m)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if constexpr (BLOCK) {
+                            const v4f_t sum = S::mma(r.w[t], r.x[m], v4f_t{0, 0, 0, 0});
+                            if (now < chunks) add_scaled(acc[m][t], sum, sc[t]);
+                        } else {
+                            acc[m][t] = S::mma(r.w[t], r.x[m], acc[m][t]);
+                        }
+                    }
+            }
         }
-    }
-    v4f_t* part = reinterpret_cast<v4f_t*>(lds.part);
+        wait_loads<0>();                        // nothing lands in LDS any more
+        v4f_t* mine = reinterpret_cast<v4f_t*>(ring[wave][0]);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < kRows; ++m)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) part[((wave * MT + m) * 2 + t) * kWave + lane] = acc[m][t];
-    __syncthreads();
-    // one row tile a wave
-    for (int m = wave; m < MT; m += kUpWaves) {
-        float r[2][4];
+            for (int t = 0; t < 2; ++t) mine[(m * 2 + t) * kWave + lane] = acc[m][t];
+        __syncthreads();
+        // one row tile a wave
+        for (int m = wave; m < kRows; m += kUpWaves) {
+            float r[2][4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            v4f_t v = part[(m * 2 + t) * kWave + lane];
+            for (int t = 0; t < 2; ++t) {
+                v4f_t v = reinterpret_cast<const v4f_t*>(ring[0][0])[(m * 2 + t) * kWave + lane];
 #pragma unroll
-            for (int o = 1; o < kUpWaves; ++o) v += part[((o * MT + m) * 2 + t) * kWave + lane];
+                for (int o = 1; o < kUpWaves; ++o)
+                    v += reinterpret_cast<const v4f_t*>(ring[o][0])[(m * 2 + t) * kWave + lane];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r[t][q] = v[q];
+                for (int q = 0; q < 4; ++q) r[t][q] = v[q];
+            }
+            const int row = r0 + m * 16 + l16;
+            if (m * 16 + l16 >= RP || row >= slot.rows) continue;
+            silu_mul4(r[0], r[1], r[0]);
+            const float weight = notes.weight[row];
+            uint16_t* o = static_cast<uint16_t*>(a.h) + (size_t)(slot.first + row) * s.F + n0 + g * 4;
+            if (g * 4 < left)                   // F is a multiple of 8
+                *reinterpret_cast<uint2*>(o) = make_uint2(pack_out2(r[0][0] * weight, r[0][1] * weight, F16),
+                                                          pack_out2(r[0][2] * weight, r[0][3] * weight, F16));
         }
-        const int row = m * 16 + l16;
-        if (row >= slot.rows) continue;
-        silu_mul4(r[0], r[1], r[0]);
-        const float weight = lds.weight[row];
-        uint16_t* o = static_cast<uint16_t*>(a.h) + (size_t)(slot.first + row) * s.F + n0 + g * 4;
-        if (g * 4 < left)                       // F is a multiple of 8
-            *reinterpret_cast<uint2*>(o) = make_uint2(pack_out2(r[0][0] * weight, r[0][1] * weight, F16),
-                                                      pack_out2(r[0][2] * weight, r[0][3] * weight, F16));
+        if (r0 + RP < slot.rows) __syncthreads();            // before the rings are filled again
     }
 }
 
-template <bool F16, bool BLOCK>
-__global__ __launch_bounds__(kUpWaves * kWave) void up_kernel(LayerShape s, LayerArgs a)
+// Dynamic LDS of down_kernel after its rings: sums [wave][token][column], the slots cut to RP rows,
+// the rows' tokens, scales [wave][2][64 units].
+struct DownLds {
+    size_t ring, sums, slots, tokens, scales;
+};
+__host__ __device__ inline DownLds down_lds(const LayerShape& s, int waves, int stage, int cols, int rp)
 {
-    __shared__ UpLds lds;
-    const int j = blockIdx.y;
-    const Slot slot = find_slot(s, a, j, lds);
-    if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) a.slots[j] = slot;
-        if ((int)threadIdx.x < slot.rows) a.tokens[slot.first + threadIdx.x] = lds.token[threadIdx.x];
-    }
-    if (slot.expert < 0) return;
-    const int n0 = blockIdx.x * kCols;
-    if (slot.rows <= 16) up_tile<F16, BLOCK, 1, 4>(s, a, slot, n0, lds);
-    else if (slot.rows <= 32) up_tile<F16, BLOCK, 2, 2>(s, a, slot, n0, lds);
-    else up_tile<F16, BLOCK, 4, 2>(s, a, slot, n0, lds);
+    DownLds l;
+    l.ring = (size_t)waves * kRing * stage;
+    l.sums = (size_t)waves * s.T * cols * 4;
+    l.slots = ((size_t)s.slots + (s.T > rp ? s.T * s.K / rp : 0)) * sizeof(Slot);
+    l.tokens = (size_t)s.T * s.K * 4;
+    l.scales = s.block ? (size_t)waves * 2 * kWave * 4 : 0;
+    return l;
 }
 
-// MT: tiles of 16 rows an expert can have.  LDS: sums [wave][token][column], the slots, the rows'
-// tokens.
-template <bool F16, bool BLOCK, int MT, int D>
-__global__ __launch_bounds__(kDownWaves * kWave) void down_kernel(LayerShape s, LayerArgs a)
+template <bool F16, bool BLOCK, int NT, int RP, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, LayerArgs a)
 {
-    typedef Chunk<F16, BLOCK> C;
-    extern __shared__ float sums[];
+    typedef Stage<F16, BLOCK, NT, RP> S;
+    constexpr int kCols = NT * 16;
+    constexpr int kThreads = WAVES * kWave;
+    extern __shared__ __align__(1024) char lds[];
     __shared__ int count_lds;
-    Slot* slots = reinterpret_cast<Slot*>(sums + kDownWaves * s.T * kCols);
-    int* tokens = reinterpret_cast<int*>(slots + s.slots);
+    const DownLds parts = down_lds(s, WAVES, S::kBytes, kCols, RP);
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, g = lane >> 4;
-    if (threadIdx.x == 0) count_lds = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < s.slots; i += kDownWaves * kWave) {
-        slots[i] = a.slots[i];
-        if (slots[i].expert >= 0) atomicMax(&count_lds, i + 1);
+    char* ring = lds + (size_t)wave * kRing * S::kBytes;
+    float* sums = reinterpret_cast<float*>(lds + parts.ring);
+    Slot* slots = reinterpret_cast<Slot*>(lds + parts.ring + parts.sums);
+    int* tokens = reinterpret_cast<int*>(lds + parts.ring + parts.sums + parts.slots);
+    float* scales = reinterpret_cast<float*>(lds + parts.ring + parts.sums + parts.slots + parts.tokens) +
+                    wave * 2 * kWave;
+    // The first wave cuts the slots to at most RP rows each.
+    if (wave == 0) {
+        int count = 0;
+        for (int i0 = 0; i0 < s.slots; i0 += kWave) {
+            Slot slot = {-1, 0, 0, 0};
+            if (i0 + lane < s.slots) slot = a.slots[i0 + lane];
+            const int pieces = slot.expert < 0 ? 0 : (slot.rows + RP - 1) / RP;
+            int upto = pieces;
+#pragma unroll
+            for (int off = 1; off < kWave; off <<= 1) {
+                const int o = __shfl_up(upto, off, kWave);
+                if (lane >= off) upto += o;
+            }
+            for (int p = 0; p < pieces; ++p)
+                slots[count + upto - pieces + p] = {slot.expert, slot.first + p * RP,
+                                                    slot.rows - p * RP < RP ? slot.rows - p * RP : RP, 0};
+            count += __builtin_amdgcn_readlane(upto, kWave - 1);
+        }
+        if (lane == 0) count_lds = count;
     }
-    for (int i = threadIdx.x; i < s.T * s.K; i += kDownWaves * kWave)
-        tokens[i] = a.tokens[i];
-    for (int i = threadIdx.x; i < kDownWaves * s.T * kCols; i += kDownWaves * kWave) sums[i] = 0.0f;
+    for (int i = threadIdx.x; i < s.T * s.K; i += kThreads) tokens[i] = a.tokens[i];
+    for (int i = threadIdx.x; i < WAVES * s.T * kCols; i += kThreads) sums[i] = 0.0f;
     __syncthreads();
     const int count = __builtin_amdgcn_readfirstlane(count_lds);
     const char* h = static_cast<const char*>(a.h);
@@ -298,14 +403,12 @@ __global__ __launch_bounds__(kDownWaves * kWave) void down_kernel(LayerShape s, 
     const uint32_t h_bytes = (uint32_t)s.F * 2;
     const int chunks = (int)((row_bytes + 127) / 128);
     const int n0 = blockIdx.x * kCols;
-    const int left = s.H - n0 < kCols ? s.H - n0 : kCols;
     const int blocks = (s.H + 127) / 128;
-    const uint32_t wrow = (uint32_t)l16 * row_bytes;
 
-    // Units (slot, chunk) go round the waves.
+    // Units (slot, chunk) go round the waves: unit i of a wave is number wave + WAVES * i.
     struct Place { int slot, chunk; };
     const auto step = [&](Place p) {
-        p.chunk += kDownWaves;
+        p.chunk += WAVES;
         while (p.chunk >= chunks) {
             p.chunk -= chunks;
             ++p.slot;
@@ -319,109 +422,152 @@ __global__ __launch_bounds__(kDownWaves * kWave) void down_kernel(LayerShape s, 
         r.rows = __builtin_amdgcn_readfirstlane(slots[i].rows);
         return r;
     };
-    v4i_t w[D][2], x[D][MT][C::kXLoads];
-    float sc[D];
-    Place ahead = {0, wave - kDownWaves};
-    ahead = step(ahead);
+    Place ahead = step(Place{0, wave - WAVES});
     Slot next = {0, 0, 0, 0};
     int held = -1;                              // the slot that `next` describes
-    const auto fetch = [&](int d) {
+    const auto fill = [&](int d) {
         const bool there = ahead.slot < count;
         if (there && held != ahead.slot) {
             next = slot_at(ahead.slot);
             held = ahead.slot;
         }
-        const __amdgpu_buffer_rsrc_t wr = make_rsrc(
-            static_cast<const char*>(a.down) + ((size_t)next.expert * s.H + n0) * row_bytes,
-            there ? (uint32_t)left * row_bytes : 0);
+        __amdgpu_buffer_rsrc_t wr[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int left = s.H - n0 - t * 16 < 16 ? s.H - n0 - t * 16 : 16;
+            wr[t] = make_rsrc(static_cast<const char*>(a.down) +
+                                  ((size_t)next.expert * s.H + n0 + t * 16) * row_bytes,
+                              there && left > 0 ? (uint32_t)left * row_bytes : 0);
+        }
         const __amdgpu_buffer_rsrc_t hr =
             make_rsrc(h + (size_t)next.first * h_bytes, there ? (uint32_t)next.rows * h_bytes : 0);
-        uint32_t wo[2], xo[C::kXLoads];
-        C::offsets(ahead.chunk, g, row_bytes, wo, xo);
+        uint32_t xoff[S::kXLoads];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) w[d][p] = load_chunk(wr, beyond(wrow, wo[p]));
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int p = 0; p < C::kXLoads; ++p)
-                x[d][m][p] = load_chunk(hr, beyond((uint32_t)(m * 16 + l16) * h_bytes, xo[p]));
-        if (BLOCK) sc[d] = a.down_scales[((size_t)next.expert * blocks + n0 / 128) * chunks + ahead.chunk];
+        for (int i = 0; i < S::kXLoads; ++i)
+            xoff[i] = S::xrow(i) < RP ? (uint32_t)S::xrow(i) * h_bytes : kRsrcPastEnd;
+        S::fill(ring + d * S::kBytes, wr, hr, row_bytes, xoff, ahead.chunk);
         ahead = step(ahead);
     };
-    v4f_t acc[MT];
+    // The scales of units 64 * batch + 0..63 of the wave, a lane each.
+    const auto fetch_scales = [&](int batch) {
+        const int unit = wave + WAVES * (batch * kWave + lane);
+        const int i = unit / chunks;
+        const uint32_t off = i < count ? (uint32_t)(((size_t)slots[i].expert * blocks + n0 / 128) * chunks +
+                                                    (unit - i * chunks)) * 4
+                                       : kRsrcPastEnd;
+        load_lds4(make_rsrc(a.down_scales, (uint32_t)s.E * blocks * chunks * 4),
+                  reinterpret_cast<char*>(scales + (batch & 1) * kWave), off);
+    };
+    if (BLOCK) fetch_scales(0);
+    v4f_t acc[S::kTiles][NT];
+    const auto clear = [&]() {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = v4f_t{0, 0, 0, 0};
+        for (int m = 0; m < S::kTiles; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[m][t] = v4f_t{0, 0, 0, 0};
+    };
+    clear();
     float* mine = sums + wave * s.T * kCols;
     // Adds an expert's sums to those of its tokens.
     const auto flush = [&](int i) {
         const Slot slot = slot_at(i);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < S::kTiles; ++m) {
             const int row = m * 16 + l16;
-            if (row < slot.rows) {
-                v4f_t* to = reinterpret_cast<v4f_t*>(mine + tokens[slot.first + row] * kCols + g * 4);
-                *to = *to + acc[m];
-            }
-            acc[m] = v4f_t{0, 0, 0, 0};
-        }
-    };
-    Place now = {0, wave - kDownWaves};
-    now = step(now);
-    int open = now.slot;
+            if (row < slot.rows)
 #pragma unroll
-    for (int d = 0; d < D; ++d) fetch(d);
+                for (int t = 0; t < NT; ++t) {
+                    v4f_t* to = reinterpret_cast<v4f_t*>(mine + tokens[slot.first + row] * kCols + t * 16 + g * 4);
+                    *to = *to + acc[m][t];
+                }
+        }
+        clear();
+    };
+    Place now = step(Place{0, wave - WAVES});
+    int open = now.slot, unit = 0;
+#pragma unroll
+    for (int d = 0; d < kRing; ++d) fill(d);
     while (now.slot < count) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
+        for (int d = 0; d < kRing; ++d) {
+            typename S::Regs r;
+            wait_loads<(kRing - 1) * S::kLoads>();
+            S::read(ring + d * S::kBytes, r);
+            float sc = 0.0f;
+            if (BLOCK) sc = scales[unit & (2 * kWave - 1)];
+            wait_lds();
+            if (BLOCK && (unit & (kWave - 1)) == 0) fetch_scales(unit / kWave + 1);
+            fill(d);
             if (now.slot < count) {
                 if (now.slot != open) {
                     flush(open);
                     open = now.slot;
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if constexpr (BLOCK) add_scaled(acc[m], C::mma(w[d], x[d][m], v4f_t{0, 0, 0, 0}), sc[d]);
-                    else acc[m] = C::mma(w[d], x[d][m], acc[m]);
-                }
+                for (int m = 0; m < S::kTiles; ++m)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if constexpr (BLOCK)
+                            add_scaled(acc[m][t], S::mma(r.w[t], r.x[m], v4f_t{0, 0, 0, 0}), sc);
+                        else
+                            acc[m][t] = S::mma(r.w[t], r.x[m], acc[m][t]);
+                    }
             }
             now = step(now);
-            fetch(d);
+            ++unit;
         }
     }
+    wait_loads<0>();                            // nothing lands in LDS any more
     if (open < count) flush(open);
     __syncthreads();
-    const bool f16 = F16;
-    for (int i = threadIdx.x; i < s.T * kCols; i += kDownWaves * kWave) {
-        const int t = i / kCols, n = i % kCols;
-        if (n >= left) continue;
+    for (int i = threadIdx.x; i < s.T * kCols; i += kThreads) {
+        const int t = i / kCols, n = n0 + i % kCols;
+        if (n >= s.H) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int o = 0; o < kDownWaves; ++o) v += sums[o * s.T * kCols + i];
-        const size_t at = (size_t)t * s.H + n0 + n;
+        for (int o = 0; o < WAVES; ++o) v += sums[o * s.T * kCols + i];
+        const size_t at = (size_t)t * s.H + n;
         if (s.id_end > s.zero_end)
             for (int k = 0; k < s.K; ++k) {
                 const int id = a.ids[t * s.K + k];
                 if (id >= s.zero_end && id < s.id_end && active(s, a, t, k))
-                    v += a.weights[t * s.K + k] * tok_lo_rt(static_cast<const uint16_t*>(a.x)[at], f16);
+                    v += a.weights[t * s.K + k] * tok_lo_rt(static_cast<const uint16_t*>(a.x)[at], F16);
             }
-        if (a.shared) v += tok_lo_rt(static_cast<const uint16_t*>(a.shared)[at], f16);
-        static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_tok_rt(v, f16);
+        if (a.shared) v += tok_lo_rt(static_cast<const uint16_t*>(a.shared)[at], F16);
+        static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_tok_rt(v, F16);
     }
+}
+
+template <bool F16, bool BLOCK, int NT, int RP, int WAVES>
+hipError_t launch_down(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
+{
+    const DownLds l = down_lds(s, WAVES, Stage<F16, BLOCK, NT, RP>::kBytes, NT * 16, RP);
+    const size_t bytes = l.ring + l.sums + l.slots + l.tokens + l.scales;
+    down_kernel<F16, BLOCK, NT, RP, WAVES><<<(unsigned)((s.H + NT * 16 - 1) / (NT * 16)), WAVES * kWave, bytes,
+                                             stream>>>(s, a);
+    return hipGetLastError();
+}
+
+template <bool F16, bool BLOCK, int RP>
+hipError_t launch_rows(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
+{
+    up_kernel<F16, BLOCK, RP><<<dim3((unsigned)((s.F + 15) / 16), (unsigned)s.slots), kUpWaves * kWave, 0,
+                                stream>>>(s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (s.H >= kWideDown) return launch_down<F16, BLOCK, 2, RP, 4>(s, a, stream);
+    // (eight rings of 32 rows with codes do not fit the 160 KB of LDS)
+    return launch_down<F16, BLOCK, 1, RP, BLOCK && RP == 32 ? 4 : 8>(s, a, stream);
 }
 
 template <bool F16, bool BLOCK>
 hipError_t launch(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
 {
-    up_kernel<F16, BLOCK><<<dim3((unsigned)((s.F + kCols - 1) / kCols), (unsigned)s.slots), kUpWaves * kWave, 0,
-                            stream>>>(s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((s.H + kCols - 1) / kCols));
-    const size_t lds = (size_t)kDownWaves * s.T * kCols * 4 + s.slots * sizeof(Slot) + (size_t)s.T * s.K * 4;
-    if (s.T <= 16) down_kernel<F16, BLOCK, 1, 4><<<grid, kDownWaves * kWave, lds, stream>>>(s, a);
-    else if (s.T <= 32) down_kernel<F16, BLOCK, 2, 4><<<grid, kDownWaves * kWave, lds, stream>>>(s, a);
-    else down_kernel<F16, BLOCK, 4, 2><<<grid, kDownWaves * kWave, lds, stream>>>(s, a);
-    return hipGetLastError();
+    // An expert's rows beyond RP read its weights again.
+    constexpr int kFew = BLOCK ? 4 : 8;         // rows that one load brings a chunk of
+    if (s.T <= kFew || s.T * s.K <= 2 * s.E) return launch_rows<F16, BLOCK, kFew>(s, a, stream);
+    if (s.T <= 16 || s.T * s.K <= 8 * s.E) return launch_rows<F16, BLOCK, 16>(s, a, stream);
+    return launch_rows<F16, BLOCK, 32>(s, a, stream);
 }
 
 }  // namespace

@@ -118,6 +118,14 @@ def test_masks_special_experts_and_shared_rows(W, BS, mask_kind, block):
     assert (y == 0).all() and not torch.signbit(y).any()
 
 
+@pytest.mark.parametrize("block", [False, True])
+@pytest.mark.parametrize("H", [1024, 6144])
+@pytest.mark.parametrize("E,K", [(1024, 16), (512, 2), (128, 16), (64, 16)])
+def test_the_most_tokens(E, K, H, block):
+    """64 tokens, with every number of rows that shares a sweep and the largest tables."""
+    Case(2, 32, E, K, H, 16, block, seed=E).check_exact()
+
+
 def test_ids_out_of_range_count_as_inactive():
     c = Case(2, 3, 8, 4, 1024, 64, seed=3)
     c.ids[0, 1] = torch.tensor([-1, 8, 2 ** 31 - 1, -2 ** 31], device=DEV)
