@@ -317,6 +317,18 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     constexpr int kXGroups = kGroups > 1 ? kGroups / 2 : 1;
     constexpr int kWFirst = kGroups > 1 ? kGroups / 2 : 0, kWGroups = kGroups - kWFirst;
     constexpr int kReadW = kWFirst >= 2 ? kWFirst - 2 : 0;
+    // Block: the sums of a group's tiles wait here with their scales until the next group's products
+    // (perhaps the next step's) take their place, so that no product is waited for.
+    v4f_t late[2][2] = {{{0, 0, 0, 0}, {0, 0, 0, 0}}, {{0, 0, 0, 0}, {0, 0, 0, 0}}};
+    float late_scale[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+    const auto settle = [&](int group, int i, int t) {
+        if constexpr (M::kBlk)
+            if (group * 2 + i < MT) add_scaled(acc[group * 2 + i][t], late[i][t], late_scale[i][t]);
+    };
+    const auto settle_all = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) settle(kGroups - 1, i >> 1, i & 1);
+    };
     // phase: step modulo the unrolling
     const auto one = [&](int phase, int step, Where where) {
         const int par = phase & 1;
@@ -353,19 +365,33 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
             for (int i = 0; i < 4; ++i)
                 if (kWFirst + i * kWGroups / 4 == q) fetch_w(step + 3, i);
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (M::kBlk) {
 #pragma unroll
-            for (int i = 0; i < 2 && q * 2 + i < MT; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if constexpr (M::kBlk)
-                        add_scaled(acc[q * 2 + i][t], M::mma(w[par][t], x[q & 1][i], Acc{0, 0, 0, 0}, 0, 0),
-                                   __int_as_float(wsc[par][t]) * __int_as_float(xsv[q & 1][i]));
-                    else
+                    for (int t = 0; t < 2; ++t) {
+                        if (q > 0 || where == kFull) settle(q > 0 ? q - 1 : kGroups - 1, i, t);
+                        if (q * 2 + i >= MT) continue;
+                        late[i][t] = M::mma(w[par][t], x[q & 1][i], Acc{0, 0, 0, 0}, 0, 0);
+                        late_scale[i][t] = __int_as_float(wsc[par][t]) * __int_as_float(xsv[q & 1][i]);
+                    }
+                // in turn: the additions that free a tile's place, its product
+#pragma unroll
+                for (int i = 0; i < 4 && q * 2 + i / 2 < MT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 && q * 2 + i < MT; ++i)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
                         acc[q * 2 + i][t] = M::mma(w[par][t], x[q & 1][i], acc[q * 2 + i][t], wsc[par][t],
                                                    xsv[q & 1][i]);
-                }
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (where == kAfterLoop) settle_all();
     };
     constexpr int kUnroll = kLdsScales ? 4 : 2;
     int step = 0;
@@ -373,6 +399,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 #pragma unroll
         for (int r = 0; r < kUnroll; ++r) one(r, step + r, kFull);
     }
+    if (step > 0) settle_all();
 #pragma unroll
     for (int r = 0; r < kUnroll - 1; ++r)
         if (step + r < steps) one(r, step + r, kAfterLoop);
