@@ -312,8 +312,9 @@ class Launch:
         if torch.cuda.current_device() != self._index:
             _launch(self._fn, self._args, self._dev, stream)
             return
-        s = torch.cuda.current_stream(self._dev) if stream is None else stream
-        status = self._fn(*self._args, ctypes.c_void_p(s.cuda_stream))
+        # (the stream's handle alone: building a torch.cuda.Stream costs 1.8 us of a 6 us call)
+        s = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
+        status = self._fn(*self._args, ctypes.c_void_p(s))
         if status != MOE_OK:
             _check(status)
 

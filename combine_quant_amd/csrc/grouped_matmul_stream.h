@@ -164,7 +164,7 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
 }
 
 template <int TYPE>
-__global__ __launch_bounds__(kStreamWaves * kWave) void stream_kernel(MatmulShape s, MatmulArgs a)
+__global__ __launch_bounds__(kStreamWaves * kWave, 2) void stream_kernel(MatmulShape s, MatmulArgs a)
 {
     constexpr int NT = 2, MT = 4, D = 2;
     __shared__ float lds[kStreamWaves * MT * NT * kWave * 4];

@@ -9,6 +9,8 @@
 #include "dc_quantize.h"
 #include "norm_internal.h"
 
+#include <type_traits>
+
 namespace moe_dc {
 namespace {
 
@@ -38,22 +40,40 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8], bool f16)
                             pack_bf16x2(f[6], f[7]));
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+// The sum of a row of 16 lanes, in every lane of the row.
+__device__ __forceinline__ float row_sum(float v)
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+    const auto moved = [&](auto pattern) {
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(pattern)::value, 0xF, 0xF, false));
+    };
+    v += moved(std::integral_constant<int, kDppQuadXor1>());
+    v += moved(std::integral_constant<int, kDppQuadXor2>());
+    v += moved(std::integral_constant<int, kDppRowHalfMirror>());
+    v += moved(std::integral_constant<int, kDppRowMirror>());
     return v;
 }
 
-// Sum over the workgroup; `scratch` holds one float per wave.
+// The workgroup's sum, or largest value, in every thread: up to 64 rows of 16 lanes meet in
+// `scratch` (64 words, those of rows that are not there cleared by the first wave).
 __device__ __forceinline__ float block_sum(float v, float* scratch)
 {
-    v = wave_sum(v);
-    if ((threadIdx.x & (kWave - 1)) == 0) scratch[threadIdx.x / kWave] = v;
+    const int lane = threadIdx.x & (kWave - 1);
+    v = row_sum(v);
+    if ((lane & 15) == 0) scratch[threadIdx.x / 16] = v;
+    if (threadIdx.x < kWave && threadIdx.x >= blockDim.x / 16) scratch[threadIdx.x] = 0.0f;
     __syncthreads();
-    float r = 0.0f;
-    for (int w = 0; w < (int)(blockDim.x / kWave); ++w) r += scratch[w];
-    return r;
+    v = row_sum(scratch[lane]);
+    v += __shfl_xor(v, 16, kWave);
+    return v + __shfl_xor(v, 32, kWave);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* scratch)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    v = group_max_u32<16>(v);
+    if ((lane & 15) == 0) scratch[threadIdx.x / 16] = v;
+    if (threadIdx.x < kWave && threadIdx.x >= blockDim.x / 16) scratch[threadIdx.x] = 0;
+    __syncthreads();
+    return group_max_u32<64>(scratch[lane]);
 }
 
 __device__ __forceinline__ float reciprocal_rms(const NormShape& s, float squares)
@@ -83,8 +103,8 @@ __device__ __forceinline__ void store_mx_scale(const NormShape& s, void* scales,
 template <int MODE, int CT, int SLOTS>
 __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
 {
-    __shared__ float sums[16];
-    __shared__ uint32_t peaks[16];
+    __shared__ float sums[kWave];
+    __shared__ uint32_t peaks[kWave];
     const size_t token = blockIdx.x;
     const uint32_t row = (uint32_t)s.H * 2;
     const bool f16 = s.tok_f16;
@@ -149,7 +169,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
         uint32_t peak = most[0];
 #pragma unroll
         for (int n = 1; n < SLOTS; ++n) peak = dpp_max(peak, most[n]);
-        peak = block_max_u32(peak, peaks);
+        peak = block_max(peak, peaks);
         float dyn, scale;
         group_dyn<CT>(peak, dyn, scale);
 #pragma unroll
@@ -191,8 +211,8 @@ template <int MODE, int CT>
 __global__ __launch_bounds__(kAnyThreads) void norm_any_kernel(NormShape s, NormArgs a)
 {
     __shared__ float y[8192];
-    __shared__ float sums[kAnyThreads / kWave];
-    __shared__ uint32_t peaks[kAnyThreads / kWave];
+    __shared__ float sums[kWave];
+    __shared__ uint32_t peaks[kWave];
     const size_t token = blockIdx.x, base = token * s.H;
     const bool f16 = s.tok_f16;
     const auto value = [&](const void* p, size_t i) { return tok_lo_rt(static_cast<const uint16_t*>(p)[i], f16); };
@@ -221,7 +241,7 @@ __global__ __launch_bounds__(kAnyThreads) void norm_any_kernel(NormShape s, Norm
         codes[i] = CT == kCodeInt8 ? (uint8_t)int8_code(p) : p != p ? (uint8_t)0 : (uint8_t)fp8_code<CT>(p);
     };
     if (MODE == 2) {
-        peak = block_max_u32(peak, peaks);
+        peak = block_max(peak, peaks);
         float dyn, scale;
         group_dyn<CT>(peak, dyn, scale);
         for (int i = threadIdx.x; i < s.H; i += kAnyThreads) code(i, dyn);
