@@ -22,10 +22,12 @@ namespace moe_dc {
 namespace {
 
 constexpr int kRing = 2;                        // stages of a wave
-// Many small workgroups hide each other's start and end.  Two waves with two stages against four
-// with two and four with three, us: 1 token on 8 experts of 7168 x 2048 bf16 127, 131, 133; 32 tokens
-// on 256 experts E4M3 1214, 1224, 1276, on 64 experts 471, 545, 621.
-constexpr int kUpWaves = 2;
+// Many small workgroups hide each other's start and end, so the up kernel's have two waves; with few
+// columns in all, four waves share the chunks of a workgroup's.  Two waves with two stages against
+// four with two and four with three, us: 1 token on 8 experts of 7168 x 2048 bf16 127, 131, 133; 32
+// tokens on 256 experts E4M3 1214, 1224, 1276, on 64 experts 471, 545, 621; 5 tokens on 8 experts of
+// 1024 x 520 fp16 with two and four waves 13.8 and 12.7.
+constexpr int64_t kFewUp = 16 * 512;            // columns (of all experts) up to which it has four
 // Columns of y and waves of a workgroup: many columns share the rows of h, but few workgroups leave
 // CUs idle.  32 columns and four waves against 16 and eight, us: H = 7168, 32 tokens on 64 experts
 // E4M3 471 and 501, 64 tokens 492 and 529; H = 2048, 16 tokens on 32 experts x 1408 bf16 132 and 108,
@@ -156,53 +158,71 @@ __device__ __forceinline__ bool active(const LayerShape& s, const LayerArgs& a, 
 
 // A wave's own notes.
 struct UpNotes {
-    uint32_t present[kMaxIds / 32];
-    int token[kLayerTokens];
+    uint32_t present[kMaxIds / 32];             // experts with tokens
+    uint32_t who[kLayerTokens / 32];            // tokens of the wave's expert
+    int token[kLayerTokens];                    // the same in ascending order
     float weight[kLayerTokens];
     float scales[2][kMaxChunks];                // of the gate's and the up rows' block
 };
 
-// The expert of slot j (the j-th of those that have tokens, by id), its tokens in ascending order and
-// the sum of the weights with which each chose it.  Lane t holds the ids of token t.
-__device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& a, int j, UpNotes& notes)
+// Inclusive sums over the first 32 lanes (the others' values do not matter).
+__device__ __forceinline__ int scan32(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    const int low = __builtin_amdgcn_readlane(v, 15);
+    return (threadIdx.x & (kWave - 1)) >= 16 ? v + low : v;
+}
+
+// The expert of slot j (the j-th of those that have tokens, by id) and its tokens in ascending order.
+// A lane holds every 64th pick.  The picks' ids (-1: inactive) and weights are left in LDS; all waves
+// of a workgroup write the same there, and each reads what it wrote.
+__device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& a, int j, UpNotes& notes,
+                                          int* ids, float* weights)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    const uint32_t picks = (uint32_t)(s.T * s.K);
-    // all loads at once
-    const __amdgpu_buffer_rsrc_t ir = make_rsrc(a.ids, picks * 4), fr = make_rsrc(a.weights, picks * 4);
+    const int picks = s.T * s.K;
+    constexpr int kPasses = kLayerTokens * kMaxK / kWave;
+    const uint32_t magic = 65536u / (uint32_t)s.K + 1;       // p / K for p < 1024
+    const auto token_of = [&](int p) { return (int)((uint32_t)p * magic >> 16); };
+    const __amdgpu_buffer_rsrc_t ir = make_rsrc(a.ids, (uint32_t)picks * 4);
+    const __amdgpu_buffer_rsrc_t fr = make_rsrc(a.weights, (uint32_t)picks * 4);
     const __amdgpu_buffer_rsrc_t mr =
-        make_rsrc(a.mask, s.mask_kind == 0 ? 0 : s.mask_kind == 1 ? (uint32_t)s.T : picks);
-    int id[kMaxK], on[kMaxK];
-    float weight[kMaxK];
+        make_rsrc(a.mask, s.mask_kind == 0 ? 0 : s.mask_kind == 1 ? (uint32_t)s.T : (uint32_t)picks);
+    int id[kPasses], on[kPasses];
+    float weight[kPasses];
+    // all loads at once
 #pragma unroll
-    for (int k = 0; k < kMaxK; ++k) {
-        id[k] = -1;
-        on[k] = 1;
-        weight[k] = 0.0f;
-        if (k < s.K) {
-            const uint32_t at = (uint32_t)(lane * s.K + k);     // past the end for lanes without a token
-            id[k] = (int)__builtin_amdgcn_raw_buffer_load_b32(ir, (int)(at * 4), 0, 0);
-            weight[k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(fr, (int)(at * 4), 0, 0));
+    for (int i = 0; i < kPasses; ++i) {
+        const int p = i * kWave + lane;
+        id[i] = -1;
+        on[i] = 1;
+        weight[i] = 0.0f;
+        if (i * kWave < picks) {
+            id[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(ir, p * 4, 0, 0);
+            weight[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(fr, p * 4, 0, 0));
             if (s.mask_kind != 0)
-                on[k] = (int)__builtin_amdgcn_raw_buffer_load_b8(
-                    mr, (int)(s.mask_kind == 1 ? (uint32_t)lane : at), 0, 0);
+                on[i] = (int)__builtin_amdgcn_raw_buffer_load_b8(mr, s.mask_kind == 1 ? token_of(p) : p, 0, 0);
         }
     }
     if (lane < kMaxIds / 32) notes.present[lane] = 0;
+    if (lane < kLayerTokens / 32) notes.who[lane] = 0;
 #pragma unroll
-    for (int k = 0; k < kMaxK; ++k)
-        if (k < s.K) {
-            if (lane >= s.T || on[k] == 0 || id[k] < 0 || id[k] >= s.E) id[k] = -1;
-            else atomicOr(&notes.present[id[k] >> 5], 1u << (id[k] & 31));
+    for (int i = 0; i < kPasses; ++i)
+        if (i * kWave < picks) {
+            const int p = i * kWave + lane;
+            if (p >= picks || on[i] == 0 || id[i] < 0 || id[i] >= s.E) id[i] = -1;
+            else atomicOr(&notes.present[id[i] >> 5], 1u << (id[i] & 31));
+            if (p < picks) {
+                ids[p] = id[i];
+                weights[p] = weight[i];
+            }
         }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const uint32_t word = lane < kMaxIds / 32 ? notes.present[lane] : 0;
-    int upto = __popc(word);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up(upto, off, kWave);
-        if (lane >= off) upto += o;
-    }
+    const int upto = scan32(__popc(word));
     const uint64_t holds = __ballot(lane < kMaxIds / 32 && upto > j && upto - __popc(word) <= j);
     Slot slot = {-1, 0, 0, 0};
     if (holds == 0) return slot;
@@ -211,43 +231,55 @@ __device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& 
     const int skip = j - (__builtin_amdgcn_readlane(upto, src) - __popc(bits));
     for (int i = 0; i < skip; ++i) bits &= bits - 1;
     slot.expert = src * 32 + __ffs((int)bits) - 1;
-    bool has = false;
-    float total = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kMaxK; ++k)
-        if (k < s.K) {
-            slot.first += __popcll((unsigned long long)__ballot(id[k] >= 0 && id[k] < slot.expert));
-            if (id[k] == slot.expert) {
-                has = true;
-                total += weight[k];
+    for (int i = 0; i < kPasses; ++i)
+        if (i * kWave < picks) {
+            slot.first += __popcll((unsigned long long)__ballot(id[i] >= 0 && id[i] < slot.expert));
+            if (id[i] == slot.expert) {
+                const int t = token_of(i * kWave + lane);
+                atomicOr(&notes.who[t >> 5], 1u << (t & 31));
             }
         }
-    const uint64_t who = __ballot(has);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const uint64_t who = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)notes.who[0]) |
+                         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)notes.who[1]) << 32;
     slot.rows = __popcll((unsigned long long)who);
-    if (has) {
-        const int at = __popcll((unsigned long long)(who & ((1ull << lane) - 1)));
-        notes.token[at] = lane;
-        notes.weight[at] = total;
-    }
+    if (who >> lane & 1) notes.token[__popcll((unsigned long long)(who & ((1ull << lane) - 1)))] = lane;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     return slot;
 }
 
+// The sum, in the picks' order, of the weights with which each of the slot's tokens chose its expert.
+__device__ __forceinline__ void sum_weights(const LayerShape& s, const Slot& slot, const int* ids,
+                                            const float* weights, UpNotes& notes)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    if (lane >= slot.rows) return;
+    const int p0 = notes.token[lane] * s.K;
+    float total = 0.0f;
+    for (int k = 0; k < s.K; ++k)
+        if (ids[p0 + k] == slot.expert) total += weights[p0 + k];
+    notes.weight[lane] = total;
+}
+
 // RP: rows of an expert that share a sweep over its weights.
-template <bool F16, bool BLOCK, int RP>
-__global__ __launch_bounds__(kUpWaves * kWave) void up_kernel(LayerShape s, LayerArgs a)
+template <bool F16, bool BLOCK, int RP, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void up_kernel(LayerShape s, LayerArgs a)
 {
     typedef Stage<F16, BLOCK, 2, RP> S;
     constexpr int kRows = S::kTiles;
-    __shared__ __align__(1024) char ring[kUpWaves][kRing][S::kBytes];
-    __shared__ UpNotes all_notes[kUpWaves];
+    __shared__ __align__(1024) char ring[WAVES][kRing][S::kBytes];
+    __shared__ UpNotes all_notes[WAVES];
     static_assert(kRing * S::kBytes >= kRows * 2 * kWave * 16, "a wave's sums take its ring's place");
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, g = lane >> 4;
     UpNotes& notes = all_notes[wave];
     const int j = blockIdx.y;
-    const Slot slot = find_slot(s, a, j, notes);
+    extern __shared__ char picks[];             // ids, then weights
+    int* ids = reinterpret_cast<int*>(picks);
+    float* weights = reinterpret_cast<float*>(ids + s.T * s.K);
+    const Slot slot = find_slot(s, a, j, notes, ids, weights);
     if (blockIdx.x == 0 && wave == 0) {
         if (lane == 0) a.slots[j] = slot;
         if (lane < slot.rows) a.tokens[slot.first + lane] = notes.token[lane];
@@ -269,6 +301,10 @@ __global__ __launch_bounds__(kUpWaves * kWave) void up_kernel(LayerShape s, Laye
             load_lds4(make_rsrc(scales + (size_t)t * blocks * chunks, (uint32_t)chunks * 4),
                       reinterpret_cast<char*>(notes.scales[t]), (uint32_t)lane * 4);
     }
+    // Each workgroup begins at another chunk, so that rows of a length that is a multiple of a large
+    // power of two are not read in step all over the chip (H = 4096, F = 1024: 44.5 -> 40.8 us).
+    const int rot = (int)(blockIdx.x * 5 % chunks);
+    const auto turn = [&](int c) { return c >= chunks ? c : c + rot >= chunks ? c + rot - chunks : c + rot; };
     for (int r0 = 0; r0 < slot.rows; r0 += RP) {
         uint32_t xoff[S::kXLoads];
 #pragma unroll
@@ -280,21 +316,22 @@ __global__ __launch_bounds__(kUpWaves * kWave) void up_kernel(LayerShape s, Laye
 #pragma unroll
         for (int m = 0; m < kRows; ++m) acc[m][0] = acc[m][1] = v4f_t{0, 0, 0, 0};
 #pragma unroll
-        for (int d = 0; d < kRing; ++d) S::fill(ring[wave][d], wr, xr, row_bytes, xoff, wave + d * kUpWaves);
-        for (int c = wave; c < chunks; c += kRing * kUpWaves) {
+        for (int d = 0; d < kRing; ++d) S::fill(ring[wave][d], wr, xr, row_bytes, xoff, turn(wave + d * WAVES));
+        if (r0 == 0) sum_weights(s, slot, ids, weights, notes);
+        for (int c = wave; c < chunks; c += kRing * WAVES) {
 #pragma unroll
             for (int d = 0; d < kRing; ++d) {
-                const int now = c + d * kUpWaves;
+                const int now = c + d * WAVES;
                 typename S::Regs r;
                 wait_loads<(kRing - 1) * S::kLoads>();
                 S::read(ring[wave][d], r);
                 float sc[2];
                 if (BLOCK) {
-                    sc[0] = notes.scales[0][now & (kMaxChunks - 1)];
-                    sc[1] = notes.scales[1][now & (kMaxChunks - 1)];
+                    sc[0] = notes.scales[0][turn(now) & (kMaxChunks - 1)];
+                    sc[1] = notes.scales[1][turn(now) & (kMaxChunks - 1)];
                 }
                 wait_lds();
-                S::fill(ring[wave][d], wr, xr, row_bytes, xoff, now + kRing * kUpWaves);
+                S::fill(ring[wave][d], wr, xr, row_bytes, xoff, turn(now + kRing * WAVES));
 #pragma unroll
                 for (int m = 0; m < kRows; ++m)
 #pragma unroll
@@ -316,13 +353,13 @@ __global__ __launch_bounds__(kUpWaves * kWave) void up_kernel(LayerShape s, Laye
             for (int t = 0; t < 2; ++t) mine[(m * 2 + t) * kWave + lane] = acc[m][t];
         __syncthreads();
         // one row tile a wave
-        for (int m = wave; m < kRows; m += kUpWaves) {
+        for (int m = wave; m < kRows; m += WAVES) {
             float r[2][4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 v4f_t v = reinterpret_cast<const v4f_t*>(ring[0][0])[(m * 2 + t) * kWave + lane];
 #pragma unroll
-                for (int o = 1; o < kUpWaves; ++o)
+                for (int o = 1; o < WAVES; ++o)
                     v += reinterpret_cast<const v4f_t*>(ring[o][0])[(m * 2 + t) * kWave + lane];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) r[t][q] = v[q];
@@ -345,10 +382,10 @@ __global__ __launch_bounds__(kUpWaves * kWave) void up_kernel(LayerShape s, Laye
 struct DownLds {
     size_t ring, sums, slots, tokens, scales;
 };
-__host__ __device__ inline DownLds down_lds(const LayerShape& s, int waves, int stage, int cols, int rp)
+__host__ __device__ inline DownLds down_lds(const LayerShape& s, int waves, int stages, int cols, int rp)
 {
     DownLds l;
-    l.ring = (size_t)waves * kRing * stage;
+    l.ring = (size_t)waves * stages;
     l.sums = (size_t)waves * s.T * cols * 4;
     l.slots = ((size_t)s.slots + (s.T > rp ? s.T * s.K / rp : 0)) * sizeof(Slot);
     l.tokens = (size_t)s.T * s.K * 4;
@@ -364,7 +401,7 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
     constexpr int kThreads = WAVES * kWave;
     extern __shared__ __align__(1024) char lds[];
     __shared__ int count_lds;
-    const DownLds parts = down_lds(s, WAVES, S::kBytes, kCols, RP);
+    const DownLds parts = down_lds(s, WAVES, kRing * S::kBytes, kCols, RP);
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, g = lane >> 4;
@@ -381,11 +418,14 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
             Slot slot = {-1, 0, 0, 0};
             if (i0 + lane < s.slots) slot = a.slots[i0 + lane];
             const int pieces = slot.expert < 0 ? 0 : (slot.rows + RP - 1) / RP;
-            int upto = pieces;
+            int upto = __popcll((unsigned long long)(__ballot(pieces > 0) & (~0ull >> (kWave - 1 - lane))));
+            if (__ballot(pieces > 1) != 0) {
+                upto = pieces;
 #pragma unroll
-            for (int off = 1; off < kWave; off <<= 1) {
-                const int o = __shfl_up(upto, off, kWave);
-                if (lane >= off) upto += o;
+                for (int off = 1; off < kWave; off <<= 1) {
+                    const int o = __shfl_up(upto, off, kWave);
+                    if (lane >= off) upto += o;
+                }
             }
             for (int p = 0; p < pieces; ++p)
                 slots[count + upto - pieces + p] = {slot.expert, slot.first + p * RP,
@@ -405,16 +445,18 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
     const int n0 = blockIdx.x * kCols;
     const int blocks = (s.H + 127) / 128;
 
-    // Units (slot, chunk) go round the waves: unit i of a wave is number wave + WAVES * i.
+    // Units (slot, chunk), one after another; a wave takes as many in a row as any other, so that it
+    // seldom goes on to another slot.
     struct Place { int slot, chunk; };
     const auto step = [&](Place p) {
-        p.chunk += WAVES;
-        while (p.chunk >= chunks) {
-            p.chunk -= chunks;
+        if (++p.chunk == chunks) {
+            p.chunk = 0;
             ++p.slot;
         }
         return p;
     };
+    const int first = (int)((int64_t)count * chunks * wave / WAVES);
+    const int units = (int)((int64_t)count * chunks * (wave + 1) / WAVES) - first;
     const auto slot_at = [&](int i) {
         Slot r;
         r.expert = __builtin_amdgcn_readfirstlane(slots[i].expert);
@@ -422,11 +464,14 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
         r.rows = __builtin_amdgcn_readfirstlane(slots[i].rows);
         return r;
     };
-    Place ahead = step(Place{0, wave - WAVES});
+    const int rot = (int)(blockIdx.x * 3 % chunks);          // as in the up kernel
+    const auto turn = [&](int c) { return c + rot >= chunks ? c + rot - chunks : c + rot; };
+    Place ahead = {first / chunks, first % chunks};
     Slot next = {0, 0, 0, 0};
     int held = -1;                              // the slot that `next` describes
+    int filled = 0;                             // units asked for
     const auto fill = [&](int d) {
-        const bool there = ahead.slot < count;
+        const bool there = filled++ < units;
         if (there && held != ahead.slot) {
             next = slot_at(ahead.slot);
             held = ahead.slot;
@@ -445,15 +490,15 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
 #pragma unroll
         for (int i = 0; i < S::kXLoads; ++i)
             xoff[i] = S::xrow(i) < RP ? (uint32_t)S::xrow(i) * h_bytes : kRsrcPastEnd;
-        S::fill(ring + d * S::kBytes, wr, hr, row_bytes, xoff, ahead.chunk);
+        S::fill(ring + d * S::kBytes, wr, hr, row_bytes, xoff, turn(ahead.chunk));
         ahead = step(ahead);
     };
     // The scales of units 64 * batch + 0..63 of the wave, a lane each.
     const auto fetch_scales = [&](int batch) {
-        const int unit = wave + WAVES * (batch * kWave + lane);
+        const int unit = first + batch * kWave + lane;
         const int i = unit / chunks;
         const uint32_t off = i < count ? (uint32_t)(((size_t)slots[i].expert * blocks + n0 / 128) * chunks +
-                                                    (unit - i * chunks)) * 4
+                                                    turn(unit - i * chunks)) * 4
                                        : kRsrcPastEnd;
         load_lds4(make_rsrc(a.down_scales, (uint32_t)s.E * blocks * chunks * 4),
                   reinterpret_cast<char*>(scales + (batch & 1) * kWave), off);
@@ -483,11 +528,11 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
         }
         clear();
     };
-    Place now = step(Place{0, wave - WAVES});
+    Place now = ahead;
     int open = now.slot, unit = 0;
 #pragma unroll
     for (int d = 0; d < kRing; ++d) fill(d);
-    while (now.slot < count) {
+    while (unit < units) {
 #pragma unroll
         for (int d = 0; d < kRing; ++d) {
             typename S::Regs r;
@@ -498,7 +543,7 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
             wait_lds();
             if (BLOCK && (unit & (kWave - 1)) == 0) fetch_scales(unit / kWave + 1);
             fill(d);
-            if (now.slot < count) {
+            if (unit < units) {
                 if (now.slot != open) {
                     flush(open);
                     open = now.slot;
@@ -518,7 +563,7 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
         }
     }
     wait_loads<0>();                            // nothing lands in LDS any more
-    if (open < count) flush(open);
+    if (units > 0) flush(open);
     __syncthreads();
     for (int i = threadIdx.x; i < s.T * kCols; i += kThreads) {
         const int t = i / kCols, n = n0 + i % kCols;
@@ -541,19 +586,26 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
 template <bool F16, bool BLOCK, int NT, int RP, int WAVES>
 hipError_t launch_down(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
 {
-    const DownLds l = down_lds(s, WAVES, Stage<F16, BLOCK, NT, RP>::kBytes, NT * 16, RP);
+    const DownLds l = down_lds(s, WAVES, kRing * Stage<F16, BLOCK, NT, RP>::kBytes, NT * 16, RP);
     const size_t bytes = l.ring + l.sums + l.slots + l.tokens + l.scales;
     down_kernel<F16, BLOCK, NT, RP, WAVES><<<(unsigned)((s.H + NT * 16 - 1) / (NT * 16)), WAVES * kWave, bytes,
                                              stream>>>(s, a);
     return hipGetLastError();
 }
 
+template <bool F16, bool BLOCK, int RP, int WAVES>
+hipError_t launch_up(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
+{
+    up_kernel<F16, BLOCK, RP, WAVES><<<dim3((unsigned)((s.F + 15) / 16), (unsigned)s.slots), WAVES * kWave,
+                                       (size_t)s.T * s.K * 8, stream>>>(s, a);
+    return hipGetLastError();
+}
+
 template <bool F16, bool BLOCK, int RP>
 hipError_t launch_rows(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
 {
-    up_kernel<F16, BLOCK, RP><<<dim3((unsigned)((s.F + 15) / 16), (unsigned)s.slots), kUpWaves * kWave, 0,
-                                stream>>>(s, a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = (int64_t)s.slots * s.F <= kFewUp ? launch_up<F16, BLOCK, RP, 4>(s, a, stream)
+                                                          : launch_up<F16, BLOCK, RP, 2>(s, a, stream);
     if (e != hipSuccess) return e;
     if (s.H >= kWideDown) return launch_down<F16, BLOCK, 2, RP, 4>(s, a, stream);
     // (eight rings of 32 rows with codes do not fit the 160 KB of LDS)
