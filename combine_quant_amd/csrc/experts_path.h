@@ -9,13 +9,17 @@ namespace moe_dc {
 enum ProductPath : int32_t {
     kPathStream = 0,            // 32 weight rows a workgroup, memory to registers
     kPathTiles = 1,             // 256 weight rows a workgroup, through LDS
-    kPathSmallTiles = 2         // 128 weight rows, 4-bit weights only
+    kPathSmallTiles = 2,        // 128 weight rows, 4-bit weights only
+    kPathThinTiles = 3          // 128 weight rows, block kinds only
 };
 
 constexpr int kTileN = 256;                     // weight rows of a workgroup
 // Most rows of x of a workgroup: as many as the 160 KB of LDS take (MX and block kinds keep scales
 // there too).
 constexpr int tile_rows(int type) { return type >= kMmMxE4m3 ? 192 : 256; }
+
+constexpr int kThinRows = 64;                   // rows of x and weight rows of a thin tile (block kinds)
+constexpr int kThinN = 128;
 
 constexpr int kW4TileM = 128;                   // rows of x and weight rows of a workgroup
 constexpr int kW4TileN = 256;
@@ -42,6 +46,16 @@ constexpr int kTileLeast = 56;
 constexpr int kSmallLeast = 144;
 constexpr int kW4TileLeast = 80;
 
+// Block kinds, us by streaming, thin and large tiles.  Large tiles from 192 of them on: 144 of them
+// (8 experts x 1024 rows, 2048 x 768) 110, 28.7, 28.4; 192 (64 x 32 rows, 7168 x 768) 123, 73.8, 68.3, (8 x
+// 512 rows, 7168 x 2048) 433, 97.5, 73.5; 48 (8 x 512 rows, 4096 x 512) 71, 24.7, 42.4.
+// Streaming for up to 32 rows an expert and fewer than 96 thin tiles: 64 of them (16 x 20 rows, 7168 x
+// 512) 19.3, 22.0, 29.5, (64 x 2 rows, 1024 x 128) 5.6, 6.3, 7.8; 128 (16 x 20 rows, 7168 x 1024) 32.0, 22.9,
+// 30.2, (64 x 4 rows, 2048 x 256) 9.6, 8.7, 11.2; with 64 rows 16 thin tiles (8 experts, 1024 x 256) 10.6, 7.8, 11.1.
+constexpr int kBlockTileLeast = 192;
+constexpr int kThinLeast = 96;
+constexpr int kBlockStreamRows = 32;
+
 // Whether there are at least `least` tiles of `height` rows and `cols` columns, in the mean over
 // the experts that can have rows.
 inline bool tiles_suffice(const MatmulShape& s, int height, int cols, int least)
@@ -55,6 +69,16 @@ inline bool tiles_suffice(const MatmulShape& s, int height, int cols, int least)
 inline ProductPath product_path(const MatmulShape& s)
 {
     const int part = s.swiglu ? 2 : 1;
+    if (s.type == kMmBlockE4m3 || s.type == kMmBlockE5m2) {
+        const int64_t active = s.rows < s.E ? s.rows : s.E;
+        const bool large = tiles_suffice(s, tile_rows(s.type), kTileN / part, kBlockTileLeast);
+        // codes need groups of 128 columns within one workgroup, which thin tiles of gate and up are not
+        if (large || (s.out_code && s.swiglu)) return kPathTiles;
+        if (s.out_code || s.rows > kBlockStreamRows * active ||
+            tiles_suffice(s, kThinRows, kThinN / part, kThinLeast))
+            return kPathThinTiles;
+        return kPathStream;
+    }
     if (!s.w4)
         return tiles_suffice(s, tile_rows(s.type), kTileN / part, kTileLeast) ? kPathTiles : kPathStream;
     // few rows per expert: the smaller tiles, where they are enough

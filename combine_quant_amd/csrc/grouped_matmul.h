@@ -10,9 +10,10 @@ namespace {
 template <int TYPE>
 hipError_t launch_type(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
-    // coded results need whole groups of 128 columns in one workgroup
-    if (Mm<TYPE>::kBlk && s.out_code) return launch_tiles<TYPE>(s, a, stream);
-    return product_path(s) == kPathTiles ? launch_tiles<TYPE>(s, a, stream) : launch_stream<TYPE>(s, a, stream);
+    const ProductPath path = product_path(s);
+    if constexpr (Mm<TYPE>::kBlk)
+        if (path == kPathThinTiles) return launch_thin_tiles<TYPE>(s, a, stream);
+    return path == kPathTiles ? launch_tiles<TYPE>(s, a, stream) : launch_stream<TYPE>(s, a, stream);
 }
 
 }  // namespace

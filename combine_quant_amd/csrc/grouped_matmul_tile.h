@@ -22,28 +22,30 @@ namespace {
 
 constexpr int kTileRing = 3;                    // steps of x in LDS
 
-template <int TYPE>
-constexpr int kTileM = tile_rows(TYPE);
+// WAVES: 8, or 4 for thin tiles (kThinRows rows x 128 weight rows), two of which share a CU.
+template <int TYPE, int WAVES>
+constexpr int kTileM = WAVES == kTileWaves ? tile_rows(TYPE) : kThinRows;
 
-template <int TYPE>
+template <int TYPE, int WAVES>
 struct TileStages {
-    char x[kTileRing][kTileM<TYPE> * 128];      // [row][128 bytes], swizzled
-    char w[kTileWaves][2][32 * 128];            // each wave's own 32 weight rows, swizzled
+    static constexpr int kRows = kTileM<TYPE, WAVES>;
+    char x[kTileRing][kRows * 128];             // [row][128 bytes], swizzled
+    char w[WAVES][2][32 * 128];                 // each wave's own 32 weight rows, swizzled
     // MX: the E8M0 bytes of four steps, 16 of each row of x, then of each weight row (with the
     // four bytes of one step at a time the requests for them outnumbered the rows': 3.45 ms
     // instead of 2.63 at 65536 skewed rows on 256 experts x 7168 x 4096)
     // Block: the floats of four steps, likewise 16 bytes of each row of x, then of the tile's two
     // rows of weight blocks
-    char scales[2][Mm<TYPE>::kMx ? (kTileM<TYPE> + kTileN) * 16 : Mm<TYPE>::kBlk ? (kTileM<TYPE> + 64) * 16 : 0];
+    char scales[2][Mm<TYPE>::kMx ? (kRows + kTileN) * 16 : Mm<TYPE>::kBlk ? (kRows + 64) * 16 : 0];
 };
 
 // The table is done with before the first stage is filled, and the stages before the largest
 // values of a coded output meet: of each row, per wave (Mm<TYPE>::kBlk).
-template <int TYPE>
+template <int TYPE, int WAVES>
 union TileLds {
-    TileStages<TYPE> st;
+    TileStages<TYPE, WAVES> st;
     TileTable table;
-    uint32_t amax[Mm<TYPE>::kBlk ? kTileM<TYPE> * kTileWaves : 1];
+    uint32_t amax[Mm<TYPE>::kBlk ? kTileM<TYPE, WAVES> * WAVES : 1];
 };
 
 // Four values as codes, the first in the lowest byte.  None is NaN.
@@ -65,10 +67,10 @@ __device__ __forceinline__ uint32_t code4(const float (&v)[4], int code)
 }
 
 // A tile's sums as codes with one scale per row and 128 columns, as dispatch codes a token in mode
-// 3.  A tile holds one group of columns with SwiGLU, else two, so the largest values of 8 or 4
+// 3.  A tile holds one group of columns with SwiGLU or thin, else two, so the largest values of 8 or 4
 // waves meet in LDS and nothing but the codes leaves the workgroup.  In a group with an infinity or a
 // NaN (whose bits are the largest) the scale is NaN and the codes are 0.
-template <int TYPE, int MT, bool SWIGLU>
+template <int TYPE, int WAVES, int MT, bool SWIGLU>
 __device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs& a, const Tile& tile,
                                           int half, int left, v4f_t (&acc)[MT][2], uint32_t* amax)
 {
@@ -76,7 +78,8 @@ __device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, g = lane >> 4;
     constexpr int kT = SWIGLU ? 1 : 2;
-    constexpr int kMeet = SWIGLU ? kTileWaves : kTileWaves / 2;      // waves of a group
+    constexpr int kMeet = kBlock / (kT * 16);                        // waves of a group
+    static_assert(WAVES % kMeet == 0, "a group of columns lies within one tile");
     const int c0 = wave * (kT * 16) + g * 4;
     __syncthreads();                            // the last step's rows have been read
 #pragma unroll
@@ -103,7 +106,7 @@ __device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs
         }
         most = dpp_max(most, __shfl_xor(most, 16, kWave));
         most = dpp_max(most, __shfl_xor(most, 32, kWave));
-        if (g == 0) amax[(m * 16 + l16) * kTileWaves + wave] = most;
+        if (g == 0) amax[(m * 16 + l16) * WAVES + wave] = most;
     }
     __syncthreads();
     const int first = wave / kMeet * kMeet;
@@ -114,7 +117,7 @@ __device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs
         if (row >= tile.rows) continue;
         uint32_t most = 0;
 #pragma unroll
-        for (int w = 0; w < kMeet; ++w) most = dpp_max(most, amax[row * kTileWaves + first + w]);
+        for (int w = 0; w < kMeet; ++w) most = dpp_max(most, amax[row * WAVES + first + w]);
         const bool finite = most < 0x7F800000u;
         float dyn = (s.out_code == kCodeE4m3 ? 448.0f : 57344.0f) / __uint_as_float(most);
         const float scale = finite ? 1.0f / dyn : NAN;
@@ -156,11 +159,12 @@ __device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs
 // step k + 1 move from LDS to registers at the start of step k, and their place takes the weights
 // of step k + 3.  Loads past the end of a row return 0 without a memory access, so every step
 // issues the same number.
-template <int TYPE, int MT, bool SWIGLU>
+template <int TYPE, int WAVES, int MT, bool SWIGLU>
 __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulArgs& a,
-                                             const Tile& tile, TileLds<TYPE>& shared)
+                                             const Tile& tile, TileLds<TYPE, WAVES>& shared)
 {
-    TileStages<TYPE>& lds = shared.st;
+    TileStages<TYPE, WAVES>& lds = shared.st;
+    constexpr int kRows = kTileM<TYPE, WAVES>, kWeightRows = 32 * WAVES;
     const int e = tile.e, n0 = tile.n0, row0 = tile.row0, rows = tile.rows;
     typedef Mm<TYPE> M;
     typedef typename M::Acc Acc;
@@ -170,7 +174,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     const uint32_t row_bytes = (uint32_t)s.in * M::kBytes;
     const int steps = (int)((row_bytes + 127) / 128);
     const int half = SWIGLU ? s.out / 2 : s.out;
-    constexpr int kCols = SWIGLU ? kTileN / 2 : kTileN;      // columns of the output
+    constexpr int kCols = SWIGLU ? kWeightRows / 2 : kWeightRows;    // columns of the output
     const int left = half - n0 < kCols ? half - n0 : kCols;
     const char* wbase = static_cast<const char*>(a.w) + ((size_t)e * s.out + n0) * row_bytes;
     const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(wbase, (uint32_t)left * row_bytes);
@@ -189,14 +193,14 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     const int lr = lane >> 3;
     const uint32_t lk = (uint32_t)((lane & 7) ^ lr) * 16;
     constexpr int kBlocks = 2 * MT;                          // of 8 rows
-    constexpr int kXLoads = (kBlocks + kTileWaves - 1) / kTileWaves;
+    constexpr int kXLoads = (kBlocks + WAVES - 1) / WAVES;
     // (where the blocks do not go round, some waves load again what another one does, so that
     // every wave issues the same number without a branch)
     uint32_t xoff[kXLoads], woff[4];
     int xblk[kXLoads];
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
-        xblk[i] = wave + i * kTileWaves;
+        xblk[i] = wave + i * WAVES;
         if (xblk[i] >= kBlocks) xblk[i] %= kBlocks;
         xoff[i] = (uint32_t)(xblk[i] * 8 + lr) * row_bytes + lk;
     }
@@ -210,8 +214,8 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     // Block: waves 3-7 the same two rows of weight blocks, of columns n0 and n0 + 128 or of gate
     // and up.
     constexpr bool kLdsScales = M::kMx || M::kBlk;
-    const bool sx = wave * 64 < kTileM<TYPE>;
-    const int sblk = sx ? wave : M::kBlk ? 0 : (wave < 6 ? wave : 6) - kTileM<TYPE> / 64;
+    const bool sx = wave * 64 < kRows;
+    const int sblk = sx ? wave : M::kBlk ? 0 : (wave < 6 ? wave : 6) - kRows / 64;
     const int srow = sblk * 64 + lane;
     const int scol = SWIGLU ? srow / 32 * 16 + (srow & 15) : srow;      // of the weight row
     const bool sok = sx ? srow < rows : M::kBlk ? srow < 2 && (SWIGLU || srow * kBlock < left) : scol < left;
@@ -221,7 +225,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         sx ? static_cast<const char*>(a.x_scales) + (size_t)row0 * ns : wsb,
         !kLdsScales ? 0 : (uint32_t)(sx ? rows : M::kBlk ? (SWIGLU ? blocks + 1 : left > kBlock ? 2 : 1)
                                                   : SWIGLU ? half + left : left) * ns);
-    const int sto = (sx ? 0 : kTileM<TYPE> * 16) + sblk * 1024;
+    const int sto = (sx ? 0 : kRows * 16) + sblk * 1024;
     // The 16 bytes of a row's last window end where the row does (from the window's own start they
     // would run into the next row and, of the last row, past the tensor), so that its steps lie
     // scale_shift bytes further; a row of fewer than 16 bytes comes a step's dword at a time, as
@@ -278,8 +282,8 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         for (int t = 0; t < 2; ++t) {
             w[par][t] = join(*reinterpret_cast<const v4i_t*>(wl + t * 2048 + f0),
                              *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f1));
-            if (M::kMx) wsc[par][t] = scale_of(where, step, kTileM<TYPE> + wave * 32 + t * 16);
-            if (M::kBlk) wsc[par][t] = scale_at(where, step, kTileM<TYPE>, SWIGLU ? t : wave >> 2);
+            if (M::kMx) wsc[par][t] = scale_of(where, step, kRows + wave * 32 + t * 16);
+            if (M::kBlk) wsc[par][t] = scale_at(where, step, kRows, SWIGLU ? t : wave >> 2);
         }
     };
     Acc acc[MT][2];
@@ -407,9 +411,9 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 
     constexpr int kT = SWIGLU ? 1 : 2;
     const int c0 = wave * (kT * 16) + g * 4;    // the lane's first column
-    if constexpr (M::kBlk) {
+    if constexpr (M::kBlk && WAVES * kT * 16 >= kBlock) {
         if (s.out_code != 0) {
-            code_tile<TYPE, MT, SWIGLU>(s, a, tile, half, left, acc, shared.amax);
+            code_tile<TYPE, WAVES, MT, SWIGLU>(s, a, tile, half, left, acc, shared.amax);
             return;
         }
     }
@@ -454,39 +458,67 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 template <int TYPE, bool SWIGLU>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, MatmulArgs a)
 {
-    __shared__ TileLds<TYPE> lds;
-    constexpr int kRows = kTileM<TYPE>;
+    constexpr int WAVES = kTileWaves;
+    __shared__ TileLds<TYPE, WAVES> lds;
+    constexpr int kRows = kTileM<TYPE, WAVES>;
     Tile t;
     if (!find_tile<kRows, SWIGLU ? kTileN / 2 : kTileN>(s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t))
         return;
     switch ((t.rows + 15) / 16) {
-    case 1: tile_product<TYPE, 1, SWIGLU>(s, a, t, lds); break;
-    case 2: tile_product<TYPE, 2, SWIGLU>(s, a, t, lds); break;
-    case 3: tile_product<TYPE, 3, SWIGLU>(s, a, t, lds); break;
-    case 4: tile_product<TYPE, 4, SWIGLU>(s, a, t, lds); break;
-    case 5: tile_product<TYPE, 5, SWIGLU>(s, a, t, lds); break;
-    case 6: tile_product<TYPE, 6, SWIGLU>(s, a, t, lds); break;
-    case 7: tile_product<TYPE, 7, SWIGLU>(s, a, t, lds); break;
-    case 8: tile_product<TYPE, 8, SWIGLU>(s, a, t, lds); break;
-    case 9: tile_product<TYPE, 9, SWIGLU>(s, a, t, lds); break;
-    case 10: tile_product<TYPE, 10, SWIGLU>(s, a, t, lds); break;
-    case 11: tile_product<TYPE, 11, SWIGLU>(s, a, t, lds); break;
-    case 12: tile_product<TYPE, 12, SWIGLU>(s, a, t, lds); break;
+    case 1: tile_product<TYPE, WAVES, 1, SWIGLU>(s, a, t, lds); break;
+    case 2: tile_product<TYPE, WAVES, 2, SWIGLU>(s, a, t, lds); break;
+    case 3: tile_product<TYPE, WAVES, 3, SWIGLU>(s, a, t, lds); break;
+    case 4: tile_product<TYPE, WAVES, 4, SWIGLU>(s, a, t, lds); break;
+    case 5: tile_product<TYPE, WAVES, 5, SWIGLU>(s, a, t, lds); break;
+    case 6: tile_product<TYPE, WAVES, 6, SWIGLU>(s, a, t, lds); break;
+    case 7: tile_product<TYPE, WAVES, 7, SWIGLU>(s, a, t, lds); break;
+    case 8: tile_product<TYPE, WAVES, 8, SWIGLU>(s, a, t, lds); break;
+    case 9: tile_product<TYPE, WAVES, 9, SWIGLU>(s, a, t, lds); break;
+    case 10: tile_product<TYPE, WAVES, 10, SWIGLU>(s, a, t, lds); break;
+    case 11: tile_product<TYPE, WAVES, 11, SWIGLU>(s, a, t, lds); break;
+    case 12: tile_product<TYPE, WAVES, 12, SWIGLU>(s, a, t, lds); break;
     default:
         if constexpr (kRows > 192) switch ((t.rows + 15) / 16) {
-            case 13: tile_product<TYPE, 13, SWIGLU>(s, a, t, lds); break;
-            case 14: tile_product<TYPE, 14, SWIGLU>(s, a, t, lds); break;
-            case 15: tile_product<TYPE, 15, SWIGLU>(s, a, t, lds); break;
-            default: tile_product<TYPE, 16, SWIGLU>(s, a, t, lds); break;
+            case 13: tile_product<TYPE, WAVES, 13, SWIGLU>(s, a, t, lds); break;
+            case 14: tile_product<TYPE, WAVES, 14, SWIGLU>(s, a, t, lds); break;
+            case 15: tile_product<TYPE, WAVES, 15, SWIGLU>(s, a, t, lds); break;
+            default: tile_product<TYPE, WAVES, 16, SWIGLU>(s, a, t, lds); break;
             }
         break;
     }
 }
 
+// Few rows per expert: tiles of at most kThinRows rows.
+template <int TYPE, bool SWIGLU>
+__global__ __launch_bounds__(4 * kWave, 2) void thin_tile_kernel(MatmulShape s, MatmulArgs a)
+{
+    constexpr int WAVES = 4;
+    __shared__ TileLds<TYPE, WAVES> lds;
+    Tile t;
+    if (!find_tile<kThinRows, SWIGLU ? kThinN / 2 : kThinN, WAVES>(s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t)) return;
+    switch ((t.rows + 15) / 16) {
+    case 1: tile_product<TYPE, WAVES, 1, SWIGLU>(s, a, t, lds); break;
+    case 2: tile_product<TYPE, WAVES, 2, SWIGLU>(s, a, t, lds); break;
+    case 3: tile_product<TYPE, WAVES, 3, SWIGLU>(s, a, t, lds); break;
+    default: tile_product<TYPE, WAVES, 4, SWIGLU>(s, a, t, lds); break;
+    }
+}
+
+template <int TYPE>
+hipError_t launch_thin_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
+{
+    const dim3 grid(tile_grid(s, kThinRows, s.swiglu ? kThinN / 2 : kThinN));
+    if (s.swiglu)
+        thin_tile_kernel<TYPE, true><<<grid, 4 * kWave, 0, stream>>>(s, a);
+    else
+        thin_tile_kernel<TYPE, false><<<grid, 4 * kWave, 0, stream>>>(s, a);
+    return hipGetLastError();
+}
+
 template <int TYPE>
 hipError_t launch_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
-    const dim3 grid(tile_grid(s, kTileM<TYPE>, s.swiglu ? kTileN / 2 : kTileN));
+    const dim3 grid(tile_grid(s, tile_rows(TYPE), s.swiglu ? kTileN / 2 : kTileN));
     if (s.swiglu)
         tile_kernel<TYPE, true><<<grid, kTileThreads, 0, stream>>>(s, a);
     else

@@ -131,6 +131,19 @@ int moe_dc_selfcheck_product_path(int type, int w4, int E, long long rows, int o
     return product_path(s);
 }
 
+// The same for a block kind whose results are coded (code: a moe_dtype, 0: tokens).
+int moe_dc_selfcheck_coded_product_path(int type, int E, long long rows, int out, int swiglu, int code)
+{
+    MatmulShape s{};
+    s.type = type;
+    s.E = E;
+    s.rows = rows;
+    s.out = out;
+    s.swiglu = swiglu;
+    s.out_code = code;
+    return product_path(s);
+}
+
 // out[i] = 2^t[i] (which = 0, t <= 0) or e^t[i] (which = 1, t <= 0) as the router forms them.
 void moe_dc_selfcheck_exp(int which, const double* t, double* out, long long n)
 {

@@ -121,3 +121,22 @@ def test_binding_refuses_cpu_tensors():
     s = torch.zeros((64, 2))
     with pytest.raises(ValueError):
         cq.grouped_matmul_quantize(_cfg(), _mm(), E4, x, s, x, s, s, s)
+
+
+@pytest.mark.parametrize("E,rows,N,swiglu,coded,want", [
+    # large tiles of 192 rows x 256 columns (SwiGLU 128 of each half): from 192 of them on
+    (64, 2048, 768, False, 0, 1), (64, 2048, 512, False, 0, 3), (8, 4096, 2048, True, 0, 1), (8, 4096, 1792, True, 0, 3),
+    # streaming: up to 32 rows an expert and fewer than 96 thin tiles of 64 rows x 128 columns
+    (8, 256, 11 * 128, False, 0, 0), (8, 256, 12 * 128, False, 0, 3), (8, 264, 128, False, 0, 3),
+    (8, 64, 11 * 128, True, 0, 0), (8, 64, 12 * 128, True, 0, 3), (8, 4, 1024, False, 0, 0),
+    # coded results: never streamed, and gate and up in large tiles
+    (8, 64, 128, False, 2, 3), (8, 64, 128, True, 3, 1), (64, 2048, 768, False, 2, 1),
+])
+@pytest.mark.parametrize("kind", [7, 8])
+def test_which_kernel(kind, E, rows, N, swiglu, coded, want):
+    import ctypes
+    from combine_quant_amd import build as B
+    fn = ctypes.CDLL(B.SELFCHECK_LIB).moe_dc_selfcheck_coded_product_path
+    fn.argtypes = [ctypes.c_int] * 2 + [ctypes.c_longlong] + [ctypes.c_int] * 3
+    fn.restype = ctypes.c_int
+    assert fn(kind, E, rows, N, int(swiglu), coded) == want

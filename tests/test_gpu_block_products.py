@@ -16,6 +16,7 @@ DEV = "cuda"
 KINDS = ("e4m3", "e5m2")
 CODE = {"e4m3": cq.MOE_DTYPE_E4M3, "e5m2": cq.MOE_DTYPE_E5M2}
 experts_path.TYPES.update(block_e4m3=7, block_e5m2=8)
+experts_path.NAMES = experts_path.NAMES[:3] + ("thin",)
 
 
 def _config(W, counts, f16=False, extra=5):
@@ -80,8 +81,9 @@ COUNTS = [
     (2, [31, 33, 64, 65, 0, 7, 100, 129]),
     (5, [300, 3, 0, 0, 513]),
 ]
-# 64 experts: enough tiles of 256 columns for the tile kernel
-MANY = (2, [(7 * e) % 23 for e in range(62)] + [193, 400])
+FEW = (2, [0, 3, 17, 50])                               # 18 rows an expert: streamed
+SOME = (2, [0, 3, 17, 65, 200, 0])                      # 48: thin tiles
+MANY = (2, [(7 * e) % 5 for e in range(254)] + [193, 400])       # 256 experts: large tiles
 
 
 @pytest.mark.parametrize("swiglu", [False, True])
@@ -96,19 +98,14 @@ SIZES = [(16, 1, False), (16, 2, True), (112, 33, False), (128, 256, True), (144
          (640, 512, False), (1136, 777, False), (1280, 1000, True)]
 
 
-@pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("I,N,swiglu", SIZES)
-def test_sizes_streamed(kind, I, N, swiglu):
-    W, counts = 2, [0, 3, 17, 50]
-    assert experts_path.path("block_" + kind, _config(W, counts), N, swiglu) == "stream"
-    _run(kind, W, counts, I, N, swiglu, seed=I + N)
+ROUTES = [(*FEW, "stream"), (*SOME, "thin"), (*MANY, "tiles")]
 
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("I,N,swiglu", SIZES)
-def test_sizes_tiled(kind, I, N, swiglu):
-    W, counts = MANY
-    assert experts_path.path("block_" + kind, _config(W, counts), N, swiglu) == "tiles"
+@pytest.mark.parametrize("W,counts,path", ROUTES)
+def test_sizes(W, counts, path, I, N, swiglu, kind):
+    assert experts_path.path("block_" + kind, _config(W, counts), N, swiglu) == path
     _run(kind, W, counts, I, N, swiglu, seed=I + N, f16=N % 2 == 0)
 
 
@@ -119,7 +116,7 @@ def test_codes_sizes(kind, to, I, N, swiglu):
 
 
 @pytest.mark.parametrize("swiglu", [False, True])
-@pytest.mark.parametrize("W,counts", COUNTS + [MANY])
+@pytest.mark.parametrize("W,counts", COUNTS + [SOME, MANY])
 def test_codes_row_counts(W, counts, swiglu):
     _run_codes("e4m3", "e4m3", W, counts, 272, 320, swiglu, seed=len(counts))
 
@@ -136,7 +133,7 @@ def _exact_case(counts, I, N, seed):
     return cfg, x, power(cap, blk.groups(I)), w, power(E, blk.groups(N), blk.groups(I))
 
 
-@pytest.mark.parametrize("counts,path", [([5, 0, 33, 64], "stream"), (MANY[1], "tiles")])
+@pytest.mark.parametrize("counts,path", [([5, 0, 33, 64], "stream"), (SOME[1], "thin"), (MANY[1], "tiles")])
 @pytest.mark.parametrize("I,N", [(48, 200), (640, 150), (1040, 256)])
 def test_every_scale_meets_its_block(counts, path, I, N):
     cfg, x, xs, w, ws = _exact_case(counts, I, N, I + N)
@@ -150,7 +147,7 @@ def test_every_scale_meets_its_block(counts, path, I, N):
     assert (out[:rows] == y.to(torch.float32).to(torch.bfloat16)).all()
 
 
-@pytest.mark.parametrize("counts", [[5, 0, 33, 64], MANY[1]])
+@pytest.mark.parametrize("counts", [[5, 0, 33, 64], SOME[1], MANY[1]])
 @pytest.mark.parametrize("bad", [math.inf, math.nan])
 def test_bad_scales_stay_in_their_row_and_block(counts, bad):
     I, N = 400, 300
@@ -192,7 +189,7 @@ def test_codes_of_groups_that_are_zero_or_not_finite():
     assert (codes[38:rows, :256] == good[38:rows, :256]).all() and (s[38:rows, :2] == gs[38:rows, :2]).all()
 
 
-@pytest.mark.parametrize("counts", [[5, 0, 33, 64], MANY[1]])
+@pytest.mark.parametrize("counts", [[5, 0, 33, 64], SOME[1], MANY[1]])
 def test_same_bytes_every_time(counts):
     cfg, mm, x, xs, w, ws, erc, off, _, _ = _case("e4m3", 2, counts, 1040, 256, True, 9)
     rows = sum(counts)
