@@ -28,7 +28,7 @@ constexpr int kTileM = WAVES == kTileWaves ? tile_rows(TYPE) : kThinRows;
 
 template <int TYPE, int WAVES>
 struct TileStages {
-    static constexpr int kRows = kTileM<TYPE, WAVES>;
+    static constexpr int kRows = kTileM<TYPE, WAVES>, kScaleRows = (kRows + 63) / 64 * 64;
     char x[kTileRing][kRows * 128];             // [row][128 bytes], swizzled
     char w[WAVES][2][32 * 128];                 // each wave's own 32 weight rows, swizzled
     // MX: the E8M0 bytes of four steps, 16 of each row of x, then of each weight row (with the
@@ -36,7 +36,7 @@ struct TileStages {
     // instead of 2.63 at 65536 skewed rows on 256 experts x 7168 x 4096)
     // Block: the floats of four steps, likewise 16 bytes of each row of x, then of the tile's two
     // rows of weight blocks
-    char scales[2][Mm<TYPE>::kMx ? (kRows + kTileN) * 16 : Mm<TYPE>::kBlk ? (kRows + 64) * 16 : 0];
+    char scales[2][Mm<TYPE>::kMx ? (kScaleRows + kTileN) * 16 : Mm<TYPE>::kBlk ? (kScaleRows + 64) * 16 : 0];
 };
 
 // The table is done with before the first stage is filled, and the stages before the largest
@@ -165,6 +165,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 {
     TileStages<TYPE, WAVES>& lds = shared.st;
     constexpr int kRows = kTileM<TYPE, WAVES>, kWeightRows = 32 * WAVES;
+    constexpr int kScaleRows = TileStages<TYPE, WAVES>::kScaleRows;
     const int e = tile.e, n0 = tile.n0, row0 = tile.row0, rows = tile.rows;
     typedef Mm<TYPE> M;
     typedef typename M::Acc Acc;
@@ -215,7 +216,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     // and up.
     constexpr bool kLdsScales = M::kMx || M::kBlk;
     const bool sx = wave * 64 < kRows;
-    const int sblk = sx ? wave : M::kBlk ? 0 : (wave < 6 ? wave : 6) - kRows / 64;
+    const int sblk = sx ? wave : M::kBlk ? 0 : (wave < 6 ? wave : 6) - kScaleRows / 64;
     const int srow = sblk * 64 + lane;
     const int scol = SWIGLU ? srow / 32 * 16 + (srow & 15) : srow;      // of the weight row
     const bool sok = sx ? srow < rows : M::kBlk ? srow < 2 && (SWIGLU || srow * kBlock < left) : scol < left;
@@ -225,7 +226,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         sx ? static_cast<const char*>(a.x_scales) + (size_t)row0 * ns : wsb,
         !kLdsScales ? 0 : (uint32_t)(sx ? rows : M::kBlk ? (SWIGLU ? blocks + 1 : left > kBlock ? 2 : 1)
                                                   : SWIGLU ? half + left : left) * ns);
-    const int sto = (sx ? 0 : kRows * 16) + sblk * 1024;
+    const int sto = (sx ? 0 : kScaleRows * 16) + sblk * 1024;
     // The 16 bytes of a row's last window end where the row does (from the window's own start they
     // would run into the next row and, of the last row, past the tensor), so that its steps lie
     // scale_shift bytes further; a row of fewer than 16 bytes comes a step's dword at a time, as
@@ -282,8 +283,8 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         for (int t = 0; t < 2; ++t) {
             w[par][t] = join(*reinterpret_cast<const v4i_t*>(wl + t * 2048 + f0),
                              *reinterpret_cast<const v4i_t*>(wl + t * 2048 + f1));
-            if (M::kMx) wsc[par][t] = scale_of(where, step, kRows + wave * 32 + t * 16);
-            if (M::kBlk) wsc[par][t] = scale_at(where, step, kRows, SWIGLU ? t : wave >> 2);
+            if (M::kMx) wsc[par][t] = scale_of(where, step, kScaleRows + wave * 32 + t * 16);
+            if (M::kBlk) wsc[par][t] = scale_at(where, step, kScaleRows, SWIGLU ? t : wave >> 2);
         }
     };
     Acc acc[MT][2];
@@ -481,8 +482,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
         if constexpr (kRows > 192) switch ((t.rows + 15) / 16) {
             case 13: tile_product<TYPE, WAVES, 13, SWIGLU>(s, a, t, lds); break;
             case 14: tile_product<TYPE, WAVES, 14, SWIGLU>(s, a, t, lds); break;
-            case 15: tile_product<TYPE, WAVES, 15, SWIGLU>(s, a, t, lds); break;
-            default: tile_product<TYPE, WAVES, 16, SWIGLU>(s, a, t, lds); break;
+            default:
+                if constexpr (kRows > 224) {
+                    if ((t.rows + 15) / 16 == 15) tile_product<TYPE, WAVES, 15, SWIGLU>(s, a, t, lds);
+                    else tile_product<TYPE, WAVES, 16, SWIGLU>(s, a, t, lds);
+                }
+                break;
             }
         break;
     }

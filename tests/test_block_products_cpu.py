@@ -124,7 +124,7 @@ def test_binding_refuses_cpu_tensors():
 
 
 @pytest.mark.parametrize("E,rows,N,swiglu,coded,want", [
-    # large tiles of 192 rows x 256 columns (SwiGLU 128 of each half): from 192 of them on
+    # large tiles of 224 rows x 256 columns (SwiGLU 128 of each half): from 192 of them on
     (64, 2048, 768, False, 0, 1), (64, 2048, 512, False, 0, 3), (8, 4096, 2048, True, 0, 1), (8, 4096, 1792, True, 0, 3),
     # streaming: up to 32 rows an expert and fewer than 96 thin tiles of 64 rows x 128 columns
     (8, 256, 11 * 128, False, 0, 0), (8, 256, 12 * 128, False, 0, 3), (8, 264, 128, False, 0, 3),

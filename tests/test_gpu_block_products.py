@@ -121,6 +121,17 @@ def test_codes_row_counts(W, counts, swiglu):
     _run_codes("e4m3", "e4m3", W, counts, 272, 320, swiglu, seed=len(counts))
 
 
+@pytest.mark.parametrize("coded", [False, True])
+def test_every_tile_height(coded):
+    """Large tiles of 1 to 14 times 16 rows."""
+    counts = [16 * h - h % 3 for h in range(1, 15)] + [1] * 242
+    assert experts_path.path("block_e4m3", _config(2, counts), 256, True) == "tiles"
+    if coded:
+        _run_codes("e4m3", "e4m3", 2, counts, 400, 256, True, seed=1)
+    else:
+        _run("e4m3", 2, counts, 400, 256, True, seed=1)
+
+
 def _exact_case(counts, I, N, seed):
     """Small whole codes and scales that are powers of two: every sum is exact in fp32."""
     g = torch.Generator(device=DEV)
