@@ -6,6 +6,10 @@
 // vectors of eight elements a thread, so that a group of 128 is 16 adjacent lanes and an MX block 4.
 // The sum of squares (and in mode 2 the largest value) meets in LDS.  Codes are formed from y before
 // its rounding to the token type, by the functions dispatch uses.
+//
+// Bound by memory: 8192 tokens x 7168 with residual and a scale per 128 (530 MB) take 92 us, 5.8 TB/s (a
+// large copy 4.9, a large read 6.2); by latency: 2 tokens 4.1 us (4.8 with sums by
+// lane shuffles and a loop over the waves).
 #include "dc_quantize.h"
 #include "norm_internal.h"
 
@@ -20,16 +24,19 @@ __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
+// STREAM: past the caches.
+template <bool STREAM>
 __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint4 o)
 {
     const u32x4_t v = {o.x, o.y, o.z, o.w};
-    __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, STREAM ? kRsrcNonTemporal : 0);
 }
 
+template <bool STREAM>
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, uint2 o)
 {
     const u32x2_t v = {o.x, o.y};
-    __builtin_amdgcn_raw_buffer_store_b64(v, r, (int)off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(v, r, (int)off, 0, STREAM ? kRsrcNonTemporal : 0);
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&f)[8], bool f16)
@@ -100,7 +107,7 @@ __device__ __forceinline__ void store_mx_scale(const NormShape& s, void* scales,
                                                                                              : inverse_power(e);
 }
 
-template <int MODE, int CT, int SLOTS>
+template <int MODE, int CT, int SLOTS, bool STREAM>
 __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
 {
     __shared__ float sums[kWave];
@@ -142,7 +149,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
     if (a.residual_out) {
         const __amdgpu_buffer_rsrc_t so = rsrc(a.residual_out, row);
 #pragma unroll
-        for (int n = 0; n < SLOTS; ++n) store16(so, at[n], pack8(f[n], f16));
+        for (int n = 0; n < SLOTS; ++n) store16<STREAM>(so, at[n], pack8(f[n], f16));
     }
     const float rms = reciprocal_rms(s, squares);
 #pragma unroll
@@ -155,7 +162,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
     if (a.y) {
         const __amdgpu_buffer_rsrc_t yo = rsrc(a.y, row);
 #pragma unroll
-        for (int n = 0; n < SLOTS; ++n) store16(yo, at[n], pack8(f[n], f16));
+        for (int n = 0; n < SLOTS; ++n) store16<STREAM>(yo, at[n], pack8(f[n], f16));
     }
     if (MODE == 0) return;
 
@@ -173,7 +180,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
         float dyn, scale;
         group_dyn<CT>(peak, dyn, scale);
 #pragma unroll
-        for (int n = 0; n < SLOTS; ++n) store8(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
+        for (int n = 0; n < SLOTS; ++n) store8<STREAM>(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
         if (threadIdx.x == 0) static_cast<float*>(a.scales)[token] = scale;
     } else if (MODE == 3) {
 #pragma unroll
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
             const uint32_t peak = group_max_u32<kGroup / 8>(most[n]);
             float dyn, scale;
             group_dyn<CT>(peak, dyn, scale);
-            store8(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
+            store8<STREAM>(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
             if ((threadIdx.x & (kGroup / 8 - 1)) == 0 && at[n] < row)
                 static_cast<float*>(a.scales)[token * s.scales_per_row + at[n] / (2 * kGroup)] = scale;
         }
@@ -190,7 +197,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
         for (int n = 0; n < SLOTS; ++n) {
             const uint32_t peak = group_max_u32<kMxBlock / 8>(most[n]);
             const int e = shared_exp<MODE, CT>(peak);
-            store8(co, at[n] / 2, dynamic_codes8<CT>(f[n], inverse_power(e)));
+            store8<STREAM>(co, at[n] / 2, dynamic_codes8<CT>(f[n], inverse_power(e)));
             if ((threadIdx.x & (kMxBlock / 8 - 1)) == 0 && at[n] < row)
                 store_mx_scale(s, a.scales, token * s.scales_per_row + at[n] / (2 * kMxBlock), e,
                                peak >= 0x7F800000u);
@@ -270,8 +277,13 @@ __global__ __launch_bounds__(kAnyThreads) void norm_any_kernel(NormShape s, Norm
     }
 }
 
-// Few tokens: as many threads as vectors; many: four vectors a thread.
-constexpr int kSlotsMany = 2;
+// Few tokens: as many threads as vectors, many: two vectors a thread.  One and two, us, H = 7168: 2 tokens
+// 4.1 and 4.7, 512 8.3 and 8.6, 1024 14.4 and 13.1, 8192 102 and 95.
+constexpr int kManyTokens = 1024;
+// Elements from which the outputs pass the caches by: they would push out what is read next.  Norm,
+// logits and dispatch after each other with and without, us: 8192 tokens x 7168 198 and 202, 8192 x 2048
+// 73 and 77, but 1024 x 7168 55.5 and 53.6 (the norm alone: 92 and 95, 24.3 and 31.9, 11.7 and 13.1).
+constexpr int64_t kStreamElements = 12 << 20;
 
 template <int MODE, int CT>
 hipError_t launch(const NormShape& s, const NormArgs& a, bool vectorized, hipStream_t stream)
@@ -282,12 +294,13 @@ hipError_t launch(const NormShape& s, const NormArgs& a, bool vectorized, hipStr
         return hipGetLastError();
     }
     const int vectors = s.H / 8;
-    if (s.tokens < 1024) {
-        norm_kernel<MODE, CT, 1><<<grid, (vectors + kWave - 1) / kWave * kWave, 0, stream>>>(s, a);
-    } else {
-        const int threads = (vectors + kSlotsMany - 1) / kSlotsMany;
-        norm_kernel<MODE, CT, kSlotsMany><<<grid, (threads + kWave - 1) / kWave * kWave, 0, stream>>>(s, a);
-    }
+    const int threads = ((s.tokens < kManyTokens ? vectors : (vectors + 1) / 2) + kWave - 1) / kWave * kWave;
+    if (s.tokens < kManyTokens)
+        norm_kernel<MODE, CT, 1, false><<<grid, threads, 0, stream>>>(s, a);
+    else if ((int64_t)s.tokens * s.H < kStreamElements)
+        norm_kernel<MODE, CT, 2, false><<<grid, threads, 0, stream>>>(s, a);
+    else
+        norm_kernel<MODE, CT, 2, true><<<grid, threads, 0, stream>>>(s, a);
     return hipGetLastError();
 }
 

@@ -122,6 +122,11 @@ def test_many_tokens(mode, kind, fmt):
     _run(4, 300, 2056, mode, kind, fmt, seed=mode)
 
 
+@pytest.mark.parametrize("mode,kind,fmt", [VARIANTS[i] for i in (0, 1, 5, 7)])
+def test_outputs_past_the_caches(mode, kind, fmt):
+    _run(8, 300, 5256, mode, kind, fmt, seed=mode)
+
+
 @pytest.mark.parametrize("H,misalign", [(1025, False), (1157, False), (8191, False), (2048, True)])
 @pytest.mark.parametrize("mode,kind,fmt", VARIANTS)
 def test_any_size_and_alignment(mode, kind, fmt, H, misalign):
