@@ -137,8 +137,12 @@ hipError_t launch_grouped_matmul(const MatmulShape& s, const MatmulArgs& a, hipS
     case moe_dc::kMmE5m2: return moe_dc::launch_grouped_e5m2(s, a, stream);
     case moe_dc::kMmMxE4m3: return moe_dc::launch_grouped_mxe4m3(s, a, stream);
     case moe_dc::kMmMxE5m2: return moe_dc::launch_grouped_mxe5m2(s, a, stream);
-    case moe_dc::kMmBlockE4m3: return moe_dc::launch_grouped_block_e4m3(s, a, stream);
-    default: return moe_dc::launch_grouped_block_e5m2(s, a, stream);
+    case moe_dc::kMmBlockE4m3:
+        return s.out_code ? moe_dc::launch_grouped_coded_e4m3(s, a, stream)
+                          : moe_dc::launch_grouped_block_e4m3(s, a, stream);
+    default:
+        return s.out_code ? moe_dc::launch_grouped_coded_e5m2(s, a, stream)
+                          : moe_dc::launch_grouped_block_e5m2(s, a, stream);
     }
 }
 

@@ -54,6 +54,9 @@ hipError_t launch_grouped_mxe4m3(const MatmulShape& s, const MatmulArgs& a, hipS
 hipError_t launch_grouped_mxe5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_block_e4m3(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_block_e5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+// The same with coded results (out_code).
+hipError_t launch_grouped_coded_e4m3(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_grouped_coded_e5m2(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_matmul_w4(const MatmulShape& s, const MatmulArgs& a,
                                     hipStream_t stream);
 

@@ -159,13 +159,19 @@ __device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs
 // step k + 1 move from LDS to registers at the start of step k, and their place takes the weights
 // of step k + 3.  Loads past the end of a row return 0 without a memory access, so every step
 // issues the same number.
-template <int TYPE, int WAVES, int MT, bool SWIGLU>
+//
+// CODED (block): the results leave as codes.  What the fp8 instructions cut (1.5e-5 of a sum) would then
+// show as another code, a step of 6 to 25 %, in a few of 10 000 results, so tiles of up to 64 rows, which the
+// matrix units do not bound, form whole products (333 rows on 12 experts x 1136 x 1424, SwiGLU: 14.5 us
+// instead of 11.0).
+template <int TYPE, int WAVES, int MT, bool SWIGLU, bool CODED = false>
 __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulArgs& a,
                                              const Tile& tile, TileLds<TYPE, WAVES>& shared)
 {
     TileStages<TYPE, WAVES>& lds = shared.st;
     constexpr int kRows = kTileM<TYPE, WAVES>, kWeightRows = 32 * WAVES;
     constexpr int kScaleRows = TileStages<TYPE, WAVES>::kScaleRows;
+    constexpr bool kWhole = CODED && MT <= 4;
     const int e = tile.e, n0 = tile.n0, row0 = tile.row0, rows = tile.rows;
     typedef Mm<TYPE> M;
     typedef typename M::Acc Acc;
@@ -377,12 +383,13 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
                     for (int t = 0; t < 2; ++t) {
                         if (q > 0 || where == kFull) settle(q > 0 ? q - 1 : kGroups - 1, i, t);
                         if (q * 2 + i >= MT) continue;
-                        late[i][t] = M::mma(w[par][t], x[q & 1][i], Acc{0, 0, 0, 0}, 0, 0);
+                        if constexpr (kWhole) late[i][t] = M::mma_whole(w[par][t], x[q & 1][i]);
+                        else late[i][t] = M::mma(w[par][t], x[q & 1][i], Acc{0, 0, 0, 0}, 0, 0);
                         late_scale[i][t] = __int_as_float(wsc[par][t]) * __int_as_float(xsv[q & 1][i]);
                     }
                 // in turn: the additions that free a tile's place, its product
 #pragma unroll
-                for (int i = 0; i < 4 && q * 2 + i / 2 < MT; ++i) {
+                for (int i = 0; !kWhole && i < 4 && q * 2 + i / 2 < MT; ++i) {
                     __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 }
@@ -412,11 +419,9 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
 
     constexpr int kT = SWIGLU ? 1 : 2;
     const int c0 = wave * (kT * 16) + g * 4;    // the lane's first column
-    if constexpr (M::kBlk && WAVES * kT * 16 >= kBlock) {
-        if (s.out_code != 0) {
-            code_tile<TYPE, WAVES, MT, SWIGLU>(s, a, tile, half, left, acc, shared.amax);
-            return;
-        }
+    if constexpr (CODED) {
+        code_tile<TYPE, WAVES, MT, SWIGLU>(s, a, tile, half, left, acc, shared.amax);
+        return;
     }
     float ws_[2][4];
     if (M::kRowScaled) {
@@ -456,7 +461,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     }
 }
 
-template <int TYPE, bool SWIGLU>
+template <int TYPE, bool SWIGLU, bool CODED>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, MatmulArgs a)
 {
     constexpr int WAVES = kTileWaves;
@@ -466,26 +471,26 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
     if (!find_tile<kRows, SWIGLU ? kTileN / 2 : kTileN>(s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t))
         return;
     switch ((t.rows + 15) / 16) {
-    case 1: tile_product<TYPE, WAVES, 1, SWIGLU>(s, a, t, lds); break;
-    case 2: tile_product<TYPE, WAVES, 2, SWIGLU>(s, a, t, lds); break;
-    case 3: tile_product<TYPE, WAVES, 3, SWIGLU>(s, a, t, lds); break;
-    case 4: tile_product<TYPE, WAVES, 4, SWIGLU>(s, a, t, lds); break;
-    case 5: tile_product<TYPE, WAVES, 5, SWIGLU>(s, a, t, lds); break;
-    case 6: tile_product<TYPE, WAVES, 6, SWIGLU>(s, a, t, lds); break;
-    case 7: tile_product<TYPE, WAVES, 7, SWIGLU>(s, a, t, lds); break;
-    case 8: tile_product<TYPE, WAVES, 8, SWIGLU>(s, a, t, lds); break;
-    case 9: tile_product<TYPE, WAVES, 9, SWIGLU>(s, a, t, lds); break;
-    case 10: tile_product<TYPE, WAVES, 10, SWIGLU>(s, a, t, lds); break;
-    case 11: tile_product<TYPE, WAVES, 11, SWIGLU>(s, a, t, lds); break;
-    case 12: tile_product<TYPE, WAVES, 12, SWIGLU>(s, a, t, lds); break;
+    case 1: tile_product<TYPE, WAVES, 1, SWIGLU, CODED>(s, a, t, lds); break;
+    case 2: tile_product<TYPE, WAVES, 2, SWIGLU, CODED>(s, a, t, lds); break;
+    case 3: tile_product<TYPE, WAVES, 3, SWIGLU, CODED>(s, a, t, lds); break;
+    case 4: tile_product<TYPE, WAVES, 4, SWIGLU, CODED>(s, a, t, lds); break;
+    case 5: tile_product<TYPE, WAVES, 5, SWIGLU, CODED>(s, a, t, lds); break;
+    case 6: tile_product<TYPE, WAVES, 6, SWIGLU, CODED>(s, a, t, lds); break;
+    case 7: tile_product<TYPE, WAVES, 7, SWIGLU, CODED>(s, a, t, lds); break;
+    case 8: tile_product<TYPE, WAVES, 8, SWIGLU, CODED>(s, a, t, lds); break;
+    case 9: tile_product<TYPE, WAVES, 9, SWIGLU, CODED>(s, a, t, lds); break;
+    case 10: tile_product<TYPE, WAVES, 10, SWIGLU, CODED>(s, a, t, lds); break;
+    case 11: tile_product<TYPE, WAVES, 11, SWIGLU, CODED>(s, a, t, lds); break;
+    case 12: tile_product<TYPE, WAVES, 12, SWIGLU, CODED>(s, a, t, lds); break;
     default:
         if constexpr (kRows > 192) switch ((t.rows + 15) / 16) {
-            case 13: tile_product<TYPE, WAVES, 13, SWIGLU>(s, a, t, lds); break;
-            case 14: tile_product<TYPE, WAVES, 14, SWIGLU>(s, a, t, lds); break;
+            case 13: tile_product<TYPE, WAVES, 13, SWIGLU, CODED>(s, a, t, lds); break;
+            case 14: tile_product<TYPE, WAVES, 14, SWIGLU, CODED>(s, a, t, lds); break;
             default:
                 if constexpr (kRows > 224) {
-                    if ((t.rows + 15) / 16 == 15) tile_product<TYPE, WAVES, 15, SWIGLU>(s, a, t, lds);
-                    else tile_product<TYPE, WAVES, 16, SWIGLU>(s, a, t, lds);
+                    if ((t.rows + 15) / 16 == 15) tile_product<TYPE, WAVES, 15, SWIGLU, CODED>(s, a, t, lds);
+                    else tile_product<TYPE, WAVES, 16, SWIGLU, CODED>(s, a, t, lds);
                 }
                 break;
             }
@@ -494,7 +499,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(MatmulShape s, Ma
 }
 
 // Few rows per expert: tiles of at most kThinRows rows.
-template <int TYPE, bool SWIGLU>
+template <int TYPE, bool SWIGLU, bool CODED>
 __global__ __launch_bounds__(4 * kWave, 2) void thin_tile_kernel(MatmulShape s, MatmulArgs a)
 {
     constexpr int WAVES = 4;
@@ -502,32 +507,35 @@ __global__ __launch_bounds__(4 * kWave, 2) void thin_tile_kernel(MatmulShape s, 
     Tile t;
     if (!find_tile<kThinRows, SWIGLU ? kThinN / 2 : kThinN, WAVES>(s, a, SWIGLU ? s.out / 2 : s.out, lds.table, &t)) return;
     switch ((t.rows + 15) / 16) {
-    case 1: tile_product<TYPE, WAVES, 1, SWIGLU>(s, a, t, lds); break;
-    case 2: tile_product<TYPE, WAVES, 2, SWIGLU>(s, a, t, lds); break;
-    case 3: tile_product<TYPE, WAVES, 3, SWIGLU>(s, a, t, lds); break;
-    default: tile_product<TYPE, WAVES, 4, SWIGLU>(s, a, t, lds); break;
+    case 1: tile_product<TYPE, WAVES, 1, SWIGLU, CODED>(s, a, t, lds); break;
+    case 2: tile_product<TYPE, WAVES, 2, SWIGLU, CODED>(s, a, t, lds); break;
+    case 3: tile_product<TYPE, WAVES, 3, SWIGLU, CODED>(s, a, t, lds); break;
+    default: tile_product<TYPE, WAVES, 4, SWIGLU, CODED>(s, a, t, lds); break;
     }
 }
 
-template <int TYPE>
+template <int TYPE, bool CODED = false>
 hipError_t launch_thin_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
     const dim3 grid(tile_grid(s, kThinRows, s.swiglu ? kThinN / 2 : kThinN));
-    if (s.swiglu)
-        thin_tile_kernel<TYPE, true><<<grid, 4 * kWave, 0, stream>>>(s, a);
-    else
-        thin_tile_kernel<TYPE, false><<<grid, 4 * kWave, 0, stream>>>(s, a);
+    if constexpr (!CODED) {                      // (thin tiles do not hold whole groups of gate and up)
+        if (s.swiglu) {
+            thin_tile_kernel<TYPE, true, false><<<grid, 4 * kWave, 0, stream>>>(s, a);
+            return hipGetLastError();
+        }
+    }
+    thin_tile_kernel<TYPE, false, CODED><<<grid, 4 * kWave, 0, stream>>>(s, a);
     return hipGetLastError();
 }
 
-template <int TYPE>
+template <int TYPE, bool CODED = false>
 hipError_t launch_tiles(const MatmulShape& s, const MatmulArgs& a, hipStream_t stream)
 {
     const dim3 grid(tile_grid(s, tile_rows(TYPE), s.swiglu ? kTileN / 2 : kTileN));
     if (s.swiglu)
-        tile_kernel<TYPE, true><<<grid, kTileThreads, 0, stream>>>(s, a);
+        tile_kernel<TYPE, true, CODED><<<grid, kTileThreads, 0, stream>>>(s, a);
     else
-        tile_kernel<TYPE, false><<<grid, kTileThreads, 0, stream>>>(s, a);
+        tile_kernel<TYPE, false, CODED><<<grid, kTileThreads, 0, stream>>>(s, a);
     return hipGetLastError();
 }
 

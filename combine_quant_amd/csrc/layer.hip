@@ -276,7 +276,7 @@ __global__ __launch_bounds__(WAVES * kWave) void up_kernel(LayerShape s, LayerAr
     const int l16 = lane & 15, g = lane >> 4;
     UpNotes& notes = all_notes[wave];
     const int j = blockIdx.y;
-    extern __shared__ char picks[];             // ids, then weights
+    extern __shared__ __align__(16) char picks[];            // ids, then weights
     int* ids = reinterpret_cast<int*>(picks);
     float* weights = reinterpret_cast<float*>(ids + s.T * s.K);
     const Slot slot = find_slot(s, a, j, notes, ids, weights);

@@ -449,7 +449,8 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
  *   codes          bytes [cap][M]
  *   out_scales     fp32 [cap][Ceil(M, 128)]
  * Rows at or past recv_offsets[W] are not written.  Numerics and errors as for
- * moe_grouped_matmul. */
+ * moe_grouped_matmul, but where an expert's rows fill no tile of more than 64 nothing is dropped of the
+ * products, since what is dropped shows as another code now and then. */
 moe_status moe_grouped_matmul_quantize(const moe_dc_config* cfg, const moe_matmul* mm,
                                        int32_t out_dtype, const void* x, const float* x_scales,
                                        const void* weight, const float* weight_scales,
@@ -586,9 +587,9 @@ size_t moe_dc_experts_layer_workspace_bytes(const moe_dc_config* cfg, const moe_
  * Numerics: products of token values and codes are exact (the tokens are not quantized); sums are
  * fp32 in an order that depends on the sizes and ids only; _BLOCK sums the products of a block,
  * multiplies by its scale and adds; SwiGLU as for moe_grouped_matmul.  w * h is rounded to the token
- * type between the two products (w is the sum of the weights where a token picked an expert more
- * than once) and y once at the end.  An infinity or NaN in a weight reaches only the tokens that
- * picked its expert.
+ * type between the two products (fp16: to infinity past 65504; w is the sum of the weights where a
+ * token picked an expert more than once) and y once at the end.  An infinity or NaN in a weight
+ * reaches only the tokens that picked its expert.
  * Errors: MOE_ERR_UNSUPPORTED for more than 64 tokens; y or the workspace overlapping an input is
  * MOE_ERR_INVALID_ARG; otherwise as for moe_dispatch.  Picks with ids out of range count as
  * inactive. */

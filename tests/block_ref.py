@@ -52,5 +52,5 @@ def check_codes(codes, scales, y, err, kind, rows):
     assert (diff <= tol).all(), (int((diff > tol).sum()), float((diff / tol).nan_to_num().max()))
 
 
-def product(x, xs, w, ws, ranges, swiglu):
-    return ref.product(rows_f64(x, xs), weights_f64(w, ws, 2 if swiglu else 1), ranges, swiglu, cut=True)
+def product(x, xs, w, ws, ranges, swiglu, cut=True):
+    return ref.product(rows_f64(x, xs), weights_f64(w, ws, 2 if swiglu else 1), ranges, swiglu, cut=cut)

@@ -33,7 +33,7 @@ def _desc(kind, I, N, swiglu):
                           activation=cq.MOE_ACT_SWIGLU if swiglu else cq.MOE_ACT_NONE)
 
 
-def _case(kind, W, counts, I, N, swiglu, seed, f16=False):
+def _case(kind, W, counts, I, N, swiglu, seed, f16=False, cut=True):
     """Config, descriptor, tensors and the 64-bit result with its bound.  Results near 1."""
     g = torch.Generator(device=DEV)
     g.manual_seed(seed)
@@ -48,7 +48,7 @@ def _case(kind, W, counts, I, N, swiglu, seed, f16=False):
         60 * math.sqrt(I))
     x.view(torch.uint8)[rows:] = 0x7F                      # NaN behind the last row
     xs[rows:] = math.nan
-    y, err = blk.product(x[:rows], xs[:rows], w, ws, ranges, swiglu)
+    y, err = blk.product(x[:rows], xs[:rows], w, ws, ranges, swiglu, cut)
     return cfg, _desc(kind, I, N, swiglu), x, xs, w, ws, erc.to(DEV), off.to(DEV), y, err
 
 
@@ -64,7 +64,8 @@ def _run(kind, W, counts, I, N, swiglu, seed=0, f16=False):
 
 
 def _run_codes(kind, to, W, counts, I, N, swiglu, seed=0):
-    cfg, mm, x, xs, w, ws, erc, off, y, err = _case(kind, W, counts, I, N, swiglu, seed)
+    # up to 64 rows a tile the products are whole
+    cfg, mm, x, xs, w, ws, erc, off, y, err = _case(kind, W, counts, I, N, swiglu, seed, cut=max(counts) > 64)
     rows, M = sum(counts), y.shape[1]
     codes = torch.full((cfg.expand_rows_capacity, M), 0x55, device=DEV, dtype=torch.uint8)
     scales = torch.full((cfg.expand_rows_capacity, blk.groups(M)), 7.25, device=DEV)
