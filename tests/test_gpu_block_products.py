@@ -133,6 +133,30 @@ def test_every_tile_height(coded):
         _run("e4m3", 2, counts, 400, 256, True, seed=1)
 
 
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("E", [130, 512, 1024])
+def test_thin_tiles_of_many_experts(E, coded):
+    counts = [0] * E
+    for e in range(0, E, E // 36):
+        counts[e] = 1 + e % 3
+    counts[E - 1] = 70
+    cfg = _config(2, counts)
+    N = 128
+    assert experts_path.path("block_e4m3", cfg, N, False) == "thin"
+    if coded:
+        _run_codes("e4m3", "e5m2", 2, counts, 272, N, False, seed=E)
+    else:
+        _run("e4m3", 2, counts, 272, N, False, seed=E)
+
+
+@pytest.mark.parametrize("I,N,swiglu,counts", [
+    (65536, 40, False, [3, 0, 1, 2]), (65536, 300, True, [0, 40, 200, 70]), (16, 65536, False, [1, 0, 2, 0]),
+    (48, 65536, True, [30, 0, 0, 65]), (32768, 1024, False, [9, 8, 7, 0])])
+def test_largest_sizes(I, N, swiglu, counts):
+    _run("e4m3", 2, counts, I, N, swiglu, seed=3)
+    _run_codes("e4m3", "e4m3", 2, counts, I, N, swiglu, seed=3)
+
+
 def _exact_case(counts, I, N, seed):
     """Small whole codes and scales that are powers of two: every sum is exact in fp32."""
     g = torch.Generator(device=DEV)

@@ -126,6 +126,12 @@ def test_the_most_tokens(E, K, H, block):
     Case(2, 32, E, K, H, 16, block, seed=E).check_exact()
 
 
+@pytest.mark.parametrize("block", [False, True])
+@pytest.mark.parametrize("H,F", [(1024, 32768), (8192, 4096)])
+def test_largest_sizes(H, F, block):
+    Case(2, 4, 2, 2, H, F, block, seed=1).check_exact()
+
+
 def test_ids_out_of_range_count_as_inactive():
     c = Case(2, 3, 8, 4, 1024, 64, seed=3)
     c.ids[0, 1] = torch.tensor([-1, 8, 2 ** 31 - 1, -2 ** 31], device=DEV)

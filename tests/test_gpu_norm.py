@@ -139,6 +139,23 @@ def test_epsilon_counts(eps, H):
     _run(2, 2, H, 3, eps=eps, spread=2.0 ** -12)
 
 
+def test_the_largest_batch():
+    """768 x 512 tokens of 8192: offsets past 32 bits."""
+    cfg = _config(768, 512, 8192, 3, "e4m3")
+    x = torch.zeros((768, 512, 8192), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    few = torch.randn((2, 512, 8192), generator=g, device=DEV).bfloat16()
+    x[0], x[767] = few[0], few[1]
+    gamma = torch.randn((8192,), generator=g, device=DEV).bfloat16()
+    out = cq.rms_norm(cfg, cq.make_norm(), x, gamma)
+    torch.cuda.synchronize()
+    _, y = _plain(few, None, gamma, 1e-6)
+    _near(out["y"][[0, 767]], y, REL)
+    _check_codes(cfg, "e4m3", out["codes"][[0, 767]], out["dynamic_scales"][[0, 767]], y)
+    assert (out["y"][1:767] == 0).all() and (out["dynamic_scales"][1:767] == 0).all()
+
+
 def test_repeats_its_bytes():
     cfg = _config(3, 500, 1152, 3, "e4m3")
     x, r, gamma = _inputs(cfg, True, 1)
