@@ -6,8 +6,9 @@
 // experts x 7168 x 4096 bf16 take 306 us, 6.2 TB/s, a read's rate on this chip.  Many rows are
 // bound by the matrix units at the clock they leave: 16384 rows on 8 experts x 7168 x 4096 run in
 // 737 us in bf16 (1310 Tflop/s), 775 in fp16, 392 in E4M3 (2450), 404 in int8, 461 in MX E4M3, 470
-// to 490 in block-scaled E4M3 (their scaled additions take as many vector cycles as the products matrix
-// cycles; three of four left out give 8 %), with the matrix units busy 72 % of a workgroup's time at 1.76 GHz (bf16).  Without its loads the loop takes 0.60 ms of the 0.74, without its products
+// to 490 in block-scaled E4M3 (whose scaled additions take as many vector cycles as the products
+// matrix cycles; three of four left out give 8 %), with the matrix units busy 72 % of a workgroup's
+// time at 1.76 GHz (bf16).  Without its loads the loop takes 0.60 ms of the 0.74, without its products
 // 0.56; without the barrier 3 % less, without the waits for loads no less.
 //
 // Also tried at that size: both operands in two stages with one barrier a step (0.99 ms against
