@@ -475,10 +475,10 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
     Place ahead = {first / chunks, first % chunks};
     Slot next = {0, 0, 0, 0};
     int held = -1;                              // the slot that `next` describes
-    int filled = 0;                             // units asked for
+    int filled = 0;                             // fills asked for
     const auto fill = [&](int d) {
-        const bool there = filled++ < units;
-        if (there && held != ahead.slot) {
+        if (filled++ >= units) return;
+        if (held != ahead.slot) {
             next = slot_at(ahead.slot);
             held = ahead.slot;
         }
@@ -488,10 +488,10 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
             const int left = s.H - n0 - t * 16 < 16 ? s.H - n0 - t * 16 : 16;
             wr[t] = make_rsrc(static_cast<const char*>(a.down) +
                                   ((size_t)next.expert * s.H + n0 + t * 16) * row_bytes,
-                              there && left > 0 ? (uint32_t)left * row_bytes : 0);
+                              left > 0 ? (uint32_t)left * row_bytes : 0);
         }
         const __amdgpu_buffer_rsrc_t hr =
-            make_rsrc(h + (size_t)next.first * h_bytes, there ? (uint32_t)next.rows * h_bytes : 0);
+            make_rsrc(h + (size_t)next.first * h_bytes, (uint32_t)next.rows * h_bytes);
         uint32_t xoff[S::kXLoads];
 #pragma unroll
         for (int i = 0; i < S::kXLoads; ++i)
@@ -541,29 +541,31 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
     while (unit < units) {
 #pragma unroll
         for (int d = 0; d < kRing; ++d) {
+            if (unit >= units) break;
             typename S::Regs r;
-            wait_loads<(kRing - 1) * S::kLoads>();
+            // no fetch is sent past the last unit (12.5 -> 12.0 us on a small layer, 164 -> 162 on a larger
+            // one), and with none behind this unit's there is nothing to leave in flight
+            if (unit + 1 < units) wait_loads<S::kLoads>();
+            else wait_loads<0>();
             S::read(ring + d * S::kBytes, r);
             float sc = 0.0f;
             if (BLOCK) sc = scales[unit & (2 * kWave - 1)];
             wait_lds();
             if (BLOCK && (unit & (kWave - 1)) == 0) fetch_scales(unit / kWave + 1);
             fill(d);
-            if (unit < units) {
-                if (now.slot != open) {
-                    flush(open);
-                    open = now.slot;
-                }
-#pragma unroll
-                for (int m = 0; m < S::kTiles; ++m)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if constexpr (BLOCK)
-                            add_scaled(acc[m][t], S::mma(r.w[t], r.x[m], v4f_t{0, 0, 0, 0}), sc);
-                        else
-                            acc[m][t] = S::mma(r.w[t], r.x[m], acc[m][t]);
-                    }
+            if (now.slot != open) {
+                flush(open);
+                open = now.slot;
             }
+#pragma unroll
+            for (int m = 0; m < S::kTiles; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if constexpr (BLOCK)
+                        add_scaled(acc[m][t], S::mma(r.w[t], r.x[m], v4f_t{0, 0, 0, 0}), sc);
+                    else
+                        acc[m][t] = S::mma(r.w[t], r.x[m], acc[m][t]);
+                }
             now = step(now);
             ++unit;
         }
