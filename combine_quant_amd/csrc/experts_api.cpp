@@ -430,7 +430,7 @@ moe_status moe_experts_layer(const moe_dc_config* cfg, const moe_experts* expert
     char* ws = static_cast<char*>(workspace);
     const moe_dc::LayerArgs a{x, expert_ids, expert_scales, x_active_mask, up, up_scales, down, down_scales,
                               shared_x, y, reinterpret_cast<moe_dc::Slot*>(ws),
-                              reinterpret_cast<int32_t*>(ws + moe_dc::layer_tokens_offset(s)),
+                              reinterpret_cast<moe_dc::Row*>(ws + moe_dc::layer_rows_offset(s)),
                               ws + moe_dc::layer_h_offset(s)};
     return launched(moe_dc::launch_experts_layer(s, a, static_cast<hipStream_t>(stream)),
                     "experts' layer launch");

@@ -8,11 +8,17 @@
 // barrier holds the stream up.
 //
 //   up:   one workgroup per (expert with tokens, 16 columns): the waves take chunks of the inner
-//         dimension in turn; gate and up rows, SwiGLU and the pick's weight, h in the token type.
+//         dimension in turn; gate and up rows, SwiGLU, h in the token type.
 //         Every wave finds its expert and its tokens in the ids by itself, one lane a token.
 //   down: one workgroup per 16 or 32 columns of y: the waves take the chunks of all experts in turn;
-//         an expert's sums are added to its tokens' in LDS, and the waves' in the end, in an order
-//         that depends on the ids only.
+//         an expert's sums are added to its tokens' in LDS, times the pick's weight, and the waves' in
+//         the end, in an order that depends on the ids only.
+//
+// h is rounded to the token type as separate calls round it, so that both ways agree and the down kernel
+// takes h as it lies as a matrix operand.  It and y's own rounding make the result sqrt(2) further from
+// 64 bits than y's alone (bf16 0.0024 against 0.0017, fp16 0.00029 against 0.00020).  A weight multiplies
+// fp32 sums: in fp16 a small one would push h among the subnormals (w 0.01, h 1e-4: an error of 0.017),
+// a large one past 65504.
 //
 // Bound by HBM: 32 tokens on 256 experts x 7168 x 2048 E4M3 (7.2 GB) take 1.17 to 1.21 ms, 6.1 TB/s, a
 // read's rate; 1 token on 8 experts bf16 (0.70 GB) 122 us, 5.8 TB/s.  By latency: 5 tokens on 8 experts x
@@ -167,7 +173,6 @@ struct UpNotes {
     uint32_t present[kMaxIds / 32];             // experts with tokens
     uint32_t who[kLayerTokens / 32];            // tokens of the wave's expert
     int token[kLayerTokens];                    // the same in ascending order
-    float weight[kLayerTokens];
     float scales[2][kMaxChunks];                // of the gate's and the up rows' block
 };
 
@@ -183,8 +188,8 @@ __device__ __forceinline__ int scan32(int v)
 }
 
 // The expert of slot j (the j-th of those that have tokens, by id) and its tokens in ascending order.
-// A lane holds every 64th pick.  The picks' ids (-1: inactive) and weights are left in LDS; all waves
-// of a workgroup write the same there, and each reads what it wrote.
+// A lane holds every 64th pick.  The picks' ids (-1: inactive) and weights are left in LDS for
+// sum_weights; all waves of a workgroup write the same there, and one that reads them has written them.
 __device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& a, int j, UpNotes& notes,
                                           int* ids, float* weights)
 {
@@ -255,17 +260,18 @@ __device__ __forceinline__ Slot find_slot(const LayerShape& s, const LayerArgs& 
     return slot;
 }
 
-// The sum, in the picks' order, of the weights with which each of the slot's tokens chose its expert.
-__device__ __forceinline__ void sum_weights(const LayerShape& s, const Slot& slot, const int* ids,
-                                            const float* weights, UpNotes& notes)
+// The sum, in the picks' order, of the weights with which each of the slot's tokens (a lane each) chose
+// its expert.
+__device__ __forceinline__ float sum_weights(const LayerShape& s, const Slot& slot, const int* ids,
+                                             const float* weights, const UpNotes& notes)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    if (lane >= slot.rows) return;
-    const int p0 = notes.token[lane] * s.K;
     float total = 0.0f;
+    if (lane >= slot.rows) return total;
+    const int p0 = notes.token[lane] * s.K;
     for (int k = 0; k < s.K; ++k)
         if (ids[p0 + k] == slot.expert) total += weights[p0 + k];
-    notes.weight[lane] = total;
+    return total;
 }
 
 // RP: rows of an expert that share a sweep over its weights.
@@ -286,10 +292,8 @@ __global__ __launch_bounds__(WAVES * kWave) void up_kernel(LayerShape s, LayerAr
     int* ids = reinterpret_cast<int*>(picks);
     float* weights = reinterpret_cast<float*>(ids + s.T * s.K);
     const Slot slot = find_slot(s, a, j, notes, ids, weights);
-    if (blockIdx.x == 0 && wave == 0) {
-        if (lane == 0) a.slots[j] = slot;
-        if (lane < slot.rows) a.tokens[slot.first + lane] = notes.token[lane];
-    }
+    const bool writes = blockIdx.x == 0 && wave == 0;        // the slot and its rows
+    if (writes && lane == 0) a.slots[j] = slot;
     if (slot.expert < 0) return;
     const int n0 = blockIdx.x * 16;
     const uint32_t row_bytes = (uint32_t)s.H * (BLOCK ? 1 : 2);
@@ -323,7 +327,10 @@ __global__ __launch_bounds__(WAVES * kWave) void up_kernel(LayerShape s, LayerAr
         for (int m = 0; m < kRows; ++m) acc[m][0] = acc[m][1] = v4f_t{0, 0, 0, 0};
 #pragma unroll
         for (int d = 0; d < kRing; ++d) S::fill(ring[wave][d], wr, xr, row_bytes, xoff, turn(wave + d * WAVES));
-        if (r0 == 0) sum_weights(s, slot, ids, weights, notes);
+        if (r0 == 0 && writes) {
+            const float weight = sum_weights(s, slot, ids, weights, notes);
+            if (lane < slot.rows) a.rows[slot.first + lane] = Row{notes.token[lane], weight};
+        }
         for (int c = wave; c < chunks; c += kRing * WAVES) {
 #pragma unroll
             for (int d = 0; d < kRing; ++d) {
@@ -373,20 +380,18 @@ __global__ __launch_bounds__(WAVES * kWave) void up_kernel(LayerShape s, LayerAr
             const int row = r0 + m * 16 + l16;
             if (m * 16 + l16 >= RP || row >= slot.rows) continue;
             silu_mul4(r[0], r[1], r[0]);
-            const float weight = notes.weight[row];
             uint16_t* o = static_cast<uint16_t*>(a.h) + (size_t)(slot.first + row) * s.F + n0 + g * 4;
             if (g * 4 < left)                   // F is a multiple of 8
-                *reinterpret_cast<uint2*>(o) = make_uint2(pack_out2(r[0][0] * weight, r[0][1] * weight, F16),
-                                                          pack_out2(r[0][2] * weight, r[0][3] * weight, F16));
+                *reinterpret_cast<uint2*>(o) = make_uint2(pack_out2(r[0][0], r[0][1], F16), pack_out2(r[0][2], r[0][3], F16));
         }
         if (r0 + RP < slot.rows) __syncthreads();            // before the rings are filled again
     }
 }
 
 // Dynamic LDS of down_kernel after its rings: sums [wave][token][column], the slots cut to RP rows,
-// the rows' tokens, scales [wave][2][64 units].
+// the rows' tokens and weights, scales [wave][2][64 units].
 struct DownLds {
-    size_t ring, sums, slots, tokens, scales;
+    size_t ring, sums, slots, rows, scales;
 };
 __host__ __device__ inline DownLds down_lds(const LayerShape& s, int waves, int stages, int cols, int rp)
 {
@@ -394,7 +399,7 @@ __host__ __device__ inline DownLds down_lds(const LayerShape& s, int waves, int 
     l.ring = (size_t)waves * stages;
     l.sums = (size_t)waves * s.T * cols * 4;
     l.slots = ((size_t)s.slots + (s.T > rp ? s.T * s.K / rp : 0)) * sizeof(Slot);
-    l.tokens = (size_t)s.T * s.K * 4;
+    l.rows = (size_t)s.T * s.K * sizeof(Row);
     l.scales = s.block ? (size_t)waves * 2 * kWave * 4 : 0;
     return l;
 }
@@ -414,8 +419,8 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
     char* ring = lds + (size_t)wave * kRing * S::kBytes;
     float* sums = reinterpret_cast<float*>(lds + parts.ring);
     Slot* slots = reinterpret_cast<Slot*>(lds + parts.ring + parts.sums);
-    int* tokens = reinterpret_cast<int*>(lds + parts.ring + parts.sums + parts.slots);
-    float* scales = reinterpret_cast<float*>(lds + parts.ring + parts.sums + parts.slots + parts.tokens) +
+    Row* rows = reinterpret_cast<Row*>(lds + parts.ring + parts.sums + parts.slots);
+    float* scales = reinterpret_cast<float*>(lds + parts.ring + parts.sums + parts.slots + parts.rows) +
                     wave * 2 * kWave;
     // The first wave cuts the slots to at most RP rows each.
     if (wave == 0) {
@@ -440,7 +445,7 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
         }
         if (lane == 0) count_lds = count;
     }
-    for (int i = threadIdx.x; i < s.T * s.K; i += kThreads) tokens[i] = a.tokens[i];
+    for (int i = threadIdx.x; i < s.T * s.K; i += kThreads) rows[i] = a.rows[i];
     for (int i = threadIdx.x; i < WAVES * s.T * kCols; i += kThreads) sums[i] = 0.0f;
     __syncthreads();
     const int count = __builtin_amdgcn_readfirstlane(count_lds);
@@ -519,18 +524,22 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
     };
     clear();
     float* mine = sums + wave * s.T * kCols;
-    // Adds an expert's sums to those of its tokens.
+    // Adds an expert's sums, times the weights, to those of its tokens.
     const auto flush = [&](int i) {
         const Slot slot = slot_at(i);
 #pragma unroll
         for (int m = 0; m < S::kTiles; ++m) {
             const int row = m * 16 + l16;
-            if (row < slot.rows)
+            if (row < slot.rows) {
+                const Row r = rows[slot.first + row];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    v4f_t* to = reinterpret_cast<v4f_t*>(mine + tokens[slot.first + row] * kCols + t * 16 + g * 4);
-                    *to = *to + acc[m][t];
+                    v4f_t* to = reinterpret_cast<v4f_t*>(mine + r.token * kCols + t * 16 + g * 4);
+                    v4f_t sum = *to;
+                    add_scaled(sum, acc[m][t], r.weight);
+                    *to = sum;
                 }
+            }
         }
         clear();
     };
@@ -595,7 +604,7 @@ template <bool F16, bool BLOCK, int NT, int RP, int WAVES>
 hipError_t launch_down(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
 {
     const DownLds l = down_lds(s, WAVES, kRing * Stage<F16, BLOCK, NT, RP>::kBytes, NT * 16, RP);
-    const size_t bytes = l.ring + l.sums + l.slots + l.tokens + l.scales;
+    const size_t bytes = l.ring + l.sums + l.slots + l.rows + l.scales;
     down_kernel<F16, BLOCK, NT, RP, WAVES><<<(unsigned)((s.H + NT * 16 - 1) / (NT * 16)), WAVES * kWave, bytes,
                                              stream>>>(s, a);
     return hipGetLastError();

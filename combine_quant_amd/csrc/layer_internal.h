@@ -22,13 +22,18 @@ struct LayerShape {
     int32_t slots;           // experts that can have tokens: min(E, T * K)
 };
 
-// Workspace: one Slot per expert that can have tokens; one int32 per pick, the token of each row of
-// h; h in the token type, [T * K][F].  Every part is written before it is read in the same call.
+// Workspace: one Slot per expert that can have tokens; one Row per pick, of each row of h; h in the
+// token type, [T * K][F].  Every part is written before it is read in the same call.
 struct Slot {
     int32_t expert;          // -1: no more experts
     int32_t first;           // its first row of h
     int32_t rows;
     int32_t unused;
+};
+
+struct Row {
+    int32_t token;
+    float weight;            // with which the token chose the expert
 };
 
 struct LayerArgs {
@@ -43,14 +48,14 @@ struct LayerArgs {
     const void* shared;          // null: none
     void* y;
     Slot* slots;                 // the workspace's parts
-    int32_t* tokens;
+    Row* rows;
     void* h;
 };
 
-inline size_t layer_tokens_offset(const LayerShape& s) { return round256((size_t)s.slots * sizeof(Slot)); }
+inline size_t layer_rows_offset(const LayerShape& s) { return round256((size_t)s.slots * sizeof(Slot)); }
 inline size_t layer_h_offset(const LayerShape& s)
 {
-    return layer_tokens_offset(s) + round256((size_t)s.T * s.K * sizeof(int32_t));
+    return layer_rows_offset(s) + round256((size_t)s.T * s.K * sizeof(Row));
 }
 inline size_t layer_workspace_bytes(const LayerShape& s)
 {
