@@ -88,6 +88,15 @@ __device__ __forceinline__ float reciprocal_rms(const NormShape& s, float square
     return 1.0f / __builtin_sqrtf(squares / (float)s.H + s.epsilon);
 }
 
+// A dynamic scale pair from the largest value's bits, as dispatch forms it; the scale of values with an
+// infinity or NaN among them is NaN (dyn is 0 or NaN then, and with it every code).
+template <int CT>
+__device__ __forceinline__ void dynamic_scale(uint32_t peak, float& dyn, float& scale)
+{
+    group_dyn<CT>(peak, dyn, scale);
+    if (peak >= 0x7F800000u) scale = NAN;
+}
+
 // Shared exponent of an MX block, 0 where it holds an infinity or NaN.
 template <int MODE, int CT>
 __device__ __forceinline__ int shared_exp(uint32_t peak)
@@ -178,7 +187,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
         for (int n = 1; n < SLOTS; ++n) peak = dpp_max(peak, most[n]);
         peak = block_max(peak, peaks);
         float dyn, scale;
-        group_dyn<CT>(peak, dyn, scale);
+        dynamic_scale<CT>(peak, dyn, scale);
 #pragma unroll
         for (int n = 0; n < SLOTS; ++n) store8<STREAM>(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
         if (threadIdx.x == 0) static_cast<float*>(a.scales)[token] = scale;
@@ -187,7 +196,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
         for (int n = 0; n < SLOTS; ++n) {
             const uint32_t peak = group_max_u32<kGroup / 8>(most[n]);
             float dyn, scale;
-            group_dyn<CT>(peak, dyn, scale);
+            dynamic_scale<CT>(peak, dyn, scale);
             store8<STREAM>(co, at[n] / 2, dynamic_codes8<CT>(f[n], dyn));
             if ((threadIdx.x & (kGroup / 8 - 1)) == 0 && at[n] < row)
                 static_cast<float*>(a.scales)[token * s.scales_per_row + at[n] / (2 * kGroup)] = scale;
@@ -250,7 +259,7 @@ __global__ __launch_bounds__(kAnyThreads) void norm_any_kernel(NormShape s, Norm
     if (MODE == 2) {
         peak = block_max(peak, peaks);
         float dyn, scale;
-        group_dyn<CT>(peak, dyn, scale);
+        dynamic_scale<CT>(peak, dyn, scale);
         for (int i = threadIdx.x; i < s.H; i += kAnyThreads) code(i, dyn);
         if (threadIdx.x == 0) static_cast<float*>(a.scales)[token] = scale;
         return;
@@ -263,7 +272,7 @@ __global__ __launch_bounds__(kAnyThreads) void norm_any_kernel(NormShape s, Norm
         for (int i = lo; i < hi; ++i) most = dpp_max(most, __float_as_uint(y[i]) & 0x7FFFFFFFu);
         if (MODE == 3) {
             float dyn, scale;
-            group_dyn<CT>(most, dyn, scale);
+            dynamic_scale<CT>(most, dyn, scale);
             for (int i = lo; i < hi; ++i) code(i, dyn);
             static_cast<float*>(a.scales)[at] = scale;
         } else if (lo >= s.H) {
