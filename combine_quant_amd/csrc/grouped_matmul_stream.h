@@ -163,6 +163,9 @@ __device__ __forceinline__ void stream_tile(const MatmulShape& s, const MatmulAr
     __syncthreads();
 }
 
+// Two workgroups a CU: without the bound block kinds take 269 registers a lane, which leaves one (333
+// rows on 12 experts x 1136 x 777: 8.6 us, 7.5 with it); the other types take 202 to 256 either way and
+// their times differ by less than 1 % (bf16, fp16, int8, E4M3, E5M2, MX; 2 to 60 rows an expert).
 template <int TYPE>
 __global__ __launch_bounds__(kStreamWaves * kWave, 2) void stream_kernel(MatmulShape s, MatmulArgs a)
 {
@@ -177,8 +180,11 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 2) void stream_kernel(MatmulS
         for (int row = begin + blockIdx.z * MT * 16; row < end; row += gridDim.z * MT * 16) {
             const int rows = end - row;
             // Up to two chunks a wave are all in flight with two stages, and four would only ask for
-            // zeros past the end (1024 inner, 8 rows to an expert: 5.7 us with four, 5.2 with two).
-            if (rows <= 16 && Mm<TYPE>::kBlk && s.in <= 2 * 128 * kStreamWaves)
+            // zeros past the end (1024 inner, 8 rows to an expert, with four and with two: block 5.7 and
+            // 5.2 us, int8 and row-scaled fp8 6.3 and 5.7, MX 6.4 and 5.3).  Not for tokens: 512 of them
+            // would gain as much (bf16 5.0 and 4.4), but with a fourth form of the tile in the kernel
+            // 1024, the least hidden size, lose 2 % (6.06 and 6.15).
+            if (rows <= 16 && Mm<TYPE>::kBytes == 1 && s.in <= 2 * 128 * kStreamWaves)
                 stream_tile<TYPE, 1, NT, 2>(s, a, e, n0, row, rows, lds);
             else if (rows <= 16)
                 stream_tile<TYPE, 1, NT, 4>(s, a, e, n0, row, rows, lds);
