@@ -60,3 +60,25 @@ def test_current_stream_goes_on_allocating(make, planned):
         torch.cuda.synchronize()
         assert torch.equal(y, want)
         del held
+
+
+@pytest.mark.parametrize("make", [_layer, _scatter])
+def test_captured_plan_with_its_own_workspace(make):
+    call, plan, n = make()
+    want = call(None, None)
+    y = torch.zeros_like(want)
+    launch, s, graph = plan(y), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        launch()
+    for _ in range(4):
+        y.zero_()
+        graph.replay()
+        held = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        y.zero_()
+        launch()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        del held
