@@ -53,6 +53,12 @@ constexpr int kW4TileLeast = 80;
 // Streaming for up to 32 rows an expert and fewer than 96 thin tiles: 64 of them (16 x 20 rows, 7168 x
 // 512) 19.3, 22.0, 29.5, (64 x 2 rows, 1024 x 128) 5.6, 6.3, 7.8; 128 (16 x 20 rows, 7168 x 1024) 32.0, 22.9,
 // 30.2, (64 x 4 rows, 2048 x 256) 9.6, 8.7, 11.2; with 64 rows 16 thin tiles (8 experts, 1024 x 256) 10.6, 7.8, 11.1.
+// The rule knows the mean alone.  us with uniform experts, with weights of 1 / rank and with one expert that
+// every token picks: 16384 rows on 32 x 7168 x 4096 SwiGLU (582, 1908, 2048 rows at most) 560, 572, 569; 8192
+// on 256 x 7168 x 4096 SwiGLU (50, 814, 1024) 1253, 1271, 1290; 1024 on 64 x 4096 x 1024 SwiGLU (23, 116, 128)
+// 42, 48, 49; 512 on 64 x 2048 x 512 (16, 91, 128) 13.1, 14.4, 15.0.  Worst near an edge: 4096 on 64 x 2048 x
+// 1024 (84, 467, 512) 27, 45, 37 in the large tiles it takes, 31, 34, 30 in thin ones; 128 on 8 x 2048 x 1024
+// (21, 36, 64) 7.3, 9.8, 11.7 streamed, 8.6, 9.8, 10.6 in thin ones.
 constexpr int kBlockTileLeast = 192;
 constexpr int kThinLeast = 96;
 constexpr int kBlockStreamRows = 32;

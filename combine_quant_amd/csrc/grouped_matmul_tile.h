@@ -8,7 +8,8 @@
 // 737 us in bf16 (1310 Tflop/s), 775 in fp16, 392 in E4M3 (2450), 404 in int8, 461 in MX E4M3, 470
 // to 490 in block-scaled E4M3 (whose scaled additions take as many vector cycles as the products
 // matrix cycles; three of four left out give 8 %), with the matrix units busy 72 % of a workgroup's
-// time at 1.76 GHz (bf16).  Without its loads the loop takes 0.60 ms of the 0.74, without its products
+// time at 1.76 GHz (bf16).  Block kinds spill 209 to 225 registers a lane, none of them in the loop:
+// tiles of 176 rows and more reload them in the one to three steps after it.  Without its loads the loop takes 0.60 ms of the 0.74, without its products
 // 0.56; without the barrier 3 % less, without the waits for loads no less.
 //
 // Also tried at that size: both operands in two stages with one barrier a step (0.99 ms against
@@ -162,10 +163,12 @@ __device__ __forceinline__ void code_tile(const MatmulShape& s, const MatmulArgs
 // of step k + 3.  Loads past the end of a row return 0 without a memory access, so every step
 // issues the same number.
 //
-// CODED (block): the results leave as codes.  What the fp8 instructions cut (1.5e-5 of a sum) would then
-// show as another code, a step of 6 to 25 %, in a few of 10 000 results, so tiles of up to 64 rows, which the
-// matrix units do not bound, form whole products (333 rows on 12 experts x 1136 x 1424, SwiGLU: 14.5 us
-// instead of 11.0).
+// CODED (block): the results leave as codes.  What the fp8 instructions cut (1.5e-5 of a sum) then
+// shows as another code, a step of 6 to 25 %, in 8 to 16 of 10 000 results, so tiles of up to 64 rows, which
+// the matrix units do not bound, form whole products (333 rows on 12 experts x 1136 x 1424, SwiGLU: 14.5 us
+// instead of 11.0).  Taller tiles do not: 16384 rows on 32 experts x 7168 x 4096, SwiGLU, would take 955 us
+// instead of 566, for values that are off by 0.00008 of their norm instead of 0.0012 where the codes
+// themselves are off by 0.023 (E4M3).  So a row's codes depend on its tile's height, as the header says.
 template <int TYPE, int WAVES, int MT, bool SWIGLU, bool CODED = false>
 __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulArgs& a,
                                              const Tile& tile, TileLds<TYPE, WAVES>& shared)
@@ -220,8 +223,8 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
     }
     // MX: every fourth step a wave brings 16 bytes of scales of 64 rows: waves 0-2 rows of x,
     // waves 3-6 weight rows (wave 7 the same as wave 6).  Rows are ns bytes, ns a multiple of 4.
-    // Block: waves 3-7 the same two rows of weight blocks, of columns n0 and n0 + 128 or of gate
-    // and up.
+    // Block: the first waves rows of x (0-3 of 224 rows, 0 of a thin tile's 64), all others the same two
+    // rows of weight blocks, of columns n0 and n0 + 128 or of gate and up.
     constexpr bool kLdsScales = M::kMx || M::kBlk;
     const bool sx = wave * 64 < kRows;
     const int sblk = sx ? wave : M::kBlk ? 0 : (wave < 6 ? wave : 6) - kScaleRows / 64;

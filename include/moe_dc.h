@@ -449,8 +449,11 @@ moe_status moe_grouped_matmul(const moe_dc_config* cfg, const moe_matmul* mm, co
  *   codes          bytes [cap][M]
  *   out_scales     fp32 [cap][Ceil(M, 128)]
  * Rows at or past recv_offsets[W] are not written.  Numerics and errors as for
- * moe_grouped_matmul, but where an expert's rows fill no tile of more than 64 nothing is dropped of the
- * products, since what is dropped shows as another code now and then. */
+ * moe_grouped_matmul, but tiles of up to 64 rows drop nothing of the products: those of an expert with up
+ * to 64 rows, and without SwiGLU of every expert where the product is small.  In taller ones what is dropped
+ * shows as another code, one step away, in about one of 1000 (7168 x 4096, 512 rows an expert: 8 to 16 of
+ * 10 000, values off by 0.0012 of their norm).  The codes of a row may therefore depend on how many rows
+ * its expert has; the same inputs give the same bytes. */
 moe_status moe_grouped_matmul_quantize(const moe_dc_config* cfg, const moe_matmul* mm,
                                        int32_t out_dtype, const void* x, const float* x_scales,
                                        const void* weight, const float* weight_scales,
