@@ -14,11 +14,11 @@
 //         an expert's sums are added to its tokens' in LDS, times the pick's weight, and the waves' in
 //         the end, in an order that depends on the ids only.
 //
-// h is rounded to the token type as separate calls round it, so that both ways agree and the down kernel
-// takes h as it lies as a matrix operand.  It and y's own rounding make the result sqrt(2) further from
-// 64 bits than y's alone (bf16 0.0024 against 0.0017, fp16 0.00029 against 0.00020).  A weight multiplies
-// fp32 sums: in fp16 a small one would push h among the subnormals (w 0.01, h 1e-4: an error of 0.017),
-// a large one past 65504.
+// h is kept as two numbers of the token type, its rounding and what that leaves (16 bits in bf16, 22 in
+// fp16), each a matrix operand as it lies: the down kernel multiplies twice, where HBM leaves it the
+// time.  With one the result would be sqrt(2) further from 64 bits (bf16 0.0024 against 0.0017, fp16
+// 0.00029 against 0.00020).  A weight multiplies fp32 sums: in fp16 a small one would push h among
+// the subnormals, a large one past 65504.
 //
 // Bound by HBM: 32 tokens on 256 experts x 7168 x 2048 E4M3 (7.2 GB) take 1.17 to 1.21 ms, 6.1 TB/s, a
 // read's rate; 1 token on 8 experts bf16 (0.70 GB) 122 us, 5.8 TB/s.  By latency: 5 tokens on 8 experts x
@@ -48,12 +48,13 @@ constexpr int kWideDown = 32 * 192;             // H from which it takes 32
 constexpr int kMaxIds = 1024;                   // experts
 constexpr int kMaxChunks = 64;                  // of an up row with scales (H <= 8192)
 
-// A chunk is 128 bytes of a weight row: 64 tokens or 128 E4M3 codes, which meet 128 or 256 bytes of a
-// row of x (or h), one or two halves of 128.  NT tiles of 16 weight rows and RP rows of x make a
-// stage; a load fills 1 KB of it.
-template <bool F16, bool BLOCK, int NT, int RP>
+// A chunk is 128 bytes of a weight row: 64 tokens or 128 E4M3 codes, which meet one or two runs of 64
+// elements of a row of x (or h).  A run is 128 bytes, or PARTS times 128 one after another (the two
+// parts of h).  NT tiles of 16 weight rows and RP rows of x make a stage; a load fills 1 KB of it.
+template <bool F16, bool BLOCK, int NT, int RP, int PARTS>
 struct Stage {
-    static constexpr int kHalves = BLOCK ? 2 : 1;
+    static constexpr int kRuns = BLOCK ? 2 : 1;
+    static constexpr int kHalves = kRuns * PARTS;            // 128 bytes each
     static constexpr int kTiles = (RP + 15) / 16;            // of rows of x
     static constexpr int kW = NT * 2048;
     static constexpr int kX = RP * 128 * kHalves < 1024 ? 1024 : RP * 128 * kHalves;
@@ -82,7 +83,7 @@ struct Stage {
     // and of row l % 16 of x those that meet them.  Piece p of row r lies at place p ^ (r & 7).
     struct Regs {
         v4i_t w[NT][2];
-        v4i_t x[kTiles][2 * kHalves];
+        v4i_t x[kTiles][PARTS][2 * kRuns];
     };
     static __device__ __forceinline__ void read(const char* st, Regs& r)
     {
@@ -98,30 +99,33 @@ struct Stage {
             const int row = m * 16 + (RP < 16 ? l16 % RP : l16);
             const char* xs = st + kW + row * 128;
 #pragma unroll
-            for (int i = 0; i < 2 * kHalves; ++i) {
-                const int half = BLOCK ? i >> 1 : 0, piece = BLOCK ? 2 * g + (i & 1) : i * 4 + g;
-                r.x[m][i] = *reinterpret_cast<const v4i_t*>(xs + half * RP * 128 + ((piece ^ (row & 7)) << 4));
-            }
+            for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                for (int i = 0; i < 2 * kRuns; ++i) {
+                    const int half = (BLOCK ? i >> 1 : 0) * PARTS + p, piece = BLOCK ? 2 * g + (i & 1) : i * 4 + g;
+                    r.x[m][p][i] = *reinterpret_cast<const v4i_t*>(xs + half * RP * 128 + ((piece ^ (row & 7)) << 4));
+                }
         }
     }
     // acc + a weight tile times a tile of rows
-    static __device__ __forceinline__ v4f_t mma(const v4i_t (&w)[2], const v4i_t (&x)[2 * kHalves], v4f_t acc)
+    static __device__ __forceinline__ v4f_t mma(const v4i_t (&w)[2], const v4i_t (&x)[PARTS][2 * kRuns], v4f_t acc)
     {
         if constexpr (BLOCK) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const v4i_t lo = {pair<false>(w[p].x), pair<true>(w[p].x), pair<false>(w[p].y), pair<true>(w[p].y)};
                 const v4i_t hi = {pair<false>(w[p].z), pair<true>(w[p].z), pair<false>(w[p].w), pair<true>(w[p].w)};
-                acc = mma16(lo, x[2 * p], acc);
-                acc = mma16(hi, x[2 * p + 1], acc);
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) acc = mma16(hi, x[q][2 * p + 1], mma16(lo, x[q][2 * p], acc));
             }
-            return acc;
         } else {
-            return mma16(w[1], x[1], mma16(w[0], x[0], acc));
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) acc = mma16(w[1], x[q][1], mma16(w[0], x[q][0], acc));
         }
+        return acc;
     }
 
-    // Byte offsets of the lane's pieces within a chunk, for the loads: weights (of a tile's first 8
+    // Byte offsets of the lane's pieces within 128 bytes, for the loads: weights (of a tile's first 8
     // rows) and, of load i, the row of x, its half and piece.
     static __device__ __forceinline__ uint32_t wpiece()
     {
@@ -133,10 +137,14 @@ struct Stage {
         const int at = (i * kWave + (int)(threadIdx.x & (kWave - 1))) / 8;
         return at / RP < kHalves ? at % RP : RP;             // RP: none
     }
+    static __device__ __forceinline__ uint32_t xhalf(int i)
+    {
+        return (uint32_t)(i * kWave + (int)(threadIdx.x & (kWave - 1))) / 8 / RP;
+    }
     static __device__ __forceinline__ uint32_t xpiece(int i)
     {
         const int lane = threadIdx.x & (kWave - 1), at = (i * kWave + lane) / 8;
-        return (uint32_t)(at / RP * 128 + (((lane & 7) ^ (at % RP & 7)) << 4));
+        return (uint32_t)((lane & 7) ^ (at % RP & 7)) * 16;
     }
     // Loads chunk c into a stage.  wr: NT tiles' resources; row_bytes of a weight row; xoff: offset of
     // the row of x (kRsrcPastEnd: none) for load i.
@@ -153,9 +161,11 @@ struct Stage {
         }
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) {
-            const uint32_t q = (uint32_t)c * (128 * kHalves) + xpiece(i);
+            // the piece's place among the row's elements, in bytes of tokens, and where it lies
+            const uint32_t e = (uint32_t)c * (128 * kRuns) + xhalf(i) / PARTS * 128 + xpiece(i);
+            const uint32_t q = (uint32_t)c * (128 * kHalves) + xhalf(i) * 128 + xpiece(i);
             load_lds16(xr, st + kW + i * 1024,
-                       xoff[i] != kRsrcPastEnd && q < row_bytes * kHalves ? xoff[i] + q : kRsrcPastEnd);
+                       xoff[i] != kRsrcPastEnd && e < row_bytes * kRuns ? xoff[i] + q : kRsrcPastEnd);
         }
     }
 };
@@ -274,11 +284,31 @@ __device__ __forceinline__ float sum_weights(const LayerShape& s, const Slot& sl
     return total;
 }
 
+// What a rounded value leaves, 0 where it is infinite or NaN.
+template <bool F16>
+__device__ __forceinline__ float rest(float v, uint32_t rounded)
+{
+    const float r = tok_lo<F16>(rounded & 0xFFFF);
+    return __builtin_fabsf(r) < INFINITY ? v - r : 0.0f;
+}
+
+// Four elements of a row of h from element n on, both parts.
+template <bool F16>
+__device__ __forceinline__ void store_h(char* row, int n, const float (&v)[4])
+{
+    char* o = row + n / 64 * 256 + n % 64 * 2;
+    const uint2 hi = make_uint2(pack_out2(v[0], v[1], F16), pack_out2(v[2], v[3], F16));
+    *reinterpret_cast<uint2*>(o) = hi;
+    *reinterpret_cast<uint2*>(o + 128) =
+        make_uint2(pack_out2(rest<F16>(v[0], hi.x), rest<F16>(v[1], hi.x >> 16), F16),
+                   pack_out2(rest<F16>(v[2], hi.y), rest<F16>(v[3], hi.y >> 16), F16));
+}
+
 // RP: rows of an expert that share a sweep over its weights.
 template <bool F16, bool BLOCK, int RP, int WAVES>
 __global__ __launch_bounds__(WAVES * kWave) void up_kernel(LayerShape s, LayerArgs a)
 {
-    typedef Stage<F16, BLOCK, 2, RP> S;
+    typedef Stage<F16, BLOCK, 2, RP, 1> S;
     constexpr int kRows = S::kTiles;
     __shared__ __align__(1024) char ring[WAVES][kRing][S::kBytes];
     __shared__ UpNotes all_notes[WAVES];
@@ -380,9 +410,8 @@ __global__ __launch_bounds__(WAVES * kWave) void up_kernel(LayerShape s, LayerAr
             const int row = r0 + m * 16 + l16;
             if (m * 16 + l16 >= RP || row >= slot.rows) continue;
             silu_mul4(r[0], r[1], r[0]);
-            uint16_t* o = static_cast<uint16_t*>(a.h) + (size_t)(slot.first + row) * s.F + n0 + g * 4;
             if (g * 4 < left)                   // F is a multiple of 8
-                *reinterpret_cast<uint2*>(o) = make_uint2(pack_out2(r[0][0], r[0][1], F16), pack_out2(r[0][2], r[0][3], F16));
+                store_h<F16>(static_cast<char*>(a.h) + (size_t)(slot.first + row) * layer_h_row(s.F), n0 + g * 4, r[0]);
         }
         if (r0 + RP < slot.rows) __syncthreads();            // before the rings are filled again
     }
@@ -407,7 +436,7 @@ __host__ __device__ inline DownLds down_lds(const LayerShape& s, int waves, int 
 template <bool F16, bool BLOCK, int NT, int RP, int WAVES>
 __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, LayerArgs a)
 {
-    typedef Stage<F16, BLOCK, NT, RP> S;
+    typedef Stage<F16, BLOCK, NT, RP, 2> S;
     constexpr int kCols = NT * 16;
     constexpr int kThreads = WAVES * kWave;
     extern __shared__ __align__(1024) char lds[];
@@ -451,7 +480,7 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
     const int count = __builtin_amdgcn_readfirstlane(count_lds);
     const char* h = static_cast<const char*>(a.h);
     const uint32_t row_bytes = (uint32_t)s.F * (BLOCK ? 1 : 2);
-    const uint32_t h_bytes = (uint32_t)s.F * 2;
+    const uint32_t h_bytes = (uint32_t)layer_h_row(s.F);
     const int chunks = (int)((row_bytes + 127) / 128);
     const int n0 = blockIdx.x * kCols;
     const int blocks = (s.H + 127) / 128;
@@ -603,7 +632,7 @@ __global__ __launch_bounds__(WAVES * kWave) void down_kernel(LayerShape s, Layer
 template <bool F16, bool BLOCK, int NT, int RP, int WAVES>
 hipError_t launch_down(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
 {
-    const DownLds l = down_lds(s, WAVES, kRing * Stage<F16, BLOCK, NT, RP>::kBytes, NT * 16, RP);
+    const DownLds l = down_lds(s, WAVES, kRing * Stage<F16, BLOCK, NT, RP, 2>::kBytes, NT * 16, RP);
     const size_t bytes = l.ring + l.sums + l.slots + l.rows + l.scales;
     down_kernel<F16, BLOCK, NT, RP, WAVES><<<(unsigned)((s.H + NT * 16 - 1) / (NT * 16)), WAVES * kWave, bytes,
                                              stream>>>(s, a);
@@ -624,9 +653,11 @@ hipError_t launch_rows(const LayerShape& s, const LayerArgs& a, hipStream_t stre
     const hipError_t e = (int64_t)s.slots * s.F <= kFewUp ? launch_up<F16, BLOCK, RP, 4>(s, a, stream)
                                                           : launch_up<F16, BLOCK, RP, 2>(s, a, stream);
     if (e != hipSuccess) return e;
-    if (s.H >= kWideDown) return launch_down<F16, BLOCK, 2, RP, 4>(s, a, stream);
-    // (eight rings of 32 rows with codes do not fit the 160 KB of LDS)
-    return launch_down<F16, BLOCK, 1, RP, BLOCK && RP == 32 ? 4 : 8>(s, a, stream);
+    // (what the 160 KB of LDS hold beside up to 60 KB of sums, slots and rows)
+    constexpr int kRows = BLOCK && RP == 32 ? 16 : RP;
+    constexpr bool kEight = 8 * kRing * Stage<F16, BLOCK, 1, kRows, 2>::kBytes <= 96 << 10;
+    if (s.H >= kWideDown) return launch_down<F16, BLOCK, 2, kRows, 4>(s, a, stream);
+    return launch_down<F16, BLOCK, 1, kRows, kEight ? 8 : 4>(s, a, stream);
 }
 
 template <bool F16, bool BLOCK>

@@ -22,8 +22,9 @@ struct LayerShape {
     int32_t slots;           // experts that can have tokens: min(E, T * K)
 };
 
-// Workspace: one Slot per expert that can have tokens; one Row per pick, of each row of h; h in the
-// token type, [T * K][F].  Every part is written before it is read in the same call.
+// Workspace: one Slot per expert that can have tokens; one Row per pick, of each row of h; h, [T * K]
+// rows of layer_h_row bytes: of every 64 elements the 64 as tokens, then the 64 rests.  Every part
+// that is read is written before in the same call.
 struct Slot {
     int32_t expert;          // -1: no more experts
     int32_t first;           // its first row of h
@@ -52,6 +53,7 @@ struct LayerArgs {
     void* h;
 };
 
+constexpr size_t layer_h_row(int32_t F) { return (size_t)((F + 63) / 64) * 256; }
 inline size_t layer_rows_offset(const LayerShape& s) { return round256((size_t)s.slots * sizeof(Slot)); }
 inline size_t layer_h_offset(const LayerShape& s)
 {
@@ -59,7 +61,7 @@ inline size_t layer_h_offset(const LayerShape& s)
 }
 inline size_t layer_workspace_bytes(const LayerShape& s)
 {
-    return layer_h_offset(s) + round256((size_t)s.T * s.K * s.F * 2);
+    return layer_h_offset(s) + (size_t)s.T * s.K * layer_h_row(s.F);
 }
 
 hipError_t launch_experts_layer(const LayerShape& s, const LayerArgs& a, hipStream_t stream);

@@ -563,7 +563,7 @@ typedef struct {
                                    with one fp32 per block of 128 x 128 elements             */
 } moe_experts;
 
-/* Workspace bytes moe_experts_layer needs (the picks' rows of F tokens,
+/* Workspace bytes moe_experts_layer needs (two rows of F tokens a pick, F up to a multiple of 64,
  * and up to 24 KiB).  0 for an invalid config or description.  Scratch, as for dispatch; one workspace must
  * not be used by two calls that may run concurrently. */
 size_t moe_dc_experts_layer_workspace_bytes(const moe_dc_config* cfg, const moe_experts* experts);
@@ -589,9 +589,9 @@ size_t moe_dc_experts_layer_workspace_bytes(const moe_dc_config* cfg, const moe_
  * cfg's quantization attributes are not used.
  * Numerics: products of token values and codes are exact (the tokens are not quantized); sums are
  * fp32 in an order that depends on the sizes and ids only; _BLOCK sums the products of a block,
- * multiplies by its scale and adds; SwiGLU as for moe_grouped_matmul.  h is rounded to the token
- * type between the two products (fp16: to infinity past 65504), as separate calls round it, and y
- * once at the end; w multiplies sums in fp32 (it is the sum of the weights where a token picked an
+ * multiplies by its scale and adds; SwiGLU as for moe_grouped_matmul.  h is kept as two
+ * numbers of the token type between the two products, its rounding and the rest: 16 bits of bf16, 22 of
+ * fp16 (down to 2^-25; infinite past 65504).  y is rounded once at the end; w multiplies sums in fp32 (it is the sum of the weights where a token picked an
  * expert more than once).  An infinity or NaN in a weight
  * reaches only the tokens that picked its expert.
  * Errors: MOE_ERR_UNSUPPORTED for more than 64 tokens; y or the workspace overlapping an input is
