@@ -35,16 +35,19 @@ namespace {
 
 constexpr int kRing = 2;                        // stages of a wave
 // Many small workgroups hide each other's start and end, so the up kernel's have two waves; with few
-// columns in all, four waves share the chunks of a workgroup's.  Two waves with two stages against
-// four with two and four with three, us: 1 token on 8 experts of 7168 x 2048 bf16 127, 131, 133; 32
-// tokens on 256 experts E4M3 1214, 1224, 1276, on 64 experts 471, 545, 621; 5 tokens on 8 experts of
-// 1024 x 520 fp16 with two and four waves 13.8 and 12.7.
+// columns in all, four waves share the chunks of a workgroup's.  Two waves against four, us: 1 token on 8
+// experts of 7168 x 2048 bf16 122 and 127; 32 tokens on 256 experts E4M3 1239 and 1242, on 64 experts 497
+// and 508; 64 tokens on 8 experts of 4096 x 4096 E4M3 121 and 149; 5 tokens on 8 experts of 1024 x 520
+// fp16 12.8 and 12.7 (13.8 and 12.7 before the weights moved to the down kernel).  A third stage with
+// four waves: 2, 4 and 14 % more in the first three.
 constexpr int64_t kFewUp = 16 * 512;            // columns (of all experts) up to which it has four
 // Columns of y and waves of a workgroup: many columns share the rows of h, but few workgroups leave
-// CUs idle.  32 columns and four waves against 16 and eight, us: H = 7168, 32 tokens on 64 experts
-// E4M3 471 and 501, 64 tokens 492 and 529; H = 2048, 16 tokens on 32 experts x 1408 bf16 132 and 108,
-// H = 4096, 8 tokens on 8 experts x 1024 48.9 and 45.2.
-constexpr int kWideDown = 32 * 192;             // H from which it takes 32
+// CUs idle.  32 columns and four waves against 16 and eight (four where the rings are large), us: H = 7168,
+// 32 tokens on 64 experts x 2048 E4M3 497 and 617, 64 tokens 546 and 642; H = 5120, 64 tokens on 64 x 1536
+// E4M3 339 and 409, 8 tokens 119 and 122; H = 4608, 64 tokens on 64 x 1536 bf16 540 and 589, 8 tokens 200
+// and 214; H = 4096, 64 tokens on 64 x 1536 E4M3 292 and 270, 32 tokens on 32 x 1024 E4M3 101 and 87, 8
+// tokens on 8 x 1024 bf16 48.8 and 43.1; H = 2048, 16 tokens on 32 x 1408 bf16 130 and 103.
+constexpr int kWideDown = 32 * 144;             // H from which it takes 32
 constexpr int kMaxIds = 1024;                   // experts
 constexpr int kMaxChunks = 64;                  // of an up row with scales (H <= 8192)
 
@@ -653,11 +656,15 @@ hipError_t launch_rows(const LayerShape& s, const LayerArgs& a, hipStream_t stre
     const hipError_t e = (int64_t)s.slots * s.F <= kFewUp ? launch_up<F16, BLOCK, RP, 4>(s, a, stream)
                                                           : launch_up<F16, BLOCK, RP, 2>(s, a, stream);
     if (e != hipSuccess) return e;
-    // (what the 160 KB of LDS hold beside up to 60 KB of sums, slots and rows)
-    constexpr int kRows = BLOCK && RP == 32 ? 16 : RP;
-    constexpr bool kEight = 8 * kRing * Stage<F16, BLOCK, 1, kRows, 2>::kBytes <= 96 << 10;
+    // The rings fit the 160 KB of LDS beside up to 62 KB of sums, slots and rows: with codes, whose chunks
+    // meet 512 bytes of a row of h, fewer rows share a sweep.  16 columns and codes, eight rows with eight
+    // waves against 16 with four, us: 2048 x 1024, 16 tokens on 16 experts 28.3 and 35.3; 4096 x 1024, 32
+    // tokens on 32 experts 87.5 and 94.6, 64 on 64 186 and 186; but with more than 8 rows an expert in the mean,
+    // 4096 x 4096, 64 tokens on 8 experts 129 and 121.
+    constexpr int kRows = BLOCK && RP == 32 ? 16 : RP, kNarrowRows = BLOCK && RP == 16 ? 8 : kRows;
+    constexpr bool kEight = 8 * kRing * Stage<F16, BLOCK, 1, kNarrowRows, 2>::kBytes <= 96 << 10;
     if (s.H >= kWideDown) return launch_down<F16, BLOCK, 2, kRows, 4>(s, a, stream);
-    return launch_down<F16, BLOCK, 1, kRows, kEight ? 8 : 4>(s, a, stream);
+    return launch_down<F16, BLOCK, 1, kNarrowRows, kEight ? 8 : 4>(s, a, stream);
 }
 
 template <bool F16, bool BLOCK>
@@ -665,8 +672,8 @@ hipError_t launch(const LayerShape& s, const LayerArgs& a, hipStream_t stream)
 {
     // An expert's rows beyond RP read its weights again, from the caches.  TB/s of weights with uniform
     // experts, with one that every token picks and with weights of 1 / rank: 64 tokens on 256 experts x 7168 x
-    // 2048 E4M3 (7, 64, 50 rows at most, four a sweep) 5.96, 5.86, 4.91, 32 tokens (5, 32, 24) 6.02, 5.90,
-    // 5.29; 64 tokens on 64 experts bf16 (18, 64, 58, sixteen a sweep) 5.69, 5.84, 5.14.
+    // 2048 E4M3 (7, 64, 50 rows at most, four a sweep) 5.88, 5.75, 4.79, 32 tokens (5, 32, 24) 5.96, 5.83,
+    // 5.18; 64 tokens on 64 experts bf16 (18, 64, 58, sixteen a sweep) 5.61, 5.74, 5.04.
     constexpr int kFew = BLOCK ? 4 : 8;         // rows that one load brings a chunk of
     if (s.T <= kFew || s.T * s.K <= 2 * s.E) return launch_rows<F16, BLOCK, kFew>(s, a, stream);
     if (s.T <= 16 || s.T * s.K <= 8 * s.E) return launch_rows<F16, BLOCK, 16>(s, a, stream);

@@ -20,7 +20,7 @@ DEV = "cuda"
 
 # every number of rows that shares a sweep in the down product, 16 and 32 columns, runs that end early
 @pytest.mark.parametrize("W,BS,E,K,H,F", [
-    (2, 1, 16, 4, 1024, 512), (2, 2, 8, 2, 7168, 208), (2, 8, 8, 2, 2048, 1040), (2, 32, 64, 4, 1040, 272),
+    (2, 1, 16, 4, 1024, 512), (2, 2, 8, 2, 7168, 208), (2, 8, 8, 2, 2048, 1040), (2, 32, 64, 4, 1040, 272), (2, 32, 64, 4, 4608, 80),
     (2, 32, 64, 4, 6160, 144), (2, 32, 4, 4, 1536, 256), (2, 32, 4, 3, 6144, 336)])
 @pytest.mark.parametrize("block,f16", [(False, False), (False, True), (True, False), (True, True)])
 def test_one_rounding(W, BS, E, K, H, F, block, f16):
