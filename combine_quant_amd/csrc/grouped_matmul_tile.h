@@ -8,8 +8,7 @@
 // 737 us in bf16 (1310 Tflop/s), 775 in fp16, 392 in E4M3 (2450), 404 in int8, 461 in MX E4M3, 470
 // to 490 in block-scaled E4M3 (whose scaled additions take as many vector cycles as the products
 // matrix cycles; three of four left out give 8 %), with the matrix units busy 72 % of a workgroup's
-// time at 1.76 GHz (bf16).  Block kinds spill 209 to 225 registers a lane, none of them in the loop:
-// tiles of 176 rows and more reload them in the one to three steps after it.  Without its loads the loop takes 0.60 ms of the 0.74, without its products
+// time at 1.76 GHz (bf16).  Without its loads the loop takes 0.60 ms of the 0.74, without its products
 // 0.56; without the barrier 3 % less, without the waits for loads no less.
 //
 // Also tried at that size: both operands in two stages with one barrier a step (0.99 ms against
@@ -264,7 +263,7 @@ __device__ __forceinline__ void tile_product(const MatmulShape& s, const MatmulA
         const char* to = lds.scales[step >> 2 & 1];
         const int k = step & 3;
         // (the address as a pointer moved step by step: summed as a number first, and chosen between the two
-        // cases, it cost MX tiles 10 registers, spills and 2.5 %)
+        // cases, it cost MX tiles 10 registers, spills and 2.5 %, and block tiles 209 to 225 spilled registers)
         const auto read = [&](const char* at) {
             return M::kBlk ? *reinterpret_cast<const int*>(at) : (int)*reinterpret_cast<const uint8_t*>(at + g);
         };
