@@ -16,13 +16,13 @@
 //
 // h is kept as two numbers of the token type, its rounding and what that leaves (16 bits in bf16, 22 in
 // fp16), each a matrix operand as it lies: the down kernel multiplies twice, where HBM leaves it the
-// time.  With one the result would be sqrt(2) further from 64 bits (bf16 0.0024 against 0.0017, fp16
-// 0.00029 against 0.00020).  A weight multiplies fp32 sums: in fp16 a small one would push h among
-// the subnormals, a large one past 65504.
+// time (an infinite weight meets both parts, and gives NaN).  With one the result would be sqrt(2) further
+// from 64 bits (bf16 0.0024 against 0.0017, fp16 0.00029 against 0.00020).  A weight of a pick multiplies
+// fp32 sums: in fp16 a small one would push h among the subnormals, a large one past 65504.
 //
-// Bound by HBM: 32 tokens on 256 experts x 7168 x 2048 E4M3 (7.2 GB) take 1.17 to 1.21 ms, 6.1 TB/s, a
+// Bound by HBM: 32 tokens on 256 experts x 7168 x 2048 E4M3 (7.2 GB) take 1.19 to 1.24 ms, 6.0 TB/s, a
 // read's rate; 1 token on 8 experts bf16 (0.70 GB) 122 us, 5.8 TB/s.  By latency: 5 tokens on 8 experts x
-// 1024 x 520 fp16 11.9 us, of which the up kernel's ids and list of tokens take 2.0, the down kernel's list of
+// 1024 x 520 fp16 12.0 us, of which the up kernel's ids and list of tokens take 2.0, the down kernel's list of
 // experts 1.0, the first bytes 1.2 each and the gap between the kernels 1.3.  (Weights straight to matrix
 // registers, rows of x too: 1.79 ms, 139 and 15.4 us.)
 #include "dc_device.h"

@@ -221,7 +221,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormShape s, NormArgs a)
 }
 
 // Any H and any alignment: y of the token in LDS, element by element, and a thread per group of codes, which
-// walks it alone.  Rows that dispatch's other kernels take element by element too; not made fast.  8192
+// walks it alone: what no vector takes, as in dispatch's element-wise kernel, and not made fast.  8192
 // tokens x 7161, modes 0, 2, 3 and 4: 334, 356, 649 and 519 us (7168: 68, 78, 78 and 79 on inputs that the
 // last cache holds in part); 2 tokens x 1025, mode 3: 29 us.
 constexpr int kAnyThreads = 256;

@@ -593,7 +593,7 @@ size_t moe_dc_experts_layer_workspace_bytes(const moe_dc_config* cfg, const moe_
  * numbers of the token type between the two products, its rounding and the rest: 16 bits of bf16, 22 of
  * fp16 (down to 2^-25; infinite past 65504).  y is rounded once at the end; w multiplies sums in fp32
  * (it is the sum of the weights where a token picked an expert more than once).  An infinity or NaN
- * in a weight reaches only the tokens that picked its expert.
+ * in a weight reaches only the tokens that picked its expert, an infinity in `down` as a NaN.
  * Errors: MOE_ERR_UNSUPPORTED for more than 64 tokens; y or the workspace overlapping an input is
  * MOE_ERR_INVALID_ARG; otherwise as for moe_dispatch.  Picks with ids out of range count as
  * inactive. */
